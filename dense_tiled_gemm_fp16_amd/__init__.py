@@ -12,6 +12,9 @@ device memory and the current stream.
     workspace_bytes(M, N, K, ...)  -> bytes of split-K workspace needed
     gemm_noalloc(a, b, out)        -> C = a @ b (float16) with no device allocation by the
                                       library (its workspace in a fixed per-GPU array)
+    quantize_mx4(x), dequantize_mx4(q), gemm_mx4(a, q)
+                                   -> microscaled 4-bit floating point: tensors and
+                                      products with 4-bit weights (mx4.py)
 """
 import ctypes
 
@@ -19,10 +22,11 @@ import torch
 
 from ._lib import (GEMM_OK, LIB_PATH, PATHS, STATUS, VARIANTS, Opts, PlanInfo, lib, make_opts,
                    status_string)
+from .mx4 import MX4, dequantize_mx4, gemm_mx4, gemm_mx4_workspace_bytes, quantize_mx4
 
 __all__ = ["gemm", "gemm_raw", "gemm_noalloc", "gemm_grouped", "pack_b", "gemm_packed", "PackedB", "plan",
            "workspace_bytes", "GemmError", "LIB_PATH",
-           "VARIANTS"]
+           "VARIANTS", "MX4", "quantize_mx4", "dequantize_mx4", "gemm_mx4", "gemm_mx4_workspace_bytes"]
 
 
 class GemmError(RuntimeError):

@@ -1,4 +1,5 @@
-"""ctypes view of libgemmf16.so (the C-ABI in include/gemm_f16.h).
+"""ctypes view of libgemmf16.so (the C-ABI in include/gemm_f16.h and
+the headers beside it).
 
 Argument marshalling only: every step of the computation runs in the HIP
 library.  There is no fallback: if the library cannot be loaded, importing
@@ -26,6 +27,10 @@ EXPORTS = ["gemm_f16", "gemm_f16_ex", "gemm_f16_plan", "gemm_f16_plan_cus", "gem
            "gemm_f16_packed_b_bytes", "gemm_f16_pack_b", "gemm_f16_packed",
            "gemm_f16_grouped", "gemm_bf16_grouped", "gemm_f8_grouped", "gemm_f16_grouped_workspace_bytes",
            "gemm_f16_noalloc", "gemm_f16_status_string", "gemm_f16_version"]
+
+# Entry points of include/gemm_mx4.h.
+EXPORTS_MX4 = ["gemm_mx4_quantize", "gemm_mx4_dequantize", "gemm_mx4", "gemm_mx4_workspace_bytes",
+               "gemm_mx4_a16"]
 
 
 class Opts(ctypes.Structure):
@@ -99,6 +104,16 @@ def _load():
     lib.gemm_f8_grouped.restype = ctypes.c_int
     lib.gemm_f16_grouped_workspace_bytes.argtypes = [i32]
     lib.gemm_f16_grouped_workspace_bytes.restype = sz
+    lib.gemm_mx4_quantize.argtypes = [vp, i32, i64, i64, i64, i64, i64, i64, vp, vp, vp]
+    lib.gemm_mx4_quantize.restype = ctypes.c_int
+    lib.gemm_mx4_dequantize.argtypes = [vp, i64, vp, i64, i64, i64, vp, i32, i64, vp]
+    lib.gemm_mx4_dequantize.restype = ctypes.c_int
+    lib.gemm_mx4.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i32, i64, i64, i64, i64, vp, vp, sz]
+    lib.gemm_mx4.restype = ctypes.c_int
+    lib.gemm_mx4_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.gemm_mx4_workspace_bytes.restype = sz
+    lib.gemm_mx4_a16.argtypes = [vp, i32, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp]
+    lib.gemm_mx4_a16.restype = ctypes.c_int
     lib.gemm_f16_status_string.argtypes = [ctypes.c_int]
     lib.gemm_f16_status_string.restype = ctypes.c_char_p
     lib.gemm_f16_version.argtypes = []

@@ -1,0 +1,292 @@
+// Quantisation to MX FP4 and back (gfx950).
+//
+// Both are one pass over memory: a few operations per element against 2 to 4
+// bytes read and 17/32 written (or the reverse), so the memory rate bounds
+// them and the kernels only have to keep wide loads in flight.
+//
+//   rows     k is the contiguous axis.  A lane takes 8 consecutive elements
+//            (one 16-byte load of a 16-bit type), four neighbouring lanes a
+//            block; the block's largest magnitude goes round the four with
+//            two lane exchanges.  A wave has U such loads in flight.  Rows
+//            shorter than a wave's 512 elements share one (rpw rows a wave).
+//   columns  any other strides: a lane owns a row and walks the 32 elements of
+//            a block, so that with rows contiguous a wave's loads cover 64
+//            consecutive elements; no lane exchange is needed.
+//
+// The scale's exponent is read off the magnitude's own bits: floor(log2 m) is
+// the exponent field of a normal float, and a subnormal m (only from fp32 or
+// bfloat16) clamps to the least scale anyway.  Division by the scale is an
+// exact multiplication by 2^(127 - byte), after which the packed convert
+// rounds to nearest even and saturates at 6.
+#pragma once
+
+#include "mx4_common.hpp"
+
+namespace gemmf16 {
+
+enum MxFormat { MX_F16 = 0, MX_BF16 = 1, MX_F32 = 2 };
+
+struct QuantArgs {
+  const void* x;
+  int64_t s_g, s_r, s_k;   // element strides
+  int64_t G, R, K;
+  uint8_t* data;           // [G R, 16 Kb]
+  uint8_t* scales;         // [G R, Kb]
+  int64_t Kb;              // blocks per row
+  int64_t segs;            // rows: wave items per row
+  int32_t rpw;             // rows: rows per wave (1 when a row fills a wave)
+};
+
+template <int FMT>
+struct MxElem {
+  using type = uint16_t;
+};
+template <>
+struct MxElem<MX_F32> {
+  using type = uint32_t;
+};
+
+template <int FMT>
+__device__ __forceinline__ float mx_in(typename MxElem<FMT>::type v) {
+  if constexpr (FMT == MX_F32)
+    return __builtin_bit_cast(float, v);
+  else
+    return cvt_in<FMT == MX_F16 ? DT_F16 : DT_BF16>(v);
+}
+
+// 8 consecutive elements as they lie, n of them valid (the rest zero).
+template <int FMT>
+struct Oct {
+  static constexpr int ES = FMT == MX_F32 ? 4 : 2;
+  u32x4 v[ES / 2];
+
+  __device__ __forceinline__ void load(const void* base, int64_t k, int64_t n) {
+    const char* p = (const char*)base + k * ES;
+    if (n >= 8) {
+      v[0] = load16(p);
+      if constexpr (FMT == MX_F32) v[1] = load16(p + 16);
+      return;
+    }
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      typename MxElem<FMT>::type e = 0;
+      if (i < n) __builtin_memcpy(&e, p + i * ES, ES);
+      h[i] = e;
+    }
+    if constexpr (FMT == MX_F32) {
+      v[0] = u32x4{h[0], h[1], h[2], h[3]};
+      v[1] = u32x4{h[4], h[5], h[6], h[7]};
+    } else {
+      v[0] = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (FMT == MX_F32) {
+      const uint32_t e = v[i / 4][i % 4];   // a copy: bit_cast of a vector's element reads element 0
+      return __builtin_bit_cast(float, e);
+    } else
+      return mx_in<FMT>((uint16_t)(v[0][i / 2] >> (16 * (i & 1))));
+  }
+};
+
+// Scale byte of a block whose largest magnitude has these bits (the sign
+// cleared; an infinity or a NaN among the elements compares largest).
+__device__ __forceinline__ uint32_t scale_of(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 23;
+  return e == 255 ? 255u : (e < 2 ? 0u : e - 2);
+}
+// 2^(127 - byte): exact, normal for every byte but 254 and 255, which
+// scale_of does not give below an infinity.
+__device__ __forceinline__ float inverse_scale(uint32_t byte) {
+  return __builtin_bit_cast(float, (254u - byte) << 23);
+}
+
+// 8 floats over their scale -> 8 codes.
+__device__ __forceinline__ uint32_t to_codes(const float* f, uint32_t byte) {
+  if (byte == 255) return 0;
+  const float r = inverse_scale(byte);
+  uint32_t d = 0;
+  d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, f[0] * r, f[1] * r, 1.0f, 0);
+  d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, f[2] * r, f[3] * r, 1.0f, 1);
+  d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, f[4] * r, f[5] * r, 1.0f, 2);
+  d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, f[6] * r, f[7] * r, 1.0f, 3);
+  return d;
+}
+
+constexpr int kQuantU = 4;   // wave items of 64 lanes x 8 elements in flight
+
+// Rows with unit k stride.  Wave item w: row (or rpw rows) w / segs, octets
+// (w % segs) 64 U .. of it.
+template <int FMT>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t rows = a.G * a.R, octs = 4 * a.Kb;
+  int64_t row = w / a.segs, o0 = (w - row * a.segs) * (64 * kQuantU) + lane;
+  bool mine = true;
+  if (a.rpw > 1) {                     // several short rows in one wave
+    const int sub = lane / (int)octs;
+    mine = sub < a.rpw;
+    row = w * a.rpw + sub;
+    o0 = lane - sub * (int)octs;
+  }
+  if (row >= rows) mine = false;
+  const int64_t g = a.G == 1 ? 0 : row / a.R, r = row - g * a.R;
+  const char* base = (const char*)a.x + (g * a.s_g + r * a.s_r) * Oct<FMT>::ES;
+  const int nu = a.rpw > 1 ? 1 : kQuantU;
+  Oct<FMT> v[kQuantU];
+#pragma unroll
+  for (int u = 0; u < kQuantU; ++u) {
+    const int64_t o = o0 + 64 * u;
+    v[u].load(base, 8 * o, mine && u < nu && o < octs ? a.K - 8 * o : 0);
+  }
+#pragma unroll
+  for (int u = 0; u < kQuantU; ++u) {
+    const int64_t o = o0 + 64 * u;
+    float f[8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f[i] = v[u].get(i);
+      const uint32_t b = __builtin_bit_cast(uint32_t, f[i]) & 0x7FFFFFFFu;
+      m = b > m ? b : m;
+    }
+    // the block's four lanes are neighbours: octets count from a multiple of 4
+    uint32_t n = __shfl_xor(m, 1);
+    m = n > m ? n : m;
+    n = __shfl_xor(m, 2);
+    m = n > m ? n : m;
+    const uint32_t s = scale_of(m);
+    if (mine && u < nu && o < octs) {
+      *(uint32_t*)(a.data + (row * octs + o) * 4) = to_codes(f, s);
+      if ((o & 3) == 0) a.scales[row * a.Kb + (o >> 2)] = (uint8_t)s;
+    }
+  }
+}
+
+// Any strides: lane -> row, wave -> (64 rows, one block).
+template <int FMT>
+__global__ __launch_bounds__(256) void quantize_columns_kernel(QuantArgs a) {
+  using E = typename MxElem<FMT>::type;
+  const int lane = threadIdx.x & 63;
+  const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t strip = w / a.Kb, b = w - strip * a.Kb;
+  const int64_t row = strip * 64 + lane;
+  if (row >= a.G * a.R) return;
+  const int64_t g = a.G == 1 ? 0 : row / a.R, r = row - g * a.R;
+  const int64_t left = a.K - 32 * b;
+  const int n = left < 32 ? (int)left : 32;
+  const E* p = (const E*)a.x + g * a.s_g + r * a.s_r + 32 * b * a.s_k;
+  E e[32];
+  if (n == 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) e[i] = p[i * a.s_k];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) e[i] = i < n ? p[i * a.s_k] : (E)0;
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const uint32_t q = __builtin_bit_cast(uint32_t, mx_in<FMT>(e[i])) & 0x7FFFFFFFu;
+    m = q > m ? q : m;
+  }
+  const uint32_t s = scale_of(m);
+  u32x4 out;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = mx_in<FMT>(e[8 * j + i]);
+    out[j] = to_codes(f, s);
+  }
+  *(u32x4*)(a.data + (row * a.Kb + b) * kMxBytes) = out;
+  a.scales[row * a.Kb + b] = (uint8_t)s;
+}
+
+struct DequantArgs {
+  const uint8_t* data;
+  int64_t ldd;
+  const uint8_t* scales;
+  int64_t lds;
+  int64_t R, K;
+  void* y;
+  int64_t ldy;     // elements
+  int64_t segs;
+  int32_t rpw;
+};
+
+// As quantize_rows_kernel: a lane turns 8 codes (4 bytes) into 8 elements.
+template <int FMT>
+__global__ __launch_bounds__(256) void dequantize_kernel(DequantArgs a) {
+  constexpr int ES = FMT == MX_F32 ? 4 : 2;
+  const int lane = threadIdx.x & 63;
+  const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t octs = (a.K + 7) / 8;
+  int64_t row = w / a.segs, o0 = (w - row * a.segs) * (64 * kQuantU) + lane;
+  bool mine = true;
+  if (a.rpw > 1) {
+    const int sub = lane / (int)octs;
+    mine = sub < a.rpw;
+    row = w * a.rpw + sub;
+    o0 = lane - sub * (int)octs;
+  }
+  if (row >= a.R) mine = false;
+  const int nu = a.rpw > 1 ? 1 : kQuantU;
+  const uint8_t* d = a.data + row * a.ldd;
+  const uint8_t* sc = a.scales + row * a.lds;
+  char* y = (char*)a.y + row * a.ldy * ES;
+  uint32_t c[kQuantU], s[kQuantU];
+#pragma unroll
+  for (int u = 0; u < kQuantU; ++u) {
+    const int64_t o = o0 + 64 * u;
+    const bool ok = mine && u < nu && o < octs;
+    c[u] = 0;
+    if (ok) __builtin_memcpy(&c[u], d + 4 * o, 4);
+    s[u] = ok ? sc[o >> 2] : 127;
+  }
+#pragma unroll
+  for (int u = 0; u < kQuantU; ++u) {
+    const int64_t o = o0 + 64 * u;
+    if (!(mine && u < nu && o < octs)) continue;
+    const float f = scale_f32(s[u]);
+    const int64_t left = a.K - 8 * o;
+    char* q = y + 8 * o * ES;
+    if constexpr (FMT == MX_BF16) {
+      const u32x4 v = __builtin_bit_cast(u32x4, mx4_to_bf16(c[u], f));
+      if (left >= 8) {
+        store16(q, v);
+      } else {
+        for (int i = 0; i < left; ++i) ((uint16_t*)q)[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+      }
+    } else {
+      // through bfloat16 (exact) and float (exact) to the output's rounding
+      const bf16x8 b = mx4_to_bf16(c[u], f);
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = (float)b[i];
+      if constexpr (FMT == MX_F32) {
+        if (left >= 8) {
+          float4 lo = {e[0], e[1], e[2], e[3]}, hi = {e[4], e[5], e[6], e[7]};
+          __builtin_memcpy(q, &lo, 16);
+          __builtin_memcpy(q + 16, &hi, 16);
+        } else {
+          for (int i = 0; i < left; ++i) ((float*)q)[i] = e[i];
+        }
+      } else {
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          h[i] = (uint32_t)cvt_out<DT_F16>(e[2 * i]) | ((uint32_t)cvt_out<DT_F16>(e[2 * i + 1]) << 16);
+        if (left >= 8) {
+          store16(q, u32x4{h[0], h[1], h[2], h[3]});
+        } else {
+          for (int i = 0; i < left; ++i) ((uint16_t*)q)[i] = (uint16_t)(h[i / 2] >> (16 * (i & 1)));
+        }
+      }
+    }
+  }
+}
+
+}  // namespace gemmf16
