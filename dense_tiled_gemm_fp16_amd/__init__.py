@@ -15,6 +15,8 @@ device memory and the current stream.
     quantize_mx4(x), dequantize_mx4(q), gemm_mx4(a, q)
                                    -> microscaled 4-bit floating point: tensors and
                                       products with 4-bit weights (mx4.py)
+    gemm_moe(x, logits, w_gate_up, w_down, top_k)
+                                   -> a mixture-of-experts layer for a few tokens (moe.py)
 """
 import ctypes
 
@@ -22,11 +24,13 @@ import torch
 
 from ._lib import (GEMM_OK, LIB_PATH, PATHS, STATUS, VARIANTS, Opts, PlanInfo, lib, make_opts,
                    status_string)
+from .moe import gemm_moe, gemm_moe_workspace_bytes
 from .mx4 import MX4, dequantize_mx4, gemm_mx4, gemm_mx4_workspace_bytes, quantize_mx4
 
 __all__ = ["gemm", "gemm_raw", "gemm_noalloc", "gemm_grouped", "pack_b", "gemm_packed", "PackedB", "plan",
            "workspace_bytes", "GemmError", "LIB_PATH",
-           "VARIANTS", "MX4", "quantize_mx4", "dequantize_mx4", "gemm_mx4", "gemm_mx4_workspace_bytes"]
+           "VARIANTS", "MX4", "quantize_mx4", "dequantize_mx4", "gemm_mx4", "gemm_mx4_workspace_bytes",
+           "gemm_moe", "gemm_moe_workspace_bytes"]
 
 
 class GemmError(RuntimeError):

@@ -31,6 +31,8 @@ EXPORTS = ["gemm_f16", "gemm_f16_ex", "gemm_f16_plan", "gemm_f16_plan_cus", "gem
 # Entry points of include/gemm_mx4.h.
 EXPORTS_MX4 = ["gemm_mx4_quantize", "gemm_mx4_dequantize", "gemm_mx4", "gemm_mx4_workspace_bytes",
                "gemm_mx4_a16"]
+# Entry points of include/gemm_moe.h.
+EXPORTS_MOE = ["gemm_moe", "gemm_moe_workspace_bytes"]
 
 
 class Opts(ctypes.Structure):
@@ -45,6 +47,14 @@ class PlanInfo(ctypes.Structure):
 
     def as_dict(self):
         return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class MoeArgs(ctypes.Structure):   # gemm_moe_args
+    _fields_ = [("X", vp), ("ldx", i64), ("logits", vp), ("ldl", i64),
+                ("W1", vp), ("w1_e", i64), ("w1_n", i64), ("S1", vp), ("s1_e", i64), ("s1_n", i64),
+                ("W2", vp), ("w2_e", i64), ("w2_n", i64), ("S2", vp), ("s2_e", i64), ("s2_n", i64),
+                ("Y", vp), ("ldy", i64), ("T", i64), ("E", i64), ("H", i64), ("I", i64), ("top_k", i32),
+                ("fmt", i32), ("fmt_logits", i32), ("mx4", i32), ("renormalize", i32)]
 
 
 def _load():
@@ -114,6 +124,10 @@ def _load():
     lib.gemm_mx4_workspace_bytes.restype = sz
     lib.gemm_mx4_a16.argtypes = [vp, i32, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp]
     lib.gemm_mx4_a16.restype = ctypes.c_int
+    lib.gemm_moe.argtypes = [ctypes.POINTER(MoeArgs), vp, vp, sz]
+    lib.gemm_moe.restype = ctypes.c_int
+    lib.gemm_moe_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    lib.gemm_moe_workspace_bytes.restype = sz
     lib.gemm_f16_status_string.argtypes = [ctypes.c_int]
     lib.gemm_f16_status_string.restype = ctypes.c_char_p
     lib.gemm_f16_version.argtypes = []

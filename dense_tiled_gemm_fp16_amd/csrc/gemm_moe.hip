@@ -1,0 +1,171 @@
+// Host side of include/gemm_moe.h: validation and the two launches of a
+// mixture-of-experts layer for a few tokens.  Everything is checked before
+// the first HIP call, so on any error nothing is enqueued.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/gemm_moe.h"
+#include "host_util.hpp"
+#include "moe_kernel.hpp"
+
+using namespace gemmf16;
+
+static_assert(kMoeTokens == GEMM_MOE_MAX_TOKENS && kMoeExperts == GEMM_MOE_MAX_EXPERTS &&
+                  kMoeTopK == GEMM_MOE_MAX_TOP_K,
+              "bounds of the header");
+
+namespace {
+
+constexpr int64_t kMaxSize = INT64_C(1) << 30;   // H and I
+
+struct Layout {
+  int64_t act_row, act_part, tab_e, tab_p, bytes;
+};
+
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+bool sizes_ok(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
+  return T >= 1 && T <= kMoeTokens && E >= 1 && E <= kMoeExperts && k >= 1 && k <= kMoeTopK && k <= E &&
+         H >= 1 && H <= kMaxSize && I >= 1 && I <= kMaxSize;
+}
+
+Layout layout(int64_t T, int64_t k, int64_t I) {
+  Layout l;
+  l.act_row = 2 * cdiv(I, 8) * 8;
+  l.act_part = up256(T * k * l.act_row);
+  l.tab_e = 2 * l.act_part;
+  l.tab_p = l.tab_e + up256(4 * T * k);
+  l.bytes = l.tab_p + up256(4 * T * k);
+  return l;
+}
+
+struct Range {
+  uintptr_t lo, hi;
+};
+
+// Bytes of a [G][R] stack of rows of row_bytes bytes (strides in bytes).
+bool stack(const void* p, int64_t G, int64_t sg, int64_t R, int64_t sr, int64_t row_bytes, Range* out) {
+  int64_t a, b;
+  if (__builtin_mul_overflow(G - 1, sg, &a) || __builtin_mul_overflow(R - 1, sr, &b) ||
+      __builtin_add_overflow(a, b, &a) || __builtin_add_overflow(a, row_bytes, &a) || a > INT64_MAX / 2)
+    return false;
+  out->lo = (uintptr_t)p;
+  out->hi = out->lo + (uintptr_t)a;
+  return out->hi >= out->lo;
+}
+
+template <int WF, int DT>
+int launch_layer(const MoeArgs& a, hipStream_t s) {
+  MoeArgs copy = a;
+  void* p[] = {&copy};
+  const dim3 up((unsigned)cdiv(a.I, 16), (unsigned)(a.by_pair ? a.T * a.k : a.E));
+  if (hipLaunchKernel((const void*)moe_up_kernel<WF, DT>, up, dim3(64 * kStripWaves), p, 0, s) != hipSuccess)
+    return GEMM_ERR_HIP;
+  const dim3 down((unsigned)cdiv(a.H, 16));
+  if (hipLaunchKernel((const void*)moe_down_kernel<WF, DT>, down, dim3(64 * kStripWaves), p, 0, s) !=
+      hipSuccess)
+    return GEMM_ERR_HIP;
+  return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gemm_moe_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I) {
+  return sizes_ok(T, E, top_k, H, I) ? (size_t)layout(T, top_k, I).bytes : 0;
+}
+
+int gemm_moe(const gemm_moe_args* g, void* stream, void* workspace, size_t workspace_bytes) {
+  if (!g || !g->X || !g->logits || !g->W1 || !g->W2 || !g->Y || (g->mx4 == 1 && (!g->S1 || !g->S2)))
+    return GEMM_ERR_NULL;
+  if (!sizes_ok(g->T, g->E, g->top_k, g->H, g->I)) return GEMM_ERR_SHAPE;
+  if ((g->fmt != GEMM_FMT_F16 && g->fmt != GEMM_FMT_BF16) || g->fmt_logits < GEMM_FMT_F16 ||
+      g->fmt_logits > GEMM_FMT_F32 || (g->mx4 != 0 && g->mx4 != 1))
+    return GEMM_ERR_OPTS;
+  const int64_t T = g->T, E = g->E, H = g->H, I = g->I;
+  const int64_t hb = cdiv(H, kMxBlock), ib = cdiv(I, kMxBlock);
+  // Row lengths and strides of the weights in bytes.
+  const int64_t es = g->mx4 ? 1 : 2;
+  const int64_t row1 = g->mx4 ? hb * kMxBytes : 2 * H, row2 = g->mx4 ? ib * kMxBytes : 2 * I;
+  if (g->ldx <= 0 || g->ldl <= 0 || g->w1_n <= 0 || g->w2_n <= 0 || g->w1_e < 0 || g->w2_e < 0)
+    return GEMM_ERR_STRIDE;
+  if (g->mx4 && (g->s1_n <= 0 || g->s2_n <= 0 || g->s1_e < 0 || g->s2_e < 0 || g->w1_n < row1 || g->s1_n < hb ||
+                 (H > 1 && (g->w2_n < row2 || g->s2_n < ib))))
+    return GEMM_ERR_STRIDE;
+  if (g->ldy < H) return GEMM_ERR_LDC;
+  if (std::max({g->ldx, g->ldl, g->ldy, g->w1_n, g->w2_n, g->w1_e, g->w2_e}) > INT64_MAX / 8)
+    return GEMM_ERR_SHAPE;
+  const int64_t el = g->fmt_logits == GEMM_FMT_F32 ? 4 : 2;
+  Range rx, rl, r1, r2, rs1{0, 0}, rs2{0, 0}, ry;
+  if (!stack(g->X, 1, 0, T, 2 * g->ldx, 2 * H, &rx) || !stack(g->logits, 1, 0, T, el * g->ldl, el * E, &rl) ||
+      !stack(g->W1, E, es * g->w1_e, 2 * I, es * g->w1_n, row1, &r1) ||
+      !stack(g->W2, E, es * g->w2_e, H, es * g->w2_n, row2, &r2) ||
+      !stack(g->Y, 1, 0, T, 2 * g->ldy, 2 * H, &ry))
+    return GEMM_ERR_SHAPE;
+  if (g->mx4 && (!stack(g->S1, E, g->s1_e, 2 * I, g->s1_n, hb, &rs1) ||
+                 !stack(g->S2, E, g->s2_e, H, g->s2_n, ib, &rs2)))
+    return GEMM_ERR_SHAPE;
+  const Range* in[] = {&rx, &rl, &r1, &r2, &rs1, &rs2};
+  for (const Range* r : in)
+    if (ranges_overlap(ry.lo, ry.hi, r->lo, r->hi)) return GEMM_ERR_ALIAS;
+  const Layout l = layout(T, g->top_k, I);
+
+  MoeArgs a;
+  a.x = (const char*)g->X;
+  a.ldx = 2 * g->ldx;
+  a.logits = g->logits;
+  a.ldl = g->ldl;
+  a.w1 = (const char*)g->W1;
+  a.w2 = (const char*)g->W2;
+  a.w1_e = es * g->w1_e;
+  a.w1_n = es * g->w1_n;
+  a.w2_e = es * g->w2_e;
+  a.w2_n = es * g->w2_n;
+  a.s1 = (const uint8_t*)g->S1;
+  a.s2 = (const uint8_t*)g->S2;
+  a.s1_e = g->s1_e;
+  a.s1_n = g->s1_n;
+  a.s2_e = g->s2_e;
+  a.s2_n = g->s2_n;
+  a.y = (uint16_t*)g->Y;
+  a.ldy = g->ldy;
+  a.act_row = l.act_row;
+  a.act_part = l.act_part;
+  a.H = H;
+  a.I = I;
+  a.T = (int32_t)T;
+  a.E = (int32_t)E;
+  a.k = g->top_k;
+  a.fmt_l = g->fmt_logits;
+  // Fewer pairs than experts: most experts are unused, so workgroups go by
+  // pair (each finds its expert) instead of by expert.
+  a.by_pair = T * g->top_k < E;
+  a.renormalize = g->renormalize != 0;
+
+  hipStream_t s = (hipStream_t)stream;
+  void* ws = workspace;
+  if (workspace) {
+    if (workspace_bytes < (size_t)l.bytes || ((uintptr_t)workspace & 255u)) return GEMM_ERR_WORKSPACE;
+    const uintptr_t w0 = (uintptr_t)workspace, w1 = w0 + (uintptr_t)l.bytes;
+    for (const Range* r : in)
+      if (ranges_overlap(w0, w1, r->lo, r->hi)) return GEMM_ERR_ALIAS;
+    if (ranges_overlap(w0, w1, ry.lo, ry.hi)) return GEMM_ERR_ALIAS;
+  } else if (hipMallocAsync(&ws, (size_t)l.bytes, s) != hipSuccess) {
+    return GEMM_ERR_HIP;
+  }
+  a.act = (char*)ws;
+  a.tab_e = (int32_t*)((char*)ws + l.tab_e);
+  a.tab_p = (float*)((char*)ws + l.tab_p);
+  int rc;
+  if (g->mx4)
+    rc = g->fmt == GEMM_FMT_F16 ? launch_layer<SW_MX4, DT_F16>(a, s) : launch_layer<SW_MX4, DT_BF16>(a, s);
+  else
+    rc = g->fmt == GEMM_FMT_F16 ? launch_layer<SW_F16, DT_F16>(a, s) : launch_layer<SW_BF16, DT_BF16>(a, s);
+  if (!workspace && hipFreeAsync(ws, s) != hipSuccess && rc == GEMM_OK) rc = GEMM_ERR_HIP;
+  return rc;
+}
+
+}  // extern "C"

@@ -1,0 +1,93 @@
+"""A mixture-of-experts layer for a few tokens (a decode step): routing, the
+experts' products and the weighted sum in two kernels.  Argument marshalling
+for include/gemm_moe.h; the computation runs in the HIP library.
+
+    gemm_moe(x, logits, w_gate_up, w_down, top_k)        -> y [T, H]
+    gemm_moe_workspace_bytes(T, E, top_k, H, I)
+"""
+import contextlib
+import ctypes
+
+import torch
+
+from ._lib import GEMM_OK, MoeArgs, lib
+from .mx4 import FORMATS, MX4, _device, _error, _stream
+
+MAX_TOKENS, MAX_EXPERTS, MAX_TOP_K = 64, 512, 16
+
+
+def gemm_moe_workspace_bytes(T, E, top_k, H, I):
+    """Bytes of workspace gemm_moe needs for these sizes."""
+    return int(lib.gemm_moe_workspace_bytes(T, E, top_k, H, I))
+
+
+def _weights(w, name):
+    """(pointer, expert stride, row stride, scales pointer and strides)."""
+    if isinstance(w, MX4):
+        return (w.data.data_ptr(), w.data.stride(0), w.data.stride(1), w.scales.data_ptr(), w.scales.stride(0),
+                w.scales.stride(1))
+    if w.stride(2) != 1 and w.shape[2] > 1:
+        raise ValueError(f"{name} must have unit stride along its last axis")
+    return w.data_ptr(), w.stride(0), w.stride(1), 0, 0, 0
+
+
+def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, workspace=None, stream=None):
+    """y [T, H] = sum over each token's top_k experts e of p_e w_down[e] (silu(g) * u),
+    with (g, u) the two halves of w_gate_up[e] x.
+
+    x [T, H] float16 or bfloat16 (T at most 64: for more tokens sort the rows
+    by expert and use gemm_grouped), logits [T, E] float32 or 16-bit, w_gate_up
+    [E, 2I, H] (gate rows first) and w_down [E, H, I], both of x's dtype or
+    both MX4.  All with unit stride along the last axis.
+
+    The top_k largest logits choose (equal ones: the lower index; -inf: never;
+    E at most 512, top_k at most 16).  p is the softmax of the chosen logits, or
+    with renormalize=False that of all.  A token of -inf logits alone, such as
+    a padded row of a batch, gets zeros.
+
+    Sums are fp32, and silu(g) * u keeps 16 significant bits or more; with
+    float16 weights it has to stay inside float16's range.
+
+    workspace: gemm_moe_workspace_bytes(T, E, top_k, H, I) bytes, 256-byte
+    aligned, not shared with a call that may overlap; allocated here when not
+    given."""
+    quantised = isinstance(w_gate_up, MX4)
+    if quantised != isinstance(w_down, MX4):
+        raise TypeError("w_gate_up and w_down must both be MX4 or both tensors")
+    if x.ndim != 2 or logits.ndim != 2 or w_gate_up.ndim != 3 or w_down.ndim != 3:
+        raise ValueError("expected x [T, H], logits [T, E], w_gate_up [E, 2I, H], w_down [E, H, I]")
+    if x.dtype not in (torch.float16, torch.bfloat16) or logits.dtype not in FORMATS:
+        raise TypeError("x must be float16 or bfloat16, logits float32, float16 or bfloat16")
+    if not quantised and (w_gate_up.dtype != x.dtype or w_down.dtype != x.dtype):
+        raise TypeError("16-bit weights must have x's dtype")
+    if not x.is_cuda or len({x.device, logits.device, w_gate_up.device, w_down.device}) != 1:
+        raise ValueError("inputs must share one GPU device")
+    T, H = x.shape
+    E, H2, I = w_down.shape
+    if logits.shape != (T, E) or w_gate_up.shape != (E, 2 * I, H) or H2 != H or min(T, H, E, I) <= 0:
+        raise ValueError("incompatible or empty shape")
+    if T > MAX_TOKENS or E > MAX_EXPERTS or not 1 <= top_k <= min(E, MAX_TOP_K):
+        raise ValueError(f"at most {MAX_TOKENS} tokens and {MAX_EXPERTS} experts, top_k in 1 .. "
+                         f"min(E, {MAX_TOP_K})")
+    if (x.stride(1) != 1 and H > 1) or (logits.stride(1) != 1 and E > 1):
+        raise ValueError("x and logits must have unit stride along the last axis")
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype or out.device != x.device or out.shape != (T, H) or out.stride(1) != 1 or \
+            out.stride(0) < H:
+        raise ValueError("out must be a row-major [T, H] tensor of x's dtype on its device")
+    p1, e1, n1, s1, se1, sn1 = _weights(w_gate_up, "w_gate_up")
+    p2, e2, n2, s2, se2, sn2 = _weights(w_down, "w_down")
+    args = MoeArgs(x.data_ptr(), x.stride(0), logits.data_ptr(), logits.stride(0), p1, e1, n1, s1, se1, sn1,
+                   p2, e2, n2, s2, se2, sn2, out.data_ptr(), out.stride(0), T, E, H, I, top_k,
+                   FORMATS[x.dtype], FORMATS[logits.dtype], int(quantised), int(bool(renormalize)))
+    with _device(x.device):
+        if workspace is None:
+            need = lib.gemm_moe_workspace_bytes(T, E, top_k, H, I)
+            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        rc = lib.gemm_moe(ctypes.byref(args), _stream(stream, x.device), workspace.data_ptr(),
+                          workspace.numel() * workspace.element_size())
+    if rc != GEMM_OK:
+        raise _error(rc)
+    return out
