@@ -9,6 +9,7 @@
 #include "../../include/gemm_mx4.h"
 #include "host_util.hpp"
 #include "mx4_convert.hpp"
+#include "mx4_tile_kernel.hpp"
 #include "strip_kernel.hpp"
 
 using namespace gemmf16;
@@ -70,6 +71,59 @@ int launch_strip_m(const StripArgs& a, hipStream_t s) {
   if (a.M <= 16) return launch_strip<XF, DT, 1, 1, 2>(a, s);
   if (a.M <= 32) return launch_strip<XF, DT, 1, 2, 2>(a, s);
   return launch_strip<XF, DT, 2, 4, 1>(a, s);
+}
+
+// The tile kernel's plan: its scale arrays, transposed, are the workspace.
+struct TilePlan {
+  int64_t steps, sa_rows, sb_rows;
+  size_t bytes;
+};
+
+TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
+  TilePlan p;
+  p.steps = cdiv(K, 128);
+  p.sa_rows = cdiv(M, Mx4Cfg::BM) * Mx4Cfg::BM;
+  p.sb_rows = cdiv(N, Mx4Cfg::BN) * Mx4Cfg::BN;
+  p.bytes = (size_t)(4 * p.steps * (p.sa_rows + p.sb_rows));
+  return p;
+}
+
+// The tile kernel takes more than 64 rows; its lane offsets span 255 rows in
+// 32 bits.
+bool takes_tile(int64_t M, int64_t K) { return M > 64 && K <= (INT64_C(1) << 24); }
+constexpr int64_t kMaxTileLd = INT64_C(1) << 24;
+
+template <int DT>
+int launch_tile(const StripArgs& a, void* ws, hipStream_t s) {
+  const TilePlan p = tile_plan(a.M, a.N, a.K);
+  uint32_t* sa = (uint32_t*)ws;
+  uint32_t* sb = sa + p.steps * p.sa_rows;
+  Mx4ScaleArgs q{{a.as, a.bs}, {a.ldas, a.ldbs}, {a.M, a.N}, {p.sa_rows, p.sb_rows}, {sa, sb},
+                 cdiv(a.K, kMxBlock), p.steps};
+  const int64_t gx = cdiv(std::max(p.sa_rows, p.sb_rows), 64), gy = cdiv(p.steps, 16);
+  Mx4TileArgs t{};
+  t.k.A = (const uint16_t*)a.a;
+  t.k.lda_m = a.lda;
+  t.k.B = (const uint16_t*)a.b;
+  t.k.ldb_n = a.ldb;
+  t.k.C = a.c;
+  t.k.ldc = a.ldc;
+  t.k.M = a.M;
+  t.k.N = a.N;
+  t.k.K = a.K;
+  t.k.GM = cdiv(a.M, Mx4Cfg::BM);
+  t.k.GN = cdiv(a.N, Mx4Cfg::BN);
+  t.k.panel = 4;
+  t.sa = sa;
+  t.sa_rows = p.sa_rows;
+  t.sb = sb;
+  t.sb_rows = p.sb_rows;
+  int64_t grid;
+  if (__builtin_mul_overflow(t.k.GM, t.k.GN, &grid) || grid > kMaxGrid || gx > kMaxGrid || gy > 65535)
+    return GEMM_ERR_SHAPE;
+  const int rc = run((const void*)mx4_scales_kernel, dim3((unsigned)gx, (unsigned)gy, 2), 256, &q, s);
+  if (rc) return rc;
+  return run((const void*)mx4_tile_kernel<DT>, dim3((unsigned)grid), Mx4Cfg::NT, &t, s);
 }
 
 }  // namespace
@@ -155,14 +209,16 @@ int gemm_mx4_dequantize(const void* data, int64_t ldd, const void* scales, int64
 }
 
 size_t gemm_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  (void)M; (void)N; (void)K;
-  return 0;
+  if (M <= 0 || N <= 0 || K <= 0 || M > INT64_MAX / 8 || N > INT64_MAX / 8 || !takes_tile(M, K)) return 0;
+  const int64_t rows = cdiv(M, 256) * 256 + cdiv(N, 256) * 256;
+  int64_t bytes;
+  if (__builtin_mul_overflow(4 * cdiv(K, 128), rows, &bytes)) return 0;
+  return (size_t)bytes;
 }
 
 int gemm_mx4(const void* A, int64_t lda, const void* SA, int64_t ldsa, const void* B, int64_t ldb,
              const void* SB, int64_t ldsb, void* C, int32_t fmt_c, int64_t ldc, int64_t M, int64_t N,
              int64_t K, void* stream, void* workspace, size_t workspace_bytes) {
-  (void)workspace; (void)workspace_bytes;
   if (!A || !SA || !B || !SB || !C) return GEMM_ERR_NULL;
   if (M <= 0 || N <= 0 || K <= 0 || K > kMaxK) return GEMM_ERR_SHAPE;
   if (fmt_c != GEMM_FMT_F16 && fmt_c != GEMM_FMT_BF16) return GEMM_ERR_OPTS;
@@ -176,8 +232,24 @@ int gemm_mx4(const void* A, int64_t lda, const void* SA, int64_t ldsa, const voi
   if (overlap(rc_, ra) || overlap(rc_, rsa) || overlap(rc_, rb) || overlap(rc_, rsb)) return GEMM_ERR_ALIAS;
   const StripArgs a{(const char*)A, lda, (const uint8_t*)SA, ldsa, (const char*)B, ldb, (const uint8_t*)SB,
                     ldsb, (uint16_t*)C, ldc, M, N, K};
-  return fmt_c == GEMM_FMT_F16 ? launch_strip_m<SX_MX4, DT_F16>(a, (hipStream_t)stream)
-                               : launch_strip_m<SX_MX4, DT_BF16>(a, (hipStream_t)stream);
+  hipStream_t s = (hipStream_t)stream;
+  const bool f16 = fmt_c == GEMM_FMT_F16;
+  if (!takes_tile(M, K) || lda > kMaxTileLd || ldb > kMaxTileLd)
+    return f16 ? launch_strip_m<SX_MX4, DT_F16>(a, s) : launch_strip_m<SX_MX4, DT_BF16>(a, s);
+  const size_t need = gemm_mx4_workspace_bytes(M, N, K);
+  if (need == 0) return GEMM_ERR_SHAPE;
+  void* ws = workspace;
+  if (workspace) {
+    if (workspace_bytes < need || ((uintptr_t)workspace & 255u)) return GEMM_ERR_WORKSPACE;
+    const Range rw{(uintptr_t)workspace, (uintptr_t)workspace + need};
+    if (overlap(rw, ra) || overlap(rw, rsa) || overlap(rw, rb) || overlap(rw, rsb) || overlap(rw, rc_))
+      return GEMM_ERR_ALIAS;
+  } else if (hipMallocAsync(&ws, need, s) != hipSuccess) {
+    return GEMM_ERR_HIP;
+  }
+  rc = f16 ? launch_tile<DT_F16>(a, ws, s) : launch_tile<DT_BF16>(a, ws, s);
+  if (!workspace && hipFreeAsync(ws, s) != hipSuccess && rc == GEMM_OK) rc = GEMM_ERR_HIP;
+  return rc;
 }
 
 int gemm_mx4_a16(const void* A, int32_t fmt, int64_t lda, const void* B, int64_t ldb, const void* SB,
