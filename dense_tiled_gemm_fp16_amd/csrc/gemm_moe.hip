@@ -56,18 +56,24 @@ bool stack(const void* p, int64_t G, int64_t sg, int64_t R, int64_t sr, int64_t 
   return out->hi >= out->lo;
 }
 
-template <int WF, int DT>
-int launch_layer(const MoeArgs& a, hipStream_t s) {
+template <int WF, int DT, int MT>
+int launch_kernels(const MoeArgs& a, hipStream_t s) {
   MoeArgs copy = a;
   void* p[] = {&copy};
-  const dim3 up((unsigned)cdiv(a.I, 16), (unsigned)(a.by_pair ? a.T * a.k : a.E));
-  if (hipLaunchKernel((const void*)moe_up_kernel<WF, DT>, up, dim3(64 * kStripWaves), p, 0, s) != hipSuccess)
+  const dim3 up((unsigned)cdiv(a.I, 16 * (kMoeWaves / a.parts)), (unsigned)(a.by_pair ? a.T * a.k : a.E));
+  if (hipLaunchKernel((const void*)moe_up_kernel<WF, DT, MT>, up, dim3(64 * kMoeWaves), p, 0, s) != hipSuccess)
     return GEMM_ERR_HIP;
   const dim3 down((unsigned)cdiv(a.H, 16));
-  if (hipLaunchKernel((const void*)moe_down_kernel<WF, DT>, down, dim3(64 * kStripWaves), p, 0, s) !=
-      hipSuccess)
+  if (hipLaunchKernel((const void*)moe_down_kernel<WF, DT, MT>, down, dim3(64 * kMoeWaves), p, 0, s) != hipSuccess)
     return GEMM_ERR_HIP;
   return GEMM_OK;
+}
+
+template <int WF, int DT>
+int launch_layer(const MoeArgs& a, hipStream_t s) {
+  if (a.T <= 16) return launch_kernels<WF, DT, 1>(a, s);
+  if (a.T <= 32) return launch_kernels<WF, DT, 2>(a, s);
+  return launch_kernels<WF, DT, 4>(a, s);
 }
 
 }  // namespace
@@ -144,6 +150,14 @@ int gemm_moe(const gemm_moe_args* g, void* stream, void* workspace, size_t works
   // pair (each finds its expert) instead of by expert.
   a.by_pair = T * g->top_k < E;
   a.renormalize = g->renormalize != 0;
+  // Parts of H per strip: as few as leave every compute unit two workgroups
+  // of distinct work (the device's at most min(E, T top_k) experts in use).
+  int cus = 0;
+  int rc = device_cus(&cus);
+  if (rc) return rc;
+  const int64_t strips = cdiv(I, 16) * std::min(E, T * g->top_k);
+  a.parts = 1;
+  while (a.parts < kMoeWaves && strips * a.parts < (int64_t)2 * cus * kMoeWaves) a.parts *= 2;
 
   hipStream_t s = (hipStream_t)stream;
   void* ws = workspace;
@@ -159,7 +173,6 @@ int gemm_moe(const gemm_moe_args* g, void* stream, void* workspace, size_t works
   a.act = (char*)ws;
   a.tab_e = (int32_t*)((char*)ws + l.tab_e);
   a.tab_p = (float*)((char*)ws + l.tab_p);
-  int rc;
   if (g->mx4)
     rc = g->fmt == GEMM_FMT_F16 ? launch_layer<SW_MX4, DT_F16>(a, s) : launch_layer<SW_MX4, DT_BF16>(a, s);
   else

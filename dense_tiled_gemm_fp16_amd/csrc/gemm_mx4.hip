@@ -57,20 +57,20 @@ int check_mx4(const void* data, int64_t ldd, const void* scales, int64_t lds, in
 // K up to 2^36, as the 16-bit tiles: chunk counters stay far inside int64.
 constexpr int64_t kMaxK = INT64_C(1) << 36;
 
-template <int XF, int DT, int NS, int MT, int UC>
+template <int XF, int DT, int NS, int MT, int UC, int NW>
 int launch_strip(const StripArgs& a, hipStream_t s) {
   const int64_t gx = cdiv(a.N, 16 * NS), gy = cdiv(a.M, 16 * MT);
   if (gx > kMaxGrid || gy > 65535) return GEMM_ERR_SHAPE;
   StripArgs copy = a;
-  return run((const void*)mx4_strip_kernel<XF, DT, NS, MT, UC>, dim3((unsigned)gx, (unsigned)gy),
-             64 * kStripWaves, &copy, s);
+  return run((const void*)mx4_strip_kernel<XF, DT, NS, MT, UC, NW>, dim3((unsigned)gx, (unsigned)gy), 64 * NW,
+             &copy, s);
 }
 
 template <int XF, int DT>
 int launch_strip_m(const StripArgs& a, hipStream_t s) {
-  if (a.M <= 16) return launch_strip<XF, DT, 1, 1, 2>(a, s);
-  if (a.M <= 32) return launch_strip<XF, DT, 1, 2, 2>(a, s);
-  return launch_strip<XF, DT, 2, 4, 1>(a, s);
+  if (a.M <= 16) return launch_strip<XF, DT, 1, 1, 2, 8>(a, s);
+  if (a.M <= 32) return launch_strip<XF, DT, 1, 2, 2, 8>(a, s);
+  return launch_strip<XF, DT, 2, 4, 1, 8>(a, s);
 }
 
 // The tile kernel's plan: its scale arrays, transposed, are the workspace.

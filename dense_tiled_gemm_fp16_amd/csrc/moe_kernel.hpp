@@ -13,18 +13,22 @@
 // the token's top_k, so results go to row t * top_k + rank of an array whose
 // rows need no sorting or prefix sums.
 //
-//   moe_up    workgroup -> (expert, 16 rows of I): gate and up strips of
-//             16 rows each over all of H, the waves splitting H; sums, silu(g)
-//             u, two 16-bit parts per value into row (token, slot).  With
+//   moe_up    wave -> (expert, 16 rows of I, a part of H): gate and up strips
+//             of 16 rows each; the parts of H meet in LDS; silu(g) u, two
+//             16-bit parts per value, into row (token, slot).  The waves of a
+//             workgroup are kMoeWaves / parts neighbouring strips times the
+//             parts: as few parts as still fill the device, so that a wave
+//             streams long rows and the workgroup's waves meet A in L1.  With
 //             fewer (token, slot) pairs than experts, a workgroup is tied to a
 //             pair instead, and only the first pair of an expert goes on.  The
-//             workgroups of the first strip also write the pair's expert and
+//             workgroups of the first strips also write the pair's expert and
 //             its softmax weight.
 //   moe_down  workgroup -> 16 columns of Y, all experts: the waves share the
-//             (expert, chunk of I) sequence evenly, each adds p * (sums) into
-//             its own [T, 16] accumulators in LDS at every expert's end, and
-//             the waves' accumulators are added in order.  So the weighted sum
-//             over experts needs no atomics and no further pass.
+//             (expert, chunk of I) sequence evenly, loads running ahead across
+//             experts, each adds p * (sums) into its own [T, 16] accumulators
+//             in LDS at every expert's end, and the waves' accumulators are
+//             added in order.  So the weighted sum over experts needs no
+//             atomics and no further pass.
 #pragma once
 
 #include "strip_kernel.hpp"
@@ -33,6 +37,7 @@ namespace gemmf16 {
 
 constexpr int kMoeTokens = 64, kMoeExperts = 512, kMoeTopK = 16;
 constexpr int kMoePairs = kMoeTokens * kMoeTopK;
+constexpr int kMoeWaves = 8;
 
 struct MoeArgs {
   const char* x;
@@ -51,6 +56,7 @@ struct MoeArgs {
   float* tab_p;                // its softmax over all experts
   int64_t H, I;
   int32_t T, E, k, fmt_l, by_pair, renormalize;
+  int32_t parts;               // of H, in moe_up: 1, 2, 4 or 8
 };
 
 // Logit as an integer of the same order: NaN above all, both zeros equal.
@@ -113,9 +119,10 @@ __device__ __forceinline__ void split_parts(float v, uint16_t& hi, uint16_t& lo)
   lo = cvt_out<DT>(r == r && fabsf(r) <= fabsf(v) ? r : 0.0f);   // nothing beside an infinity or a NaN
 }
 
+template <int MT>
 struct MoeUpShared {
   union {
-    f32x4 part[kStripWaves * 2 * 4 * 64];
+    f32x4 part[kMoeWaves * 2 * MT * 64];
     uint32_t key[kMoeExperts];
   };
   int rank[kMoeTokens];     // slot of the expert in the token's choice, -1 not chosen
@@ -124,66 +131,74 @@ struct MoeUpShared {
 };
 
 template <int WF, int DT, int MT, int UC>
-__device__ __forceinline__ void moe_up_tiles(const MoeArgs& a, MoeUpShared& sh, int e, int64_t i0, int lane,
-                                             int wave) {
+__device__ __forceinline__ void moe_up_tiles(const MoeArgs& a, MoeUpShared<MT>& sh, int e, int lane, int wave) {
   using S = Strip<WF, DT == DT_F16 ? SX_F16 : SX_BF16, 2, MT, UC>;
-  const int m = sh.count;
-  S s;
-  s.xp = 0;
-  int64_t row = i0 + (lane & 15);
-  if (row >= a.I) row = a.I - 1;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    s.w[h] = a.w1 + e * a.w1_e + (h * a.I + row) * a.w1_n;
-    s.ws[h] = a.s1 + e * a.s1_e + (h * a.I + row) * a.s1_n;
-  }
-  f32x4 acc[2][MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int p = 16 * t + (lane & 15);
-    s.x[t] = a.x + sh.list[p < m ? p : m - 1] * a.ldx;
-    s.xs[t] = nullptr;
-    acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-  const int64_t nc = S::chunks(a.H);
-  s.run(acc, nc * wave / kStripWaves, nc * (wave + 1) / kStripWaves, a.H, lane);
   constexpr int TILES = 2 * MT;
+  const int m = __builtin_amdgcn_readfirstlane(sh.count), tiles = (m + 15) / 16;
+  const int strips = kMoeWaves / a.parts;      // of this workgroup
+  const int strip = wave / a.parts, part = wave - strip * a.parts;
+  const int64_t i0 = ((int64_t)blockIdx.x * strips + strip) * 16;
+  if (i0 < a.I) {
+    typename S::WPtr w;
+    typename S::XPtr x;
+    x.part = 0;
+    int64_t row = i0 + (lane & 15);
+    if (row >= a.I) row = a.I - 1;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      w.w[h] = a.w1 + e * a.w1_e + (h * a.I + row) * a.w1_n;
+      w.s[h] = a.s1 + e * a.s1_e + (h * a.I + row) * a.s1_n;
+    }
 #pragma unroll
-    for (int t = 0; t < MT; ++t) sh.part[(wave * TILES + h * MT + t) * 64 + lane] = acc[h][t];
+    for (int t = 0; t < MT; ++t) {
+      const int p = 16 * t + (lane & 15);
+      x.x[t] = a.x + sh.list[p < m ? p : m - 1] * a.ldx;
+      x.s[t] = nullptr;
+    }
+    f32x4 acc[2][MT];
+    S::clear(acc);
+    const int64_t nc = S::chunks(a.H);
+    S::run(acc, w, x, nc * part / a.parts, nc * (part + 1) / a.parts, a.H, lane >> 4, tiles == 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) sh.part[(wave * TILES + h * MT + t) * 64 + lane] = acc[h][t];
+  }
   __syncthreads();
-  if (wave < MT) {
-    const f32x4 gate = sum_waves<kStripWaves, TILES>(sh.part, wave, lane);
-    const f32x4 up = sum_waves<kStripWaves, TILES>(sh.part, MT + wave, lane);
-    const int p = 16 * wave + (lane & 15);
-    const int64_t i = i0 + 4 * (lane >> 4);
+  for (int j = wave; j < strips * tiles; j += kMoeWaves) {
+    const int s = j / tiles, t = j - s * tiles;
+    const f32x4* base = sh.part + s * a.parts * TILES * 64 + t * 64;
+    const int p = 16 * t + (lane & 15);
+    const int64_t i = ((int64_t)blockIdx.x * strips + s) * 16 + 4 * (lane >> 4);
     if (p < m && i < a.I) {       // rows hold a multiple of 8 values: all four fit
-      const int t = sh.list[p];
+      const f32x4 gate = sum_waves(base, TILES * 64, a.parts, lane);
+      const f32x4 up = sum_waves(base + MT * 64, TILES * 64, a.parts, lane);
+      const int token = sh.list[p];
       uint16_t hi[4], lo[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         split_parts<WF == SW_F16>(gate[r] / (1.0f + expf(-gate[r])) * up[r], hi[r], lo[r]);
-      char* q = a.act + (t * a.k + sh.rank[t]) * a.act_row + 2 * i;
+      char* q = a.act + (token * a.k + sh.rank[token]) * a.act_row + 2 * i;
       __builtin_memcpy(q, hi, 8);
       __builtin_memcpy(q + a.act_part, lo, 8);
     }
   }
 }
 
-// Grid (strips of 16 rows of I, experts or pairs).  DT: format of X.
-template <int WF, int DT>
-__global__ __launch_bounds__(64 * kStripWaves) void moe_up_kernel(MoeArgs a) {
-  __shared__ MoeUpShared sh;
+// Grid (groups of strips of 16 rows of I, experts or pairs).  DT: format of X;
+// MT: tiles of 16 tokens that T needs.
+template <int WF, int DT, int MT>
+__global__ __launch_bounds__(64 * kMoeWaves, MT < 2 ? 4 : 2) void moe_up_kernel(MoeArgs a) {
+  __shared__ MoeUpShared<MT> sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slot = blockIdx.y;
   int e = slot;
   if (a.by_pair) {
     // The expert of rank slot % k of token slot / k.
     const int t0 = slot / a.k, r0 = slot - t0 * a.k;
-    for (int j = tid; j < a.E; j += 64 * kStripWaves) sh.key[j] = logit_key(load_logit(a, t0, j));
+    for (int j = tid; j < a.E; j += 64 * kMoeWaves) sh.key[j] = logit_key(load_logit(a, t0, j));
     __syncthreads();
-    for (int c = tid; c < a.E; c += 64 * kStripWaves) {
+    for (int c = tid; c < a.E; c += 64 * kMoeWaves) {
       const uint32_t kc = sh.key[c];
       int n = 0;
       for (int j = 0; j < a.E; ++j) n += (sh.key[j] > kc || (sh.key[j] == kc && j < c)) ? 1 : 0;
@@ -201,7 +216,7 @@ __global__ __launch_bounds__(64 * kStripWaves) void moe_up_kernel(MoeArgs a) {
     __syncthreads();
   }
   const bool writes = blockIdx.x == 0;
-  for (int t = wave; t < a.T; t += kStripWaves) {
+  for (int t = wave; t < a.T; t += kMoeWaves) {
     const float l = load_logit(a, t, e);
     const uint32_t ke = logit_key(l);
     const int r = logit_rank(a, t, e, ke, lane);
@@ -224,7 +239,7 @@ __global__ __launch_bounds__(64 * kStripWaves) void moe_up_kernel(MoeArgs a) {
   if (m == 0) return;
   if (a.by_pair && __builtin_amdgcn_readfirstlane(sh.list[0]) != slot / a.k) return;
   if (writes) {
-    for (int i = wave; i < m; i += kStripWaves) {
+    for (int i = wave; i < m; i += kMoeWaves) {
       const int t = sh.list[i];
       const float p = softmax_weight(a, t, e, lane);
       if (lane == 0) {
@@ -233,65 +248,27 @@ __global__ __launch_bounds__(64 * kStripWaves) void moe_up_kernel(MoeArgs a) {
       }
     }
   }
-  const int64_t i0 = (int64_t)blockIdx.x * 16;
-  if (m <= 16)
-    moe_up_tiles<WF, DT, 1, WF == SW_MX4 ? 2 : 4>(a, sh, e, i0, lane, wave);
-  else if (m <= 32)
-    moe_up_tiles<WF, DT, 2, WF == SW_MX4 ? 1 : 4>(a, sh, e, i0, lane, wave);
-  else
-    moe_up_tiles<WF, DT, 4, WF == SW_MX4 ? 1 : 2>(a, sh, e, i0, lane, wave);
+  moe_up_tiles<WF, DT, MT, WF == SW_MX4 ? (MT == 4 ? 1 : 2) : (MT == 4 ? 2 : 4)>(a, sh, e, lane, wave);
 }
 
+template <int MT>
 struct MoeDownShared {
-  float own[kStripWaves][kMoeTokens][16];
+  float own[kMoeWaves][16 * MT][16];
   uint32_t mask[kMoeExperts][2];     // tokens of an expert
   uint16_t active[kMoeExperts], place[kMoeExperts];
   uint16_t start[kMoeExperts + 1];
-  uint32_t rows[kMoePairs];          // token << 16 | pair, by expert
-  int32_t expert[kMoePairs];
-  float prob[kMoePairs];
+  uint32_t rows[16 * MT * kMoeTopK];   // token << 16 | pair, by expert
+  int32_t expert[16 * MT * kMoeTopK];
+  float prob[16 * MT * kMoeTopK];
   int n_active;
 };
 
-// p * (W2[e] rows h0 .. h0+15) (act rows of e) over chunks [c0, c1), into this
-// wave's accumulators.
-template <int WF, int MT, int UC>
-__device__ __forceinline__ void moe_down_segment(const MoeArgs& a, MoeDownShared& sh, int e, int first, int m,
-                                                 int64_t h0, int64_t c0, int64_t c1, int lane, int wave) {
-  using S = Strip<WF, WF == SW_F16 ? SX_F16P : SX_BF16P, 1, MT, UC>;
-  S s;
-  s.xp = a.act_part;
-  int64_t row = h0 + (lane & 15);
-  if (row >= a.H) row = a.H - 1;
-  s.w[0] = a.w2 + e * a.w2_e + row * a.w2_n;
-  s.ws[0] = a.s2 + e * a.s2_e + row * a.s2_n;
-  f32x4 acc[1][MT];
-  uint32_t who[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int p = 16 * t + (lane & 15);
-    who[t] = sh.rows[first + (p < m ? p : m - 1)];
-    s.x[t] = a.act + (int64_t)(who[t] & 0xFFFFu) * a.act_row;
-    s.xs[t] = nullptr;
-    acc[0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-  s.run(acc, c0, c1, a.I, lane);
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    if (16 * t + (lane & 15) < m) {
-      const float p = sh.prob[who[t] & 0xFFFFu];
-      float* q = &sh.own[wave][who[t] >> 16][4 * (lane >> 4)];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) q[r] += p * acc[0][t][r];
-    }
-  }
-}
-
-template <int WF, int DT>
-__global__ __launch_bounds__(64 * kStripWaves) void moe_down_kernel(MoeArgs a) {
-  __shared__ MoeDownShared sh;
+template <int WF, int DT, int MT>
+__global__ __launch_bounds__(64 * kMoeWaves, MT < 2 ? 4 : 2) void moe_down_kernel(MoeArgs a) {
+  __shared__ MoeDownShared<MT> sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  constexpr int NT = 64 * kStripWaves;
+  constexpr int kPairs = 16 * MT * kMoeTopK;
+  constexpr int NT = 64 * kMoeWaves;
   const int pairs = a.T * a.k;
   for (int i = tid; i < a.E; i += NT) sh.mask[i][0] = sh.mask[i][1] = 0;
   for (int i = tid; i < pairs; i += NT) {
@@ -333,9 +310,9 @@ __global__ __launch_bounds__(64 * kStripWaves) void moe_down_kernel(MoeArgs a) {
     }
   }
   __syncthreads();
-  float prob[(kMoePairs + NT - 1) / NT];
+  float prob[(kPairs + NT - 1) / NT];
 #pragma unroll
-  for (int q = 0; q < (kMoePairs + NT - 1) / NT; ++q) {
+  for (int q = 0; q < (kPairs + NT - 1) / NT; ++q) {
     const int i = tid + q * NT;
     if (i >= pairs || sh.expert[i] < 0) continue;
     const int t = i / a.k, e = sh.expert[i];
@@ -350,38 +327,100 @@ __global__ __launch_bounds__(64 * kStripWaves) void moe_down_kernel(MoeArgs a) {
   }
   __syncthreads();
 #pragma unroll
-  for (int q = 0; q < (kMoePairs + NT - 1) / NT; ++q) {
+  for (int q = 0; q < (kPairs + NT - 1) / NT; ++q) {
     const int i = tid + q * NT;
     if (i < pairs && sh.expert[i] >= 0) sh.prob[i] = prob[q];
   }
   __syncthreads();
 
+  // This wave's share of the (expert, chunk) sequence, by groups of chunks of
+  // one expert; the weights of the next group load while a group's are
+  // multiplied, across experts too.
+  constexpr int UC = WF == SW_MX4 ? (MT == 1 ? 2 : 1) : (MT == 4 ? 2 : 4);
+  using S = Strip<WF, WF == SW_F16 ? SX_F16P : SX_BF16P, 1, MT, UC>;
   const int64_t h0 = (int64_t)blockIdx.x * 16;
-  constexpr int CK = WF == SW_MX4 ? 128 : 32;
-  const int cpe = (int)((a.I + CK - 1) / CK), n = __builtin_amdgcn_readfirstlane(sh.n_active);
+  const int g = lane >> 4;
+  const int cpe = (int)S::chunks(a.I), n = __builtin_amdgcn_readfirstlane(sh.n_active);
   const int64_t units = (int64_t)n * cpe;
-  int64_t u = units * wave / kStripWaves;
-  const int64_t u1 = units * (wave + 1) / kStripWaves;
-  while (u < u1) {
-    const int i = (int)(u / cpe), c0 = (int)(u - (int64_t)i * cpe);
-    const int c1 = (int)(c0 + (u1 - u) < cpe ? c0 + (u1 - u) : cpe);
-    const int e = __builtin_amdgcn_readfirstlane(sh.active[i]);
-    const int first = __builtin_amdgcn_readfirstlane(sh.start[i]);
-    const int m = __builtin_amdgcn_readfirstlane(sh.start[i + 1]) - first;
-    if (m <= 16)
-      moe_down_segment<WF, 1, WF == SW_MX4 ? 2 : 4>(a, sh, e, first, m, h0, c0, c1, lane, wave);
-    else if (m <= 32)
-      moe_down_segment<WF, 2, WF == SW_MX4 ? 1 : 4>(a, sh, e, first, m, h0, c0, c1, lane, wave);
-    else
-      moe_down_segment<WF, 4, WF == SW_MX4 ? 1 : 2>(a, sh, e, first, m, h0, c0, c1, lane, wave);
-    u += c1 - c0;
+  const int64_t u0 = units * wave / kMoeWaves, u1 = units * (wave + 1) / kMoeWaves;
+  int64_t row = h0 + (lane & 15);
+  if (row >= a.H) row = a.H - 1;
+  const char* const w_row = a.w2 + row * a.w2_n;
+  const uint8_t* const s_row = a.s2 + row * a.s2_n;
+  auto weights = [&](int i) {
+    const int64_t e = __builtin_amdgcn_readfirstlane(sh.active[i]);
+    typename S::WPtr p;
+    p.w[0] = w_row + e * a.w2_e;
+    p.s[0] = s_row + e * a.s2_e;
+    return p;
+  };
+  if (u0 < u1) {
+    int i = (int)(u0 / cpe), c = (int)(u0 - (int64_t)i * cpe);
+    int64_t left = u1 - u0;                                  // chunks from (i, c) on
+    int end = left < cpe - c ? c + (int)left : cpe;          // of this wave, in expert i
+    typename S::WPtr wp = weights(i);
+    typename S::XPtr xp;
+    xp.part = a.act_part;
+    typename S::WBuf cur, nxt;
+    typename S::XBuf x;
+    uint32_t who[MT];
+    int m = 0;
+    f32x4 acc[1][MT];
+    S::clear(acc);
+    bool fresh = true;
+    S::load_w(cur, wp, c, end, a.I, g);
+    while (true) {
+      if (fresh) {                                           // rows of the expert's tokens
+        const int first = __builtin_amdgcn_readfirstlane(sh.start[i]);
+        m = __builtin_amdgcn_readfirstlane(sh.start[i + 1]) - first;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const int p = 16 * t + (lane & 15);
+          who[t] = sh.rows[first + (p < m ? p : m - 1)];
+          xp.x[t] = a.act + (int64_t)(who[t] & 0xFFFFu) * a.act_row;
+          xp.s[t] = nullptr;
+        }
+        fresh = false;
+      }
+      S::load_x(x, xp, c, end, a.I, g, m <= 16);
+      // The next group: of this expert, or of the next one.
+      const bool last_of_expert = c + UC >= end;
+      const int64_t left_after = last_of_expert ? left - (end - c) : left - UC;
+      const bool more = left_after > 0;
+      const int i2 = last_of_expert ? i + 1 : i, c2 = last_of_expert ? 0 : c + UC;
+      const int end2 = !last_of_expert ? end : (left_after < cpe ? (int)left_after : cpe);
+      if (more) {
+        if (last_of_expert) wp = weights(i2);
+        S::load_w(nxt, wp, c2, end2, a.I, g);
+      }
+      S::mma(acc, cur, x, m <= 16);
+      if (last_of_expert) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          if (16 * t + (lane & 15) < m) {
+            const float p = sh.prob[who[t] & 0xFFFFu];
+            float* q = &sh.own[wave][who[t] >> 16][4 * g];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) q[r] += p * acc[0][t][r];
+          }
+        }
+        S::clear(acc);
+        fresh = true;
+      }
+      if (!more) break;
+      cur = nxt;
+      i = i2;
+      c = c2;
+      end = end2;
+      left = left_after;
+    }
   }
   __syncthreads();
   for (int i = tid; i < a.T * 4; i += NT) {
     const int t = i >> 2, g = i & 3;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < kStripWaves; ++w)
+    for (int w = 0; w < kMoeWaves; ++w)
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[r] += sh.own[w][t][4 * g + r];
     const int64_t h = h0 + 4 * g;

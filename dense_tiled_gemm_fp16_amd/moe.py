@@ -5,13 +5,12 @@ for include/gemm_moe.h; the computation runs in the HIP library.
     gemm_moe(x, logits, w_gate_up, w_down, top_k)        -> y [T, H]
     gemm_moe_workspace_bytes(T, E, top_k, H, I)
 """
-import contextlib
 import ctypes
 
 import torch
 
 from ._lib import GEMM_OK, MoeArgs, lib
-from .mx4 import FORMATS, MX4, _device, _error, _stream
+from .mx4 import FORMATS, MX4, _error, _on, _stream, _workspace
 
 MAX_TOKENS, MAX_EXPERTS, MAX_TOP_K = 64, 512, 16
 
@@ -73,21 +72,19 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
         raise ValueError("x and logits must have unit stride along the last axis")
     if out is None:
         out = torch.empty((T, H), dtype=x.dtype, device=x.device)
-    elif out.dtype != x.dtype or out.device != x.device or out.shape != (T, H) or out.stride(1) != 1 or \
-            out.stride(0) < H:
+    elif out.dtype != x.dtype or out.device != x.device or out.shape != (T, H) or \
+            (out.stride(1) != 1 and H > 1) or out.stride(0) < H:
         raise ValueError("out must be a row-major [T, H] tensor of x's dtype on its device")
     p1, e1, n1, s1, se1, sn1 = _weights(w_gate_up, "w_gate_up")
     p2, e2, n2, s2, se2, sn2 = _weights(w_down, "w_down")
     args = MoeArgs(x.data_ptr(), x.stride(0), logits.data_ptr(), logits.stride(0), p1, e1, n1, s1, se1, sn1,
                    p2, e2, n2, s2, se2, sn2, out.data_ptr(), out.stride(0), T, E, H, I, top_k,
                    FORMATS[x.dtype], FORMATS[logits.dtype], int(quantised), int(bool(renormalize)))
-    with _device(x.device):
-        if workspace is None:
-            need = lib.gemm_moe_workspace_bytes(T, E, top_k, H, I)
-            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        rc = lib.gemm_moe(ctypes.byref(args), _stream(stream, x.device), workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size())
+    if workspace is None:
+        workspace = _workspace(lib.gemm_moe_workspace_bytes(T, E, top_k, H, I), x.device, stream)
+    rc = _on(x.device, lambda: lib.gemm_moe(ctypes.byref(args), _stream(stream, x.device),
+                                            workspace.data_ptr(),
+                                            workspace.numel() * workspace.element_size()))
     if rc != GEMM_OK:
         raise _error(rc)
     return out

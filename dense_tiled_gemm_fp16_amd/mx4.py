@@ -9,8 +9,6 @@ computation runs in the HIP library.
                                      or float16 / bfloat16 [M, K]
     gemm_mx4_workspace_bytes(M, N, K)
 """
-import contextlib
-
 import torch
 
 from ._lib import GEMM_OK, lib
@@ -25,15 +23,27 @@ def _error(rc):
     return GemmError(rc)
 
 
-def _device(device):
-    """The device made current for a call; nothing to do where it is already."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# The current stream as an integer, without the Stream object around it.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on(device, call):
+    """call() with `device` current."""
+    if device.index == torch.cuda.current_device():
+        return call()
+    with torch.cuda.device(device):
+        return call()
 
 
 def _stream(stream, device):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
+
+
+def _workspace(nbytes, device, stream):
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 class MX4:
@@ -49,6 +59,8 @@ class MX4:
     Both have unit stride along the last axis; data rows start 16-byte aligned.
     Slices of rows and of the stack are views (q[g], q[g, r0:r1], q[r0:r1])."""
 
+    __slots__ = ("_data", "_scales", "_buffer", "K", "shape", "device")
+
     def __init__(self, data, scales, K):
         blocks = -(-K // BLOCK)
         if data.dtype != torch.uint8 or scales.dtype != torch.uint8:
@@ -61,25 +73,64 @@ class MX4:
             raise ValueError("data and scales must share one device")
         if data.stride(-1) != 1 or (scales.stride(-1) != 1 and blocks > 1):
             raise ValueError("data and scales must have unit stride along the last axis")
-        self.data, self.scales, self.K = data, scales, K
+        self._data, self._scales, self._buffer = data, scales, None
+        self.K, self.shape, self.device = K, (*data.shape[:-1], K), data.device
+
+    @classmethod
+    def _empty(cls, shape, device):
+        """Contiguous and uninitialised, data and scales in one allocation
+        (the tensors are made when they are asked for)."""
+        q = cls.__new__(cls)
+        rows = 1
+        for n in shape[:-1]:
+            rows *= n
+        K = shape[-1]
+        q._data = q._scales = None
+        q._buffer = torch.empty(17 * rows * -(-K // BLOCK), dtype=torch.uint8, device=device)
+        q.K, q.shape, q.device = K, tuple(shape), device
+        return q
+
+    def _split(self):
+        blocks = -(-self.K // BLOCK)
+        n = self._buffer.numel() // 17 * 16
+        self._data = self._buffer[:n].view(*self.shape[:-1], 16 * blocks)
+        self._scales = self._buffer[n:].view(*self.shape[:-1], blocks)
 
     @property
-    def shape(self):
-        return torch.Size((*self.data.shape[:-1], self.K))
+    def data(self):
+        if self._data is None:
+            self._split()
+        return self._data
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._split()
+        return self._scales
 
     @property
     def ndim(self):
-        return self.data.ndim
+        return len(self.shape)
 
     @property
-    def device(self):
-        return self.data.device
+    def is_cuda(self):
+        return self.device.type == "cuda"
+
+    def is_contiguous(self):
+        return self._buffer is not None or (self._data.is_contiguous() and self._scales.is_contiguous())
+
+    def _rows(self):
+        """(data pointer, row stride, scales pointer, row stride)."""
+        if self._buffer is not None:
+            p, blocks = self._buffer.data_ptr(), -(-self.K // BLOCK)
+            return p, 16 * blocks, p + self._buffer.numel() // 17 * 16, blocks
+        return self._data.data_ptr(), self._data.stride(-2), self._scales.data_ptr(), self._scales.stride(-2)
 
     def __getitem__(self, rows):
         return MX4(self.data[rows], self.scales[rows], self.K)
 
     def __repr__(self):
-        return f"MX4(shape={tuple(self.shape)}, device={self.device})"
+        return f"MX4(shape={self.shape}, device={self.device})"
 
 
 def quantize_mx4(x, out=None, stream=None):
@@ -91,27 +142,24 @@ def quantize_mx4(x, out=None, stream=None):
     6 scales.  A block with an infinity or a NaN becomes NaN.  The elements
     past K of the last block are zero.  out: an MX4 of x's shape with
     contiguous data and scales."""
-    if x.dtype not in FORMATS:
+    fmt, shape, strides, device = FORMATS.get(x.dtype), x.shape, x.stride(), x.device
+    if fmt is None:
         raise TypeError("expected float16, bfloat16 or float32")
-    if x.ndim not in (2, 3) or not x.is_cuda:
+    if len(shape) not in (2, 3) or not x.is_cuda:
         raise ValueError("expected an [R, K] matrix or a [G, R, K] stack on a GPU")
-    if min(x.shape) <= 0:
+    if min(shape) <= 0:
         raise ValueError("empty shape")
-    if min(x.stride()) <= 0:
+    if min(strides) <= 0:
         raise ValueError("strides must be positive")
-    K = x.shape[-1]
-    blocks = -(-K // BLOCK)
     if out is None:
-        out = MX4(torch.empty((*x.shape[:-1], 16 * blocks), dtype=torch.uint8, device=x.device),
-                  torch.empty((*x.shape[:-1], blocks), dtype=torch.uint8, device=x.device), K)
-    elif out.shape != x.shape or out.device != x.device or not out.data.is_contiguous() or \
-            not out.scales.is_contiguous():
+        out = MX4._empty(shape, device)
+    elif out.shape != tuple(shape) or out.device != device or not out.is_contiguous():
         raise ValueError("out must be an MX4 of x's shape on its device, contiguous")
-    G, sg = (x.shape[0], x.stride(0)) if x.ndim == 3 else (1, 1)
-    with _device(x.device):
-        rc = lib.gemm_mx4_quantize(x.data_ptr(), FORMATS[x.dtype], sg, x.stride(-2), x.stride(-1), G,
-                                   x.shape[-2], K, out.data.data_ptr(), out.scales.data_ptr(),
-                                   _stream(stream, x.device))
+    G, sg = (shape[0], strides[0]) if len(shape) == 3 else (1, 1)
+    data, _, scales, _ = out._rows()
+    rc = _on(device, lambda: lib.gemm_mx4_quantize(
+        x.data_ptr(), fmt, sg, strides[-2], strides[-1], G, shape[-2], shape[-1], data, scales,
+        _stream(stream, device)))
     if rc != GEMM_OK:
         raise _error(rc)
     return out
@@ -121,25 +169,26 @@ def dequantize_mx4(q, dtype=torch.bfloat16, out=None, stream=None):
     """The values of an MX4 matrix or stack, each rounded once to dtype
     (float16, bfloat16 or float32).  out: of q's shape, contiguous, or for a
     matrix row-major with any row stride."""
-    if dtype not in FORMATS:
+    fmt, shape, device = FORMATS.get(dtype), q.shape, q.device
+    if fmt is None:
         raise TypeError("dtype must be float16, bfloat16 or float32")
-    if not q.data.is_cuda or min(q.shape) <= 0:
+    if not q.is_cuda or min(shape) <= 0:
         raise ValueError("expected a non-empty MX4 on a GPU")
     if out is None:
-        out = torch.empty(q.shape, dtype=dtype, device=q.device)
-    elif out.dtype != dtype or out.device != q.device or out.shape != q.shape or out.stride(-1) != 1 or \
-            (out.ndim == 3 and not out.is_contiguous()):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    elif out.dtype != dtype or out.device != device or out.shape != shape or \
+            (out.stride(-1) != 1 and shape[-1] > 1) or (len(shape) == 3 and not out.is_contiguous()):
         raise ValueError("out must be of q's shape, of dtype, on its device, with unit column stride "
                          "(a stack contiguous)")
-    if q.ndim == 3 and not (q.data.is_contiguous() and q.scales.is_contiguous()):
-        for i in range(q.shape[0]):
-            dequantize_mx4(q[i], dtype, out[i], stream)
-        return out
-    R = q.shape[0] * q.shape[1] if q.ndim == 3 else q.shape[0]
-    with _device(q.device):
-        rc = lib.gemm_mx4_dequantize(q.data.data_ptr(), q.data.stride(-2), q.scales.data_ptr(),
-                                     q.scales.stride(-2), R, q.K, out.data_ptr(), FORMATS[dtype],
-                                     out.stride(-2), _stream(stream, q.device))
+    R = shape[0]
+    if len(shape) == 3:
+        if not q.is_contiguous():
+            for i in range(R):
+                dequantize_mx4(q[i], dtype, out[i], stream)
+            return out
+        R *= shape[1]
+    rc = _on(device, lambda: lib.gemm_mx4_dequantize(
+        *q._rows(), R, q.K, out.data_ptr(), fmt, out.stride(-2), _stream(stream, device)))
     if rc != GEMM_OK:
         raise _error(rc)
     return out
@@ -163,12 +212,14 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
     shared with a call that may overlap; allocated here when not given."""
     if not isinstance(b, MX4) or b.ndim != 2 or a.ndim != 2:
         raise ValueError("expected a matrix a and an MX4 matrix b [N, K]")
-    if not b.data.is_cuda or a.device != b.device:
+    device = b.device
+    if not b.is_cuda or a.device != device:
         raise ValueError("inputs must share one GPU device")
     (M, K), (N, Kb) = a.shape, b.shape
     if K != Kb or min(M, N, K) <= 0:
         raise ValueError("incompatible or empty shape")
-    if isinstance(a, MX4):
+    quantised = isinstance(a, MX4)
+    if quantised:
         dtype = dtype or torch.float16
         if dtype not in (torch.float16, torch.bfloat16):
             raise TypeError("dtype must be float16 or bfloat16")
@@ -181,26 +232,23 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
         if (a.stride(1) != 1 and K > 1) or a.stride(0) <= 0:
             raise ValueError("a must have unit stride along K and a positive row stride")
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=b.device)
-    elif out.dtype != dtype or out.device != b.device or out.shape != (M, N) or out.stride(1) != 1 or \
-            out.stride(0) < N:
+        out = torch.empty((M, N), dtype=dtype, device=device)
+    elif out.dtype != dtype or out.device != device or out.shape != (M, N) or \
+            (out.stride(1) != 1 and N > 1) or out.stride(0) < N:
         raise ValueError("out must be a row-major [M, N] tensor of the output dtype on the inputs' device")
-    with _device(b.device):
-        if isinstance(a, MX4):
+    fmt, ldc = FORMATS[dtype], out.stride(0)
+    if quantised:
+        if workspace is None:
             need = lib.gemm_mx4_workspace_bytes(M, N, K)
-            if need and workspace is None:
-                with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-                    workspace = torch.empty(need, dtype=torch.uint8, device=b.device)
-            ws, nws = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
-                if workspace is not None else (0, 0)
-            rc = lib.gemm_mx4(a.data.data_ptr(), a.data.stride(0), a.scales.data_ptr(), a.scales.stride(0),
-                              b.data.data_ptr(), b.data.stride(0), b.scales.data_ptr(), b.scales.stride(0),
-                              out.data_ptr(), FORMATS[dtype], out.stride(0), M, N, K,
-                              _stream(stream, b.device), ws, nws)
-        else:
-            rc = lib.gemm_mx4_a16(a.data_ptr(), FORMATS[dtype], a.stride(0), b.data.data_ptr(),
-                                  b.data.stride(0), b.scales.data_ptr(), b.scales.stride(0),
-                                  out.data_ptr(), out.stride(0), M, N, K, _stream(stream, b.device))
+            if need:
+                workspace = _workspace(need, device, stream)
+        ws, nws = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
+            if workspace is not None else (0, 0)
+        rc = _on(device, lambda: lib.gemm_mx4(*a._rows(), *b._rows(), out.data_ptr(), fmt, ldc, M, N, K,
+                                              _stream(stream, device), ws, nws))
+    else:
+        rc = _on(device, lambda: lib.gemm_mx4_a16(a.data_ptr(), fmt, a.stride(0), *b._rows(), out.data_ptr(),
+                                                  ldc, M, N, K, _stream(stream, device)))
     if rc != GEMM_OK:
         raise _error(rc)
     return out
