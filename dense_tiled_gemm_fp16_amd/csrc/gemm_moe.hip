@@ -18,7 +18,10 @@ static_assert(kMoeTokens == GEMM_MOE_MAX_TOKENS && kMoeExperts == GEMM_MOE_MAX_E
 
 namespace {
 
-constexpr int64_t kMaxSize = INT64_C(1) << 30;   // H and I
+constexpr int64_t kMaxH = INT64_C(1) << 30, kMaxI = INT64_C(1) << 20;
+// The kernels reach the rows of an expert's W1, of 32 rows of W2 and of all
+// tokens by 32-bit offsets beside a 64-bit address.
+constexpr int64_t kMaxOffset = (INT64_C(1) << 32) - (INT64_C(1) << 16);
 
 struct Layout {
   int64_t act_row, act_part, tab_e, tab_p, bytes;
@@ -28,7 +31,7 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 bool sizes_ok(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
   return T >= 1 && T <= kMoeTokens && E >= 1 && E <= kMoeExperts && k >= 1 && k <= kMoeTopK && k <= E &&
-         H >= 1 && H <= kMaxSize && I >= 1 && I <= kMaxSize;
+         H >= 1 && H <= kMaxH && I >= 1 && I <= kMaxI;
 }
 
 Layout layout(int64_t T, int64_t k, int64_t I) {
@@ -56,15 +59,32 @@ bool stack(const void* p, int64_t G, int64_t sg, int64_t R, int64_t sr, int64_t 
   return out->hi >= out->lo;
 }
 
+// Shapes of the two kernels: strips of I (NI) and columns of Y (NS) per wave,
+// chunks per group (UC), waves per SIMD that the registers are limited to
+// (WPS).
+template <int WF, int MT>
+struct Shape {
+  static constexpr int NI = 1, UP_UC = 2, UP_WPS = MT == 1 ? 4 : 2;
+  static constexpr int NS = 2, DOWN_UC = 2, DOWN_WPS = MT == 1 ? 4 : 2;
+};
+template <int MT>
+struct Shape<SW_MX4, MT> {
+  static constexpr int NI = MT == 1 ? 2 : 1, UP_UC = MT == 1 ? 2 : 1, UP_WPS = 2;
+  static constexpr int NS = 2, DOWN_UC = 1, DOWN_WPS = 2;
+};
+
 template <int WF, int DT, int MT>
 int launch_kernels(const MoeArgs& a, hipStream_t s) {
+  using P = Shape<WF, MT>;
   MoeArgs copy = a;
   void* p[] = {&copy};
-  const dim3 up((unsigned)cdiv(a.I, 16 * (kMoeWaves / a.parts)), (unsigned)(a.by_pair ? a.T * a.k : a.E));
-  if (hipLaunchKernel((const void*)moe_up_kernel<WF, DT, MT>, up, dim3(64 * kMoeWaves), p, 0, s) != hipSuccess)
+  const dim3 up((unsigned)cdiv(a.I, 16 * P::NI * (kMoeWaves / a.parts)), (unsigned)(a.by_pair ? a.T * a.k : a.E));
+  if (hipLaunchKernel((const void*)moe_up_kernel<WF, DT, MT, P::NI, P::UP_UC, P::UP_WPS>, up, dim3(64 * kMoeWaves),
+                      p, 0, s) != hipSuccess)
     return GEMM_ERR_HIP;
-  const dim3 down((unsigned)cdiv(a.H, 16));
-  if (hipLaunchKernel((const void*)moe_down_kernel<WF, DT, MT>, down, dim3(64 * kMoeWaves), p, 0, s) != hipSuccess)
+  const dim3 down((unsigned)cdiv(a.H, 16 * P::NS));
+  if (hipLaunchKernel((const void*)moe_down_kernel<WF, DT, MT, P::NS, P::DOWN_UC, P::DOWN_WPS>, down,
+                      dim3(64 * kMoeWaves), p, 0, s) != hipSuccess)
     return GEMM_ERR_HIP;
   return GEMM_OK;
 }
@@ -72,7 +92,6 @@ int launch_kernels(const MoeArgs& a, hipStream_t s) {
 template <int WF, int DT>
 int launch_layer(const MoeArgs& a, hipStream_t s) {
   if (a.T <= 16) return launch_kernels<WF, DT, 1>(a, s);
-  if (a.T <= 32) return launch_kernels<WF, DT, 2>(a, s);
   return launch_kernels<WF, DT, 4>(a, s);
 }
 
@@ -114,6 +133,9 @@ int gemm_moe(const gemm_moe_args* g, void* stream, void* workspace, size_t works
   if (g->mx4 && (!stack(g->S1, E, g->s1_e, 2 * I, g->s1_n, hb, &rs1) ||
                  !stack(g->S2, E, g->s2_e, H, g->s2_n, ib, &rs2)))
     return GEMM_ERR_SHAPE;
+  if ((T - 1) * g->ldx > kMaxOffset / 2 || es * g->w1_n > kMaxOffset / (2 * I) || es * g->w2_n > kMaxOffset / 32 ||
+      (g->mx4 && (g->s1_n > kMaxOffset / (2 * I) || g->s2_n > kMaxOffset / 32)))
+    return GEMM_ERR_LAYOUT;
   const Range* in[] = {&rx, &rl, &r1, &r2, &rs1, &rs2};
   for (const Range* r : in)
     if (ranges_overlap(ry.lo, ry.hi, r->lo, r->hi)) return GEMM_ERR_ALIAS;
@@ -150,14 +172,6 @@ int gemm_moe(const gemm_moe_args* g, void* stream, void* workspace, size_t works
   // pair (each finds its expert) instead of by expert.
   a.by_pair = T * g->top_k < E;
   a.renormalize = g->renormalize != 0;
-  // Parts of H per strip: as few as leave every compute unit two workgroups
-  // of distinct work (the device's at most min(E, T top_k) experts in use).
-  int cus = 0;
-  int rc = device_cus(&cus);
-  if (rc) return rc;
-  const int64_t strips = cdiv(I, 16) * std::min(E, T * g->top_k);
-  a.parts = 1;
-  while (a.parts < kMoeWaves && strips * a.parts < (int64_t)2 * cus * kMoeWaves) a.parts *= 2;
 
   hipStream_t s = (hipStream_t)stream;
   void* ws = workspace;
@@ -167,9 +181,16 @@ int gemm_moe(const gemm_moe_args* g, void* stream, void* workspace, size_t works
     for (const Range* r : in)
       if (ranges_overlap(w0, w1, r->lo, r->hi)) return GEMM_ERR_ALIAS;
     if (ranges_overlap(w0, w1, ry.lo, ry.hi)) return GEMM_ERR_ALIAS;
-  } else if (hipMallocAsync(&ws, (size_t)l.bytes, s) != hipSuccess) {
-    return GEMM_ERR_HIP;
   }
+  // Parts of H per strip: as few as leave every compute unit two workgroups
+  // of distinct work (the device's at most min(E, T top_k) experts in use).
+  int cus = 0;
+  int rc = device_cus(&cus);
+  if (rc) return rc;
+  const int64_t strips = cdiv(I, g->mx4 && T <= 16 ? 32 : 16) * std::min(E, T * g->top_k);
+  a.parts = 1;
+  while (a.parts < kMoeWaves && strips * a.parts < (int64_t)2 * cus * kMoeWaves) a.parts *= 2;
+  if (!workspace && hipMallocAsync(&ws, (size_t)l.bytes, s) != hipSuccess) return GEMM_ERR_HIP;
   a.act = (char*)ws;
   a.tab_e = (int32_t*)((char*)ws + l.tab_e);
   a.tab_p = (float*)((char*)ws + l.tab_p);

@@ -66,10 +66,17 @@ int launch_strip(const StripArgs& a, hipStream_t s) {
              &copy, s);
 }
 
+// The strip kernel's lanes reach 64 rows of A and 32 rows of B by 32-bit
+// offsets: row strides of at most 2^26 bytes.
+constexpr int64_t kMaxStripLd = INT64_C(1) << 26;
+bool strip_takes(const StripArgs& a) {
+  return a.lda <= kMaxStripLd && a.ldas <= kMaxStripLd && a.ldb <= kMaxStripLd && a.ldbs <= kMaxStripLd;
+}
+
 template <int XF, int DT>
 int launch_strip_m(const StripArgs& a, hipStream_t s) {
+  if (!strip_takes(a)) return GEMM_ERR_LAYOUT;
   if (a.M <= 16) return launch_strip<XF, DT, 1, 1, 2, 8>(a, s);
-  if (a.M <= 32) return launch_strip<XF, DT, 1, 2, 2, 8>(a, s);
   return launch_strip<XF, DT, 2, 4, 1, 8>(a, s);
 }
 

@@ -68,8 +68,8 @@ __device__ __forceinline__ uint32_t logit_key(float l) {
 }
 __device__ __forceinline__ float load_logit(const MoeArgs& a, int t, int e) {
   const int64_t i = t * a.ldl + e;
-  if (a.fmt_l == 2) return ((const float*)a.logits)[i];
-  const uint16_t h = ((const uint16_t*)a.logits)[i];
+  if (a.fmt_l == 2) return gload<float>((const float*)a.logits + i);
+  const uint16_t h = gload<uint16_t>((const uint16_t*)a.logits + i);
   return a.fmt_l == 0 ? cvt_in<DT_F16>(h) : cvt_in<DT_BF16>(h);
 }
 
@@ -119,77 +119,89 @@ __device__ __forceinline__ void split_parts(float v, uint16_t& hi, uint16_t& lo)
   lo = cvt_out<DT>(r == r && fabsf(r) <= fabsf(v) ? r : 0.0f);   // nothing beside an infinity or a NaN
 }
 
-template <int MT>
-struct MoeUpShared {
-  union {
-    f32x4 part[kMoeWaves * 2 * MT * 64];
-    uint32_t key[kMoeExperts];
-  };
-  int rank[kMoeTokens];     // slot of the expert in the token's choice, -1 not chosen
-  int list[kMoeTokens];     // the expert's tokens
-  int count, found;
-};
+// What a wave of moe_up takes: NI strips of 16 rows of I (gate and up: 2 NI
+// strips of W1), UC chunks at a time.
+template <int WF, int DT, int MT, int NI_, int UC>
+struct MoeUp {
+  static constexpr int NI = NI_;
+  using S = Strip<WF, DT == DT_F16 ? SX_F16 : SX_BF16, 2 * NI, MT, UC>;
+  static constexpr int TILES = 2 * NI * MT;
 
-template <int WF, int DT, int MT, int UC>
-__device__ __forceinline__ void moe_up_tiles(const MoeArgs& a, MoeUpShared<MT>& sh, int e, int lane, int wave) {
-  using S = Strip<WF, DT == DT_F16 ? SX_F16 : SX_BF16, 2, MT, UC>;
-  constexpr int TILES = 2 * MT;
-  const int m = __builtin_amdgcn_readfirstlane(sh.count), tiles = (m + 15) / 16;
-  const int strips = kMoeWaves / a.parts;      // of this workgroup
-  const int strip = wave / a.parts, part = wave - strip * a.parts;
-  const int64_t i0 = ((int64_t)blockIdx.x * strips + strip) * 16;
-  if (i0 < a.I) {
-    typename S::WPtr w;
-    typename S::XPtr x;
-    x.part = 0;
-    int64_t row = i0 + (lane & 15);
-    if (row >= a.I) row = a.I - 1;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      w.w[h] = a.w1 + e * a.w1_e + (h * a.I + row) * a.w1_n;
-      w.s[h] = a.s1 + e * a.s1_e + (h * a.I + row) * a.s1_n;
-    }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int p = 16 * t + (lane & 15);
-      x.x[t] = a.x + sh.list[p < m ? p : m - 1] * a.ldx;
-      x.s[t] = nullptr;
-    }
-    f32x4 acc[2][MT];
+  struct Shared {
+    union {
+      char wave[kMoeWaves][S::LDS];
+      f32x4 part[kMoeWaves * TILES * 64];
+      uint32_t key[kMoeExperts];
+    };
+    int rank[kMoeTokens];     // slot of the expert in the token's choice, -1 not chosen
+    int list[kMoeTokens];     // the expert's tokens
+    int count, found;
+  };
+
+  static __device__ __forceinline__ void run(const MoeArgs& a, Shared& sh, int e, int lane, int wave) {
+    const int m = __builtin_amdgcn_readfirstlane(sh.count), tiles = (m + 15) / 16;
+    const int strips = kMoeWaves / a.parts;      // of this workgroup
+    const int strip = wave / a.parts, part = wave - strip * a.parts;
+    const int64_t i0 = ((int64_t)blockIdx.x * strips + strip) * (16 * NI);
+    f32x4 acc[2 * NI][MT];
     S::clear(acc);
-    const int64_t nc = S::chunks(a.H);
-    S::run(acc, w, x, nc * part / a.parts, nc * (part + 1) / a.parts, a.H, lane >> 4, tiles == 1);
+    if (i0 < a.I) {
+      const typename S::WPtr w{a.w1 + e * a.w1_e + i0 * a.w1_n, a.s1 + e * a.s1_e + i0 * a.s1_n};
+      typename S::WOff wo;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+          int64_t row = 16 * n + (lane >> 2), srow = 16 * n + (lane < 16 ? lane : 0);
+          if (row >= a.I - i0) row = a.I - i0 - 1;
+          if (srow >= a.I - i0) srow = a.I - i0 - 1;
+          wo.w[h * NI + n] = (uint32_t)((h * a.I + row) * a.w1_n) + 16 * (lane & 3);
+          wo.s[h * NI + n] = (uint32_t)((h * a.I + srow) * a.s1_n);
+        }
+      auto rows = [&](int t) {
+        const int p = 16 * t + (lane >> 2);
+        typename S::XPtr x;
+        x.x = a.x;
+        x.xo = (uint32_t)(sh.list[p < m ? p : m - 1] * a.ldx) + 16 * (lane & 3);
+        x.s = nullptr;
+        x.so = 0;
+        return x;
+      };
+      S::run(acc, sh.wave[wave], w, wo, rows, 0, part, a.parts, a.H, tiles, lane);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2 * NI; ++h)
 #pragma unroll
       for (int t = 0; t < MT; ++t) sh.part[(wave * TILES + h * MT + t) * 64 + lane] = acc[h][t];
-  }
-  __syncthreads();
-  for (int j = wave; j < strips * tiles; j += kMoeWaves) {
-    const int s = j / tiles, t = j - s * tiles;
-    const f32x4* base = sh.part + s * a.parts * TILES * 64 + t * 64;
-    const int p = 16 * t + (lane & 15);
-    const int64_t i = ((int64_t)blockIdx.x * strips + s) * 16 + 4 * (lane >> 4);
-    if (p < m && i < a.I) {       // rows hold a multiple of 8 values: all four fit
-      const f32x4 gate = sum_waves(base, TILES * 64, a.parts, lane);
-      const f32x4 up = sum_waves(base + MT * 64, TILES * 64, a.parts, lane);
-      const int token = sh.list[p];
-      uint16_t hi[4], lo[4];
+    __syncthreads();
+    for (int j = wave; j < strips * NI * tiles; j += kMoeWaves) {
+      const int t = j % tiles, n = j / tiles % NI, s = j / (tiles * NI);
+      const f32x4* base = sh.part + s * a.parts * TILES * 64 + (n * MT + t) * 64;
+      const int p = 16 * t + (lane & 15);
+      const int64_t i = (((int64_t)blockIdx.x * strips + s) * NI + n) * 16 + 4 * (lane >> 4);
+      if (p < m && i < a.I) {       // rows hold a multiple of 8 values: all four fit
+        const f32x4 gate = sum_waves(base, TILES * 64, a.parts, lane);
+        const f32x4 up = sum_waves(base + NI * MT * 64, TILES * 64, a.parts, lane);
+        const int token = sh.list[p];
+        uint16_t hi[4], lo[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        split_parts<WF == SW_F16>(gate[r] / (1.0f + expf(-gate[r])) * up[r], hi[r], lo[r]);
-      char* q = a.act + (token * a.k + sh.rank[token]) * a.act_row + 2 * i;
-      __builtin_memcpy(q, hi, 8);
-      __builtin_memcpy(q + a.act_part, lo, 8);
+        for (int r = 0; r < 4; ++r)
+          split_parts<WF == SW_F16>(gate[r] / (1.0f + expf(-gate[r])) * up[r], hi[r], lo[r]);
+        char* q = a.act + (token * a.k + sh.rank[token]) * a.act_row + 2 * i;
+        gstore(q, u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16});
+        gstore(q + a.act_part, u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16});
+      }
     }
   }
-}
+};
 
-// Grid (groups of strips of 16 rows of I, experts or pairs).  DT: format of X;
-// MT: tiles of 16 tokens that T needs.
-template <int WF, int DT, int MT>
-__global__ __launch_bounds__(64 * kMoeWaves, MT < 2 ? 4 : 2) void moe_up_kernel(MoeArgs a) {
-  __shared__ MoeUpShared<MT> sh;
+// Grid (groups of strips of rows of I, experts or pairs).  DT: format of X; MT:
+// tiles of 16 tokens that T needs.
+template <int WF, int DT, int MT, int NI, int UC, int WPS>
+__global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_up_kernel(MoeArgs a) {
+  using U = MoeUp<WF, DT, MT, NI, UC>;
+  __shared__ typename U::Shared sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slot = blockIdx.y;
   int e = slot;
@@ -248,26 +260,36 @@ __global__ __launch_bounds__(64 * kMoeWaves, MT < 2 ? 4 : 2) void moe_up_kernel(
       }
     }
   }
-  moe_up_tiles<WF, DT, MT, WF == SW_MX4 ? (MT == 4 ? 1 : 2) : (MT == 4 ? 2 : 4)>(a, sh, e, lane, wave);
+  U::run(a, sh, e, lane, wave);
 }
 
-template <int MT>
-struct MoeDownShared {
-  float own[kMoeWaves][16 * MT][16];
-  uint32_t mask[kMoeExperts][2];     // tokens of an expert
-  uint16_t active[kMoeExperts], place[kMoeExperts];
-  uint16_t start[kMoeExperts + 1];
-  uint32_t rows[16 * MT * kMoeTopK];   // token << 16 | pair, by expert
-  int32_t expert[16 * MT * kMoeTopK];
-  float prob[16 * MT * kMoeTopK];
-  int n_active;
+// What a workgroup of moe_down takes: NS strips of 16 columns of Y.
+template <int WF, int MT, int NS_, int UC>
+struct MoeDown {
+  static constexpr int NS = NS_;
+  using S = Strip<WF, WF == SW_F16 ? SX_F16P : SX_BF16P, NS, MT, UC>;
+  static constexpr int kPairs = 16 * MT * kMoeTopK;
+
+  struct Shared {
+    char wave[kMoeWaves][S::LDS];
+    float own[kMoeWaves][16 * MT][16 * NS];
+    uint32_t mask[kMoeExperts][2];     // tokens of an expert
+    uint16_t active[kMoeExperts], place[kMoeExperts];
+    uint16_t start[kMoeExperts + 1];
+    uint32_t rows[kPairs];             // token << 16 | pair, by expert
+    int32_t expert[kPairs];
+    float prob[kPairs];
+    int n_active;
+  };
 };
 
-template <int WF, int DT, int MT>
-__global__ __launch_bounds__(64 * kMoeWaves, MT < 2 ? 4 : 2) void moe_down_kernel(MoeArgs a) {
-  __shared__ MoeDownShared<MT> sh;
+template <int WF, int DT, int MT, int NS, int UC, int WPS>
+__global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a) {
+  using D = MoeDown<WF, MT, NS, UC>;
+  using S = typename D::S;
+  constexpr int kPairs = D::kPairs;
+  __shared__ typename D::Shared sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  constexpr int kPairs = 16 * MT * kMoeTopK;
   constexpr int NT = 64 * kMoeWaves;
   const int pairs = a.T * a.k;
   for (int i = tid; i < a.E; i += NT) sh.mask[i][0] = sh.mask[i][1] = 0;
@@ -275,7 +297,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, MT < 2 ? 4 : 2) void moe_down_kerne
     sh.expert[i] = a.tab_e[i];
     sh.prob[i] = a.tab_p[i];
   }
-  for (int i = lane; i < a.T * 16; i += 64) sh.own[wave][i / 16][i % 16] = 0.0f;
+  for (int i = lane; i < a.T * (16 * NS); i += 64) sh.own[wave][i / (16 * NS)][i % (16 * NS)] = 0.0f;
   __syncthreads();
   for (int i = tid; i < pairs; i += NT) {
     const int t = i / a.k;
@@ -333,91 +355,91 @@ __global__ __launch_bounds__(64 * kMoeWaves, MT < 2 ? 4 : 2) void moe_down_kerne
   }
   __syncthreads();
 
-  // This wave's share of the (expert, chunk) sequence, by groups of chunks of
-  // one expert; the weights of the next group load while a group's are
-  // multiplied, across experts too.
-  constexpr int UC = WF == SW_MX4 ? (MT == 1 ? 2 : 1) : (MT == 4 ? 2 : 4);
-  using S = Strip<WF, WF == SW_F16 ? SX_F16P : SX_BF16P, 1, MT, UC>;
-  const int64_t h0 = (int64_t)blockIdx.x * 16;
-  const int g = lane >> 4;
-  const int cpe = (int)S::chunks(a.I), n = __builtin_amdgcn_readfirstlane(sh.n_active);
-  const int64_t units = (int64_t)n * cpe;
-  const int64_t u0 = units * wave / kMoeWaves, u1 = units * (wave + 1) / kMoeWaves;
-  int64_t row = h0 + (lane & 15);
-  if (row >= a.H) row = a.H - 1;
-  const char* const w_row = a.w2 + row * a.w2_n;
-  const uint8_t* const s_row = a.s2 + row * a.s2_n;
-  auto weights = [&](int i) {
-    const int64_t e = __builtin_amdgcn_readfirstlane(sh.active[i]);
-    typename S::WPtr p;
-    p.w[0] = w_row + e * a.w2_e;
-    p.s[0] = s_row + e * a.s2_e;
-    return p;
+  // The whole groups of chunks of all experts, dealt to the waves in turn (a
+  // row's neighbouring pieces are then read at about the same time), loads
+  // running ahead across experts; then the partial groups, if I has one.
+  const int64_t h0 = (int64_t)blockIdx.x * (16 * NS);
+  const int n = __builtin_amdgcn_readfirstlane(sh.n_active);
+  struct Cursor {
+    const MoeArgs* a;
+    const typename D::Shared* sh;
+    int64_t h0;
+    int i, n, g, gpe, first, m, lane;     // group g of gpe of expert i of n
+    __device__ __forceinline__ void at_expert() {
+      while (g >= gpe && i < n) {
+        g -= gpe;
+        ++i;
+      }
+      if (i < n) {
+        first = __builtin_amdgcn_readfirstlane(sh->start[i]);
+        m = __builtin_amdgcn_readfirstlane(sh->start[i + 1]) - first;
+      }
+    }
+    __device__ __forceinline__ bool more() const { return i < n; }
+    __device__ __forceinline__ bool last() const { return g + kMoeWaves >= gpe; }   // of the wave's, in an expert
+    __device__ __forceinline__ void next() {
+      g += kMoeWaves;
+      at_expert();
+    }
+    __device__ __forceinline__ int64_t c() const { return (int64_t)g * S::UC; }
+    __device__ __forceinline__ typename S::WPtr w() const {
+      const int64_t e = __builtin_amdgcn_readfirstlane(sh->active[i]);
+      return {a->w2 + e * a->w2_e + h0 * a->w2_n, a->s2 + e * a->s2_e + h0 * a->s2_n};
+    }
+    __device__ __forceinline__ typename S::XPtr x(int t) const {
+      const int p = 16 * t + (lane >> 2);
+      typename S::XPtr x;
+      x.x = a->act;
+      x.xo = (sh->rows[first + (p < m ? p : m - 1)] & 0xFFFFu) * (uint32_t)a->act_row + 16 * (lane & 3);
+      x.s = nullptr;
+      x.so = 0;
+      return x;
+    }
+    __device__ __forceinline__ int tiles() const { return (m + 15) / 16; }
   };
-  if (u0 < u1) {
-    int i = (int)(u0 / cpe), c = (int)(u0 - (int64_t)i * cpe);
-    int64_t left = u1 - u0;                                  // chunks from (i, c) on
-    int end = left < cpe - c ? c + (int)left : cpe;          // of this wave, in expert i
-    typename S::WPtr wp = weights(i);
-    typename S::XPtr xp;
-    xp.part = a.act_part;
-    typename S::WBuf cur, nxt;
-    typename S::XBuf x;
-    uint32_t who[MT];
-    int m = 0;
-    f32x4 acc[1][MT];
+  {
+    char* const lds = sh.wave[wave];
+    const typename S::WOff wo = S::offsets(a.H - h0, 16, a.w2_n, a.s2_n, lane);
+    const int gpe = (int)S::groups(a.I);
+    f32x4 acc[NS][MT];
     S::clear(acc);
-    bool fresh = true;
-    S::load_w(cur, wp, c, end, a.I, g);
-    while (true) {
-      if (fresh) {                                           // rows of the expert's tokens
-        const int first = __builtin_amdgcn_readfirstlane(sh.start[i]);
-        m = __builtin_amdgcn_readfirstlane(sh.start[i + 1]) - first;
+    // p times an expert's sums into the wave's accumulators.
+    auto add = [&](const Cursor& cc) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          const int p = 16 * t + (lane & 15);
-          who[t] = sh.rows[first + (p < m ? p : m - 1)];
-          xp.x[t] = a.act + (int64_t)(who[t] & 0xFFFFu) * a.act_row;
-          xp.s[t] = nullptr;
-        }
-        fresh = false;
-      }
-      S::load_x(x, xp, c, end, a.I, g, m <= 16);
-      // The next group: of this expert, or of the next one.
-      const bool last_of_expert = c + UC >= end;
-      const int64_t left_after = last_of_expert ? left - (end - c) : left - UC;
-      const bool more = left_after > 0;
-      const int i2 = last_of_expert ? i + 1 : i, c2 = last_of_expert ? 0 : c + UC;
-      const int end2 = !last_of_expert ? end : (left_after < cpe ? (int)left_after : cpe);
-      if (more) {
-        if (last_of_expert) wp = weights(i2);
-        S::load_w(nxt, wp, c2, end2, a.I, g);
-      }
-      S::mma(acc, cur, x, m <= 16);
-      if (last_of_expert) {
+      for (int t = 0; t < MT; ++t) {
+        const int p = 16 * t + (lane & 15);
+        if (p < cc.m) {
+          const uint32_t who = sh.rows[cc.first + p];
+          const float prob = sh.prob[who & 0xFFFFu];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          if (16 * t + (lane & 15) < m) {
-            const float p = sh.prob[who[t] & 0xFFFFu];
-            float* q = &sh.own[wave][who[t] >> 16][4 * g];
+          for (int s = 0; s < NS; ++s) {
+            float* q = &sh.own[wave][who >> 16][16 * s + 4 * (lane >> 4)];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) q[r] += p * acc[0][t][r];
+            for (int r = 0; r < 4; ++r) q[r] += prob * acc[s][t][r];
           }
         }
-        S::clear(acc);
-        fresh = true;
       }
-      if (!more) break;
-      cur = nxt;
-      i = i2;
-      c = c2;
-      end = end2;
-      left = left_after;
+      S::clear(acc);
+    };
+    if (gpe > 0) {
+      Cursor cur{&a, &sh, h0, 0, n, wave, gpe, 0, 0, lane};
+      cur.at_expert();
+      S::stream(acc, lds, cur, wo, a.act_part, a.I, lane, [&](const Cursor& cc) {
+        if (cc.last()) add(cc);
+      });
     }
+    if (S::rest(a.I))
+      for (int i = wave; i < n; i += kMoeWaves) {
+        Cursor cur{&a, &sh, h0, i, n, 0, gpe + 1, 0, 0, lane};
+        cur.at_expert();
+        cur.g = gpe;
+        S::finish(acc, lds, cur, wo, a.act_part, a.I, lane);
+        add(cur);
+      }
   }
   __syncthreads();
-  for (int i = tid; i < a.T * 4; i += NT) {
-    const int t = i >> 2, g = i & 3;
+  for (int i = tid; i < a.T * (4 * NS); i += NT) {
+    const int t = i / (4 * NS), g = i % (4 * NS);
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < kMoeWaves; ++w)
@@ -429,9 +451,9 @@ __global__ __launch_bounds__(64 * kMoeWaves, MT < 2 ? 4 : 2) void moe_down_kerne
 #pragma unroll
     for (int r = 0; r < 4; ++r) o[r] = cvt_out<DT>(s[r]);
     if (h + 4 <= a.H) {
-      __builtin_memcpy(y, o, 8);
+      gstore(y, u32x2{o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16});
     } else {
-      for (int r = 0; r < 4 && h + r < a.H; ++r) y[r] = o[r];
+      for (int r = 0; r < 4 && h + r < a.H; ++r) gstore<uint16_t>(y + r, o[r]);
     }
   }
 }

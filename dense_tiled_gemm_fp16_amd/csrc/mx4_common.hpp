@@ -21,14 +21,39 @@ constexpr int kMxBytes = 16;    // their codes
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// 16 bytes at any alignment: one global_load_dwordx4 (the hardware takes
-// unaligned addresses; aligned ones cost nothing extra).
-__device__ __forceinline__ u32x4 load16(const void* p) {
-  u32x4 v;
-  __builtin_memcpy(&v, p, 16);
-  return v;
+// Loads and stores of global memory at any alignment (the hardware takes
+// unaligned addresses; aligned ones cost nothing extra).  The address space is
+// named, because a pointer that went through integers or structures is taken
+// for a generic one: a flat instruction then also counts with the LDS, and
+// every wait for an LDS read waits for all loads in flight.
+#define GEMM_GLOBAL __attribute__((address_space(1)))
+template <class T>
+__device__ __forceinline__ T gload(const void* p) {
+  typedef T Any __attribute__((aligned(1)));
+  return *(const GEMM_GLOBAL Any*)p;
 }
-__device__ __forceinline__ void store16(void* p, u32x4 v) { __builtin_memcpy(p, &v, 16); }
+template <class T>
+__device__ __forceinline__ void gstore(void* p, T v) {
+  typedef T Any __attribute__((aligned(1)));
+  *(GEMM_GLOBAL Any*)p = v;
+}
+__device__ __forceinline__ u32x4 load16(const void* p) { return gload<u32x4>(p); }
+__device__ __forceinline__ void store16(void* p, u32x4 v) { gstore<u32x4>(p, v); }
+
+// n (1, 2 or 4) dwords.
+template <int N>
+__device__ __forceinline__ void load_dwords(uint32_t (&d)[N], const void* p) {
+  if constexpr (N == 4) {
+    const u32x4 v = gload<u32x4>(p);
+    d[0] = v[0]; d[1] = v[1]; d[2] = v[2]; d[3] = v[3];
+  } else if constexpr (N == 2) {
+    const u32x2 v = gload<u32x2>(p);
+    d[0] = v[0]; d[1] = v[1];
+  } else {
+    static_assert(N == 1, "1, 2 or 4");
+    d[0] = gload<uint32_t>(p);
+  }
+}
 
 // A scale byte as the float whose exponent the converts use.
 __device__ __forceinline__ float scale_f32(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }

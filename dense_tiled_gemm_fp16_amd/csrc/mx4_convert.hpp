@@ -71,7 +71,7 @@ struct Oct {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       typename MxElem<FMT>::type e = 0;
-      if (i < n) __builtin_memcpy(&e, p + i * ES, ES);
+      if (i < n) e = gload<typename MxElem<FMT>::type>(p + i * ES);
       h[i] = e;
     }
     if constexpr (FMT == MX_F32) {
@@ -159,8 +159,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
     m = n > m ? n : m;
     const uint32_t s = scale_of(m);
     if (mine && u < nu && o < octs) {
-      *(uint32_t*)(a.data + (row * octs + o) * 4) = to_codes(f, s);
-      if ((o & 3) == 0) a.scales[row * a.Kb + (o >> 2)] = (uint8_t)s;
+      gstore(a.data + (row * octs + o) * 4, to_codes(f, s));
+      if ((o & 3) == 0) gstore<uint8_t>(a.scales + row * a.Kb + (o >> 2), (uint8_t)s);
     }
   }
 }
@@ -181,10 +181,10 @@ __global__ __launch_bounds__(256) void quantize_columns_kernel(QuantArgs a) {
   E e[32];
   if (n == 32) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) e[i] = p[i * a.s_k];
+    for (int i = 0; i < 32; ++i) e[i] = gload<E>(p + i * a.s_k);
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) e[i] = i < n ? p[i * a.s_k] : (E)0;
+    for (int i = 0; i < 32; ++i) e[i] = i < n ? gload<E>(p + i * a.s_k) : (E)0;
   }
   uint32_t m = 0;
 #pragma unroll
@@ -201,8 +201,8 @@ __global__ __launch_bounds__(256) void quantize_columns_kernel(QuantArgs a) {
     for (int i = 0; i < 8; ++i) f[i] = mx_in<FMT>(e[8 * j + i]);
     out[j] = to_codes(f, s);
   }
-  *(u32x4*)(a.data + (row * a.Kb + b) * kMxBytes) = out;
-  a.scales[row * a.Kb + b] = (uint8_t)s;
+  store16(a.data + (row * a.Kb + b) * kMxBytes, out);
+  gstore<uint8_t>(a.scales + row * a.Kb + b, (uint8_t)s);
 }
 
 struct DequantArgs {
@@ -243,8 +243,8 @@ __global__ __launch_bounds__(256) void dequantize_kernel(DequantArgs a) {
     const int64_t o = o0 + 64 * u;
     const bool ok = mine && u < nu && o < octs;
     c[u] = 0;
-    if (ok) __builtin_memcpy(&c[u], d + 4 * o, 4);
-    s[u] = ok ? sc[o >> 2] : 127;
+    if (ok) c[u] = gload<uint32_t>(d + 4 * o);
+    s[u] = ok ? gload<uint8_t>(sc + (o >> 2)) : 127;
   }
 #pragma unroll
   for (int u = 0; u < kQuantU; ++u) {
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel(DequantArgs a) {
       if (left >= 8) {
         store16(q, v);
       } else {
-        for (int i = 0; i < left; ++i) ((uint16_t*)q)[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+        for (int i = 0; i < left; ++i) gstore<uint16_t>((uint16_t*)q + i, (uint16_t)(v[i / 2] >> (16 * (i & 1))));
       }
     } else {
       // through bfloat16 (exact) and float (exact) to the output's rounding
@@ -268,11 +268,10 @@ __global__ __launch_bounds__(256) void dequantize_kernel(DequantArgs a) {
       for (int i = 0; i < 8; ++i) e[i] = (float)b[i];
       if constexpr (FMT == MX_F32) {
         if (left >= 8) {
-          float4 lo = {e[0], e[1], e[2], e[3]}, hi = {e[4], e[5], e[6], e[7]};
-          __builtin_memcpy(q, &lo, 16);
-          __builtin_memcpy(q + 16, &hi, 16);
+          gstore(q, f32x4{e[0], e[1], e[2], e[3]});
+          gstore(q + 16, f32x4{e[4], e[5], e[6], e[7]});
         } else {
-          for (int i = 0; i < left; ++i) ((float*)q)[i] = e[i];
+          for (int i = 0; i < left; ++i) gstore<float>((float*)q + i, e[i]);
         }
       } else {
         uint32_t h[4];
@@ -282,7 +281,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel(DequantArgs a) {
         if (left >= 8) {
           store16(q, u32x4{h[0], h[1], h[2], h[3]});
         } else {
-          for (int i = 0; i < left; ++i) ((uint16_t*)q)[i] = (uint16_t)(h[i / 2] >> (16 * (i & 1)));
+          for (int i = 0; i < left; ++i) gstore<uint16_t>((uint16_t*)q + i, (uint16_t)(h[i / 2] >> (16 * (i & 1))));
         }
       }
     }

@@ -3,23 +3,31 @@
 //
 // With few rows the time goes to reading the weights once, so the loop is
 // built around those loads: a wave owns NS strips of 16 weight rows and a
-// range of K, loads the weights 16 bytes per lane straight into registers (no
-// LDS: no other wave of the workgroup wants them), the loads of the next UC
-// chunks in flight while this one's are multiplied, and the waves of a
-// workgroup, which share the strips and split K, add their sums through LDS at
-// the end.  The few rows of A come from L1/L2.
+// range of K and keeps the weights of two groups of UC chunks (64 bytes per
+// row each) in flight beside the group that it multiplies; waves that share
+// strips and split K add their sums through LDS at the end.  The few rows of A
+// come from L2 the same way, one group ahead.  Loads return in order, so a
+// group's A is issued before the weights of the group after it: waiting for
+// the former then leaves the latter in flight.
 //
 // The matrix instruction is 16 x 16 (k 32, or 128 for MX4 x MX4), its first
-// operand the weights: lane l holds weight row l % 16 and, of each chunk, the
-// k octet or block l / 16; the sums land as weight rows 4 (l / 16) + r of
-// column (row of A) l % 16.  Only the order of k is free, as long as both
-// operands share it:
-//   16-bit weights   a chunk is 32 k; lane group g takes octet g (16 bytes).
-//   MX4 weights      a chunk is 128 k, 64 bytes of a row; lane group g takes
-//                    block g (16 bytes, one scale).  With a 16-bit A dword j
-//                    of the block meets octet 4 g + j of the chunk in the
-//                    j-th of four instructions; with an MX4 A one scaled
-//                    128-k instruction takes the chunk.
+// operand the weights: lane l holds weight row l % 16 and k octet or block
+// l / 16; the sums land as weight rows 4 (l / 16) + r of column (row of A)
+// l % 16.  Loaded in that arrangement, every four neighbouring lanes touch four
+// rows, and the address unit takes 64 cycles for a 1 KiB load instruction; four
+// lanes on the 64 bytes of one row take 16 (both measured).  So lane l loads
+// piece l % 4 of row l / 4, and the pieces change lanes through a part of LDS
+// that belongs to the wave: written and read in the wave's own order, without
+// barriers.  Piece p of row r lies in slot p ^ fa(r) of its 64 bytes, which
+// keeps both sides free of bank conflicts.
+//
+// Only the order of k is free, as long as both operands share it:
+//   16-bit weights   a chunk is 32 k; lane group g takes octet g.
+//   MX4 weights      a chunk is 128 k; lane group g takes block g (16 bytes,
+//                    one scale).  With a 16-bit A, dword j of the block meets
+//                    octet 4 g + j of the chunk in the j-th of four
+//                    instructions; with an MX4 A one scaled 128-k instruction
+//                    takes the chunk.
 //
 // Weights in MX4 are widened exactly: to bfloat16 at any scale; to binary16,
 // for a binary16 A, where the scale byte is in 104 .. 140 (or below 61, where
@@ -31,6 +39,7 @@
 // enters as zero on both sides.
 #pragma once
 
+#include "dma_a128_kernel.hpp"
 #include "mx4_common.hpp"
 
 namespace gemmf16 {
@@ -51,11 +60,13 @@ __device__ __forceinline__ T as8(u32x4 v) {
   return __builtin_bit_cast(T, v);
 }
 
-// Elements k .. k+7 of a 16-bit row, zero from K on.
-__device__ __forceinline__ u32x4 load8_tail(const char* row, int64_t k, int64_t K) {
-  if (k + 8 <= K) return load16(row + 2 * k);
-  const int64_t n = K - k;
-  return load_partial8((const uint16_t*)row + (n > 0 ? k : 0), 1, n > 0 ? (int)n : 0);
+// The first n of the eight 16-bit elements at p, the others zero.
+__device__ __forceinline__ u32x4 load8_rest(const char* p, int64_t n) {
+  if (n >= 8) return load16(p);
+  uint32_t h[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h[e] = e < n ? (uint32_t)gload<uint16_t>(p + 2 * e) : 0u;
+  return u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
 }
 
 // Wait states after matrix instructions, tied to their sums.  The compiler
@@ -63,10 +74,16 @@ __device__ __forceinline__ u32x4 load8_tail(const char* row, int64_t k, int64_t 
 // a basic block, but leaves them out where the reader, often only a register
 // move, is the first of the next block: a group's sums pass through here
 // before any branch.  (16 states; the longest instruction here needs 12.)
-__device__ __forceinline__ void settle(f32x4 (&a)[1]) { asm volatile("s_nop 15" : "+v"(a[0])); }
-__device__ __forceinline__ void settle(f32x4 (&a)[2]) { asm volatile("s_nop 15" : "+v"(a[0]), "+v"(a[1])); }
-__device__ __forceinline__ void settle(f32x4 (&a)[4]) {
-  asm volatile("s_nop 15" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
+template <int N, int MT>
+__device__ __forceinline__ void settle(f32x4 (&a)[N][MT], int t) {
+  if constexpr (N == 1) {
+    asm volatile("s_nop 15" : "+v"(a[0][t]));
+  } else if constexpr (N == 2) {
+    asm volatile("s_nop 15" : "+v"(a[0][t]), "+v"(a[1][t]));
+  } else {
+    static_assert(N == 4, "strips of a wave");
+    asm volatile("s_nop 15" : "+v"(a[0][t]), "+v"(a[1][t]), "+v"(a[2][t]), "+v"(a[3][t]));
+  }
 }
 
 // binary16 -> two bfloat16 parts, exactly: 11 significant bits as 8 + 3.
@@ -80,33 +97,65 @@ __device__ __forceinline__ void split_bf16(f16x8 x, bf16x8& hi, bf16x8& lo) {
   }
 }
 
+// Order of one wave's LDS accesses: the hardware keeps it, the compiler has to
+// be told that lanes read what other lanes wrote.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // NS strips of 16 weight rows x MT tiles of 16 rows of A, UC chunks at a time.
-// `g` is the lane's group, lane / 16.
 template <int WF, int XF, int NS_, int MT_, int UC_>
 struct Strip {
   static constexpr int NS = NS_, MT = MT_, UC = UC_;
   static constexpr bool W4 = WF == SW_MX4, X4 = XF == SX_MX4;
   static constexpr int PL = (XF == SX_F16P || XF == SX_BF16P) ? 2 : 1;
   static constexpr int CK = W4 ? 128 : 32;                  // k per chunk
-  static constexpr int XV = X4 ? 1 : (W4 ? 4 : 1);          // 16-byte A loads per chunk and part
+  static constexpr int XV = X4 ? 1 : (W4 ? 4 : 1);          // 64-byte pieces of A per chunk, row and part
   static_assert(W4 || !X4, "MX4 A takes MX4 weights");
+  // A wave's LDS: the group's weights, one chunk of one part of A, scales.
+  static constexpr int X_AT = UC * NS * 1024, S_AT = X_AT + XV * 1024, XS_AT = S_AT + (W4 ? NS * 16 * UC * 4 : 0);
+  static constexpr int LDS = XS_AT + (X4 ? 16 * UC * 4 : 0);
 
+  // A uniform address and the lane's 32-bit offset beside it, so that moving
+  // along K or to another expert is scalar arithmetic.
   struct WPtr {
-    const char* w[NS];        // this lane's weight rows
-    const uint8_t* s[NS];     // their scales (MX4)
+    const char* w;            // the strips' first row
+    const uint8_t* s;         // its scales (MX4)
+  };
+  struct WOff {
+    uint32_t w[NS];           // row lane / 4 of each strip, piece lane % 4
+    uint32_t s[NS];           // scales of row lane for lanes 0 .. 15, of row 0 for the others (MX4)
   };
   struct XPtr {
-    const char* x[MT];        // this lane's rows of A
-    const uint8_t* s[MT];     // their scales (MX4)
-    int64_t part;             // bytes to the second part's rows
+    const char* x;            // uniform, as for the weights
+    const uint8_t* s;
+    uint32_t xo;              // row lane / 4 of a tile, piece lane % 4
+    uint32_t so;              // scales of row lane % 16 (MX4 A)
   };
-  struct WBuf {
-    u32x4 v[UC][NS];
-    uint32_t s[UC][NS];
+
+  // Offsets of strips that start `stride` rows apart, `rows` rows from the
+  // first strip's first one on existing.
+  static __device__ __forceinline__ WOff offsets(int64_t rows, int64_t stride, int64_t ld, int64_t lds, int lane) {
+    WOff o;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      int64_t r = i * stride + (lane >> 2), q = i * stride + (lane < 16 ? lane : 0);
+      if (r >= rows) r = rows - 1;
+      if (q >= rows) q = rows - 1;
+      o.w[i] = (uint32_t)(r * ld) + 16 * (lane & 3);
+      o.s[i] = (uint32_t)(q * lds);
+    }
+    return o;
+  }
+
+  struct WRegs {
+    u32x4 w[UC][NS];
+    uint32_t s[NS][UC];
   };
-  struct XBuf {
-    u32x4 v[UC][MT][PL][XV];
-    uint32_t s[UC][MT];
+  struct XRegs {
+    u32x4 x[UC][PL][XV];
+    uint32_t xs[UC];
   };
 
   static __device__ __forceinline__ int64_t chunks(int64_t K) { return (K + CK - 1) / CK; }
@@ -118,207 +167,337 @@ struct Strip {
       for (int t = 0; t < MT; ++t) acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // A whole group: all its chunks exist and end by K.
-  static __device__ __forceinline__ bool whole(int64_t c, int64_t end, int64_t K) {
-    return c + UC <= end && (c + UC) * CK <= K;
+  // Whole groups of a row of K, and whether chunks are left behind them.
+  static __device__ __forceinline__ int64_t groups(int64_t K) { return K / (UC * CK); }
+  static __device__ __forceinline__ bool rest(int64_t K) { return K % (UC * CK) != 0; }
+
+  // The loads of a whole group, chunks c .. c+UC-1, are straight-line code: a
+  // branch around them would make the compiler join their registers with
+  // others behind it, by moves that wait for the loads at once.
+  static __device__ __forceinline__ void load_w(WRegs& b, const WPtr& p, const WOff& o, int64_t c) {
+    const char* w = uniform_ptr(p.w + c * 64);
+#pragma unroll
+    for (int u = 0; u < UC; ++u)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) b.w[u][s] = load16(w + o.w[s] + 64 * u);
+    if constexpr (W4) {
+      const char* sp = uniform_ptr((const char*)p.s + 4 * c);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) load_dwords(b.s[s], sp + o.s[s]);
+    }
+  }
+  static __device__ __forceinline__ void load_x(XRegs& b, const XPtr& p, int64_t xpart, int64_t c) {
+    const char* x = uniform_ptr(p.x + c * (64 * XV));
+#pragma unroll
+    for (int u = 0; u < UC; ++u)
+#pragma unroll
+      for (int q = 0; q < PL; ++q)
+#pragma unroll
+        for (int j = 0; j < XV; ++j) b.x[u][q][j] = load16(x + q * xpart + p.xo + u * (64 * XV) + 64 * j);
+    if constexpr (X4) load_dwords(b.xs, uniform_ptr((const char*)p.s + 4 * c) + p.so);
   }
 
-  // Weights of chunks c .. c+UC-1, zeros from `end` on (uniform bounds).
-  static __device__ __forceinline__ void load_w(WBuf& b, const WPtr& p, int64_t c, int64_t end, int64_t K,
-                                                int g) {
-    if (whole(c, end, K)) {
-#pragma unroll
-      for (int u = 0; u < UC; ++u)
-#pragma unroll
-        for (int s = 0; s < NS; ++s) b.v[u][s] = load16(p.w[s] + (c + u) * 64 + 16 * g);
-      if constexpr (W4) {
-        // One load of the group's 4 UC scales, the lane's picked by shifts.
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          uint32_t d[UC];
-          __builtin_memcpy(d, p.s[s] + 4 * c, 4 * UC);
-#pragma unroll
-          for (int u = 0; u < UC; ++u) b.s[u][s] = (d[u] >> (8 * g)) & 255u;
-        }
-      }
-      return;
-    }
+  // The last, partial group of a row: chunks c .. , zeros past K.
+  static __device__ __forceinline__ void load_w_rest(WRegs& b, const WPtr& p, const WOff& o, int64_t c, int64_t K,
+                                                     int lane) {
+    const int piece = lane & 3;
 #pragma unroll
     for (int u = 0; u < UC; ++u) {
       const int64_t cc = c + u;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        b.v[u][s] = zero4();
-        b.s[u][s] = 127u;
-      }
-      if (cc < end) {
         if constexpr (W4) {
-          const int64_t blk = 4 * cc + g;
-          if (blk * 32 < K) {
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-              b.v[u][s] = load16(p.w[s] + blk * 16);
-              b.s[u][s] = p.s[s][blk];
-            }
-          }
+          b.w[u][s] = (4 * cc + piece) * 32 < K ? load16(p.w + cc * 64 + o.w[s]) : zero4();
+          b.s[s][u] = scales_rest(p.s + 4 * cc + o.s[s], cc, K);
         } else {
-#pragma unroll
-          for (int s = 0; s < NS; ++s) b.v[u][s] = load8_tail(p.w[s], cc * 32 + 8 * g, K);
+          b.w[u][s] = load8_rest(p.w + cc * 64 + o.w[s], K - (cc * 32 + 8 * piece));
         }
       }
     }
   }
-
-  // The same chunks of A, of all tiles or (one) the first alone.
-  static __device__ __forceinline__ void load_x(XBuf& b, const XPtr& p, int64_t c, int64_t end, int64_t K, int g,
-                                                bool one) {
-    const bool all = whole(c, end, K);
+  static __device__ __forceinline__ void load_x_rest(XRegs& b, const XPtr& p, int64_t xpart, int64_t c, int64_t K,
+                                                     int lane) {
+    const int piece = lane & 3;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      if (t > 0 && one) continue;
-      if (all) {
-        if constexpr (X4) {
-          uint32_t d[UC];
-          __builtin_memcpy(d, p.s[t] + 4 * c, 4 * UC);
-#pragma unroll
-          for (int u = 0; u < UC; ++u) {
-            b.v[u][t][0][0] = load16(p.x[t] + (c + u) * 64 + 16 * g);
-            b.s[u][t] = (d[u] >> (8 * g)) & 255u;
-          }
-        } else {
-#pragma unroll
-          for (int u = 0; u < UC; ++u)
-#pragma unroll
-            for (int q = 0; q < PL; ++q)
-#pragma unroll
-              for (int j = 0; j < XV; ++j)
-                b.v[u][t][q][j] = load16(p.x[t] + q * p.part + (c + u) * (2 * CK) + g * (16 * XV) + 16 * j);
-        }
-        continue;
-      }
-#pragma unroll
-      for (int u = 0; u < UC; ++u) {
-        const int64_t cc = c + u;
+    for (int u = 0; u < UC; ++u) {
+      const int64_t cc = c + u;
+      if constexpr (X4) {
+        const int64_t left = K - (4 * cc + piece) * 32;
+        b.x[u][0][0] = left > 0 ? mask_codes(load16(p.x + cc * 64 + p.xo), left < 32 ? (int)left : 32) : zero4();
+        b.xs[u] = scales_rest(p.s + 4 * cc + p.so, cc, K);
+      } else {
 #pragma unroll
         for (int q = 0; q < PL; ++q)
 #pragma unroll
-          for (int j = 0; j < XV; ++j) b.v[u][t][q][j] = zero4();
-        b.s[u][t] = 127u;
-        if (cc < end) {
-          if constexpr (X4) {
-            const int64_t blk = 4 * cc + g, left = K - blk * 32;
-            if (left > 0) {
-              b.v[u][t][0][0] = mask_codes(load16(p.x[t] + blk * 16), left < 32 ? (int)left : 32);
-              b.s[u][t] = p.s[t][blk];
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < PL; ++q)
-#pragma unroll
-              for (int j = 0; j < XV; ++j)
-                b.v[u][t][q][j] = load8_tail(p.x[t] + q * p.part, cc * CK + g * (8 * XV) + 8 * j, K);
-          }
-        }
+          for (int j = 0; j < XV; ++j)
+            b.x[u][q][j] = load8_rest(p.x + cc * (64 * XV) + q * xpart + p.xo + 64 * j,
+                                      K - (cc * CK + 32 * j + 8 * piece));
       }
     }
   }
 
-  // Products of a group, T tiles of A, without a branch between the matrix
-  // instructions (see settle).
-  template <int T, bool WIDE>
-  static __device__ __forceinline__ void mma_tiles(f32x4 (&acc)[NS][MT], const WBuf& wb, const XBuf& xb) {
+  // The four scales of chunk c at p, 2^0 past K.
+  static __device__ __forceinline__ uint32_t scales_rest(const uint8_t* p, int64_t c, int64_t K) {
+    uint32_t d = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d |= ((4 * c + i) * 32 < K ? (uint32_t)gload<uint8_t>(p + i) : 127u) << (8 * i);
+    return d;
+  }
+
+  // A group's weights and scales into the wave's LDS.
+  static __device__ __forceinline__ void stage_w(char* lds, const WRegs& b, int lane) {
+    wave_order();
+    const int r = lane >> 2, at = r * 64 + (((lane & 3) ^ fa(r)) << 4);
+#pragma unroll
+    for (int u = 0; u < UC; ++u)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) *(u32x4*)(lds + (u * NS + s) * 1024 + at) = b.w[u][s];
+    if constexpr (W4) {
+      if (lane < 16) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int u = 0; u < UC; ++u) *(uint32_t*)(lds + S_AT + ((s * 16 + lane) * UC + u) * 4) = b.s[s][u];
+      }
+    }
+  }
+
+  // Chunk u, part q of A through the wave's LDS: this lane's octets.
+  static __device__ __forceinline__ void turn_x(char* lds, const XRegs& b, int u, int q, u32x4 (&f)[XV], int lane) {
+    wave_order();
+    const int wr = lane >> 2, at = wr * 64 + (((lane & 3) ^ fa(wr)) << 4);
+#pragma unroll
+    for (int j = 0; j < XV; ++j) *(u32x4*)(lds + X_AT + j * 1024 + at) = b.x[u][q][j];
+    wave_order();
+    const int r = lane & 15, g = lane >> 4;
+    if constexpr (XV == 1) {
+      f[0] = *(const u32x4*)(lds + X_AT + r * 64 + ((g ^ fa(r)) << 4));
+    } else {
+#pragma unroll
+      for (int j = 0; j < XV; ++j) f[j] = *(const u32x4*)(lds + X_AT + g * 1024 + r * 64 + ((j ^ fa(r)) << 4));
+    }
+  }
+
+  // A tile's octets of the whole group.
+  struct XFrags {
+    u32x4 f[UC][PL][XV];
+    uint32_t s[UC];
+  };
+  static __device__ __forceinline__ void turn(XFrags& f, char* lds, const XRegs& b, int lane) {
+    if constexpr (X4) {
+      wave_order();
+      if (lane < 16) {
+#pragma unroll
+        for (int u = 0; u < UC; ++u) *(uint32_t*)(lds + XS_AT + (lane * UC + u) * 4) = b.xs[u];
+      }
+    }
 #pragma unroll
     for (int u = 0; u < UC; ++u) {
 #pragma unroll
+      for (int q = 0; q < PL; ++q) turn_x(lds, b, u, q, f.f[u][q], lane);
+      if constexpr (X4) f.s[u] = *(const uint32_t*)(lds + XS_AT + ((lane & 15) * UC + u) * 4) >> (8 * (lane >> 4));
+    }
+  }
+
+  // Products of the staged group with tile T of A, no branch between the
+  // matrix instructions (see settle), the strips in turn so that neighbouring
+  // instructions do not wait for each other's sums.
+  template <int T, bool WIDE>
+  static __device__ __forceinline__ void mma_tile(f32x4 (&acc)[NS][MT], const char* lds, const XFrags& x, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int u = 0; u < UC; ++u) {
+      u32x4 w[NS];
+      uint32_t sb[NS];
+#pragma unroll
       for (int s = 0; s < NS; ++s) {
-        if constexpr (X4) {
-          const u32x4 a = wb.v[u][s];
-          const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+        w[s] = *(const u32x4*)(lds + (u * NS + s) * 1024 + r * 64 + ((g ^ fa(r)) << 4));
+        if constexpr (W4) sb[s] = (*(const uint32_t*)(lds + S_AT + ((s * 16 + r) * UC + u) * 4) >> (8 * g)) & 255u;
+      }
+      if constexpr (X4) {
+        const u32x4 b = x.f[u][0][0];
+        const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
 #pragma unroll
-          for (int t = 0; t < T; ++t) {
-            const u32x4 b = xb.v[u][t][0][0];
-            const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-            acc[s][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc[s][t], 4, 4, 0,
-                                                                         (int)wb.s[u][s], 0, (int)xb.s[u][t]);
-          }
-        } else if constexpr (W4) {
-          const float sc = scale_f32(wb.s[u][s]);
+        for (int s = 0; s < NS; ++s) {
+          const i32x8 av = {(int)w[s][0], (int)w[s][1], (int)w[s][2], (int)w[s][3], 0, 0, 0, 0};
+          acc[s][T] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc[s][T], 4, 4, 0, (int)sb[s], 0,
+                                                                       (int)x.s[u]);
+        }
+      } else if constexpr (W4) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (XF == SX_F16 && !WIDE) {
-              const f16x8 wf = mx4_to_f16(wb.v[u][s][j], sc);
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (XF == SX_F16 && WIDE) {
+            bf16x8 hi, lo;
+            split_bf16(as8<f16x8>(x.f[u][0][j]), hi, lo);
 #pragma unroll
-              for (int t = 0; t < T; ++t) acc[s][t] = mfma16(wf, as8<f16x8>(xb.v[u][t][0][j]), acc[s][t]);
-            } else {
-              static_assert(XF != SX_F16P, "MX4 weights take bfloat16 parts");
-              const bf16x8 wf = mx4_to_bf16(wb.v[u][s][j], sc);
+            for (int s = 0; s < NS; ++s) {
+              const bf16x8 wf = mx4_to_bf16(w[s][j], scale_f32(sb[s]));
+              acc[s][T] = mfma16(wf, lo, acc[s][T]);
+              acc[s][T] = mfma16(wf, hi, acc[s][T]);
+            }
+            __builtin_amdgcn_sched_barrier(0);   // one octet's registers at a time
+          } else {
+            static_assert(XF != SX_F16P, "MX4 weights take bfloat16 parts");
 #pragma unroll
-              for (int t = 0; t < T; ++t) {
-                if constexpr (XF == SX_F16) {
-                  bf16x8 hi, lo;
-                  split_bf16(as8<f16x8>(xb.v[u][t][0][j]), hi, lo);
-                  acc[s][t] = mfma16(wf, lo, acc[s][t]);
-                  acc[s][t] = mfma16(wf, hi, acc[s][t]);
-                  __builtin_amdgcn_sched_barrier(0);   // one split's registers at a time
-                } else {
+            for (int s = 0; s < NS; ++s) {
+              if constexpr (XF == SX_F16) {
+                acc[s][T] = mfma16(mx4_to_f16(w[s][j], scale_f32(sb[s])), as8<f16x8>(x.f[u][0][j]), acc[s][T]);
+              } else {
+                const bf16x8 wf = mx4_to_bf16(w[s][j], scale_f32(sb[s]));
 #pragma unroll
-                  for (int q = PL - 1; q >= 0; --q)
-                    acc[s][t] = mfma16(wf, as8<bf16x8>(xb.v[u][t][q][j]), acc[s][t]);
-                }
+                for (int q = PL - 1; q >= 0; --q)   // the smaller part first
+                  acc[s][T] = mfma16(wf, as8<bf16x8>(x.f[u][q][j]), acc[s][T]);
               }
             }
           }
-        } else {
-          using V = std::conditional_t<WF == SW_F16, f16x8, bf16x8>;
-#pragma unroll
-          for (int t = 0; t < T; ++t)
-#pragma unroll
-            for (int q = PL - 1; q >= 0; --q)
-              acc[s][t] = mfma16(as8<V>(wb.v[u][s]), as8<V>(xb.v[u][t][q][0]), acc[s][t]);
         }
+      } else {
+        using V = std::conditional_t<WF == SW_F16, f16x8, bf16x8>;
+#pragma unroll
+        for (int q = PL - 1; q >= 0; --q)
+#pragma unroll
+          for (int s = 0; s < NS; ++s) acc[s][T] = mfma16(as8<V>(w[s]), as8<V>(x.f[u][q][0]), acc[s][T]);
       }
     }
-#pragma unroll
-    for (int s = 0; s < NS; ++s) settle(acc[s]);
+    settle(acc, T);
   }
 
-  static __device__ __forceinline__ void mma(f32x4 (&acc)[NS][MT], const WBuf& wb, const XBuf& xb, bool one) {
-    bool wide = false;
-    if constexpr (W4 && XF == SX_F16) {   // scales that binary16 does not hold
+  // Some scale of the group is one that binary16 does not hold (lanes 0 .. 15
+  // have them).
+  static __device__ __forceinline__ bool wide(const WRegs& b, int lane) {
+    bool w = false;
+    if constexpr (W4 && XF == SX_F16) {
 #pragma unroll
-      for (int u = 0; u < UC; ++u)
+      for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          const uint32_t b = wb.s[u][s];
-          wide = wide || b > 140 || (b > 60 && b < 104);
-        }
-      wide = __any(wide);
+        for (int u = 0; u < UC; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x = (b.s[s][u] >> (8 * i)) & 255u;
+            w = w || x > 140 || (x > 60 && x < 104);
+          }
+      w = __any(w && lane < 16);
     }
-    if (W4 && XF == SX_F16 && wide) {
-      if (MT > 1 && one)
-        mma_tiles<1, true>(acc, wb, xb);
-      else
-        mma_tiles<MT, true>(acc, wb, xb);
-    } else {
-      if (MT > 1 && one)
-        mma_tiles<1, false>(acc, wb, xb);
-      else
-        mma_tiles<MT, false>(acc, wb, xb);
+    return w;
+  }
+
+  template <int T>
+  static __device__ __forceinline__ void mma(f32x4 (&acc)[NS][MT], const char* lds, const XFrags& x, bool is_wide,
+                                             int lane) {
+    if (W4 && XF == SX_F16 && is_wide)
+      mma_tile<T, true>(acc, lds, x, lane);
+    else
+      mma_tile<T, false>(acc, lds, x, lane);
+  }
+
+  // Tiles 1 .. tiles-1 of A against the staged group: few calls have any, so
+  // their rows are fetched when they are needed.
+  template <int T, bool REST, class Cursor>
+  static __device__ __forceinline__ void more_tiles(f32x4 (&acc)[NS][MT], char* lds, const Cursor& cc, int64_t xpart,
+                                                    int64_t K, bool is_wide, int lane) {
+    if constexpr (T < MT) {
+      if (T < cc.tiles()) {
+        XRegs b;
+        XFrags x;
+        if constexpr (REST)
+          load_x_rest(b, cc.x(T), xpart, cc.c(), K, lane);
+        else
+          load_x(b, cc.x(T), xpart, cc.c());
+        turn(x, lds, b, lane);
+        mma<T>(acc, lds, x, is_wide, lane);
+        more_tiles<T + 1, REST>(acc, lds, cc, xpart, K, is_wide, lane);
+      }
     }
   }
 
-  // Sums over chunks [c0, c1); `one`: only the first tile of A is in use.
-  static __device__ __forceinline__ void run(f32x4 (&acc)[NS][MT], const WPtr& wp, const XPtr& xp, int64_t c0,
-                                             int64_t c1, int64_t K, int g, bool one) {
-    WBuf cur, nxt;
-    XBuf x;
-    load_w(cur, wp, c0, c1, K, g);
-    for (int64_t c = c0; c < c1; c += UC) {
-      load_x(x, xp, c, c1, K, g, one);
-      if (c + UC < c1) load_w(nxt, wp, c + UC, c1, K, g);
-      mma(acc, cur, x, one);
-      cur = nxt;
+  // Runs over a sequence of whole groups with three cursors on it, of one type:
+  // one for the weights (two groups ahead), one for A (one ahead), one for the
+  // products.  A cursor has bool more(), void next(), int64_t c() (the group's
+  // first chunk), WPtr w(), XPtr x(int tile), int tiles(); done(cursor) is called
+  // after each group's products.  The cursors that run ahead stop at the last
+  // group and load it again.
+  template <class Cursor, class Done>
+  static __device__ __forceinline__ void stream(f32x4 (&acc)[NS][MT], char* lds, Cursor cc, const WOff& wo,
+                                                int64_t xpart, int64_t K, int lane, const Done& done) {
+    if (!cc.more()) return;
+    Cursor wc = cc, xc = cc;
+    auto ahead = [](Cursor& c) {
+      Cursor n = c;
+      n.next();
+      if (n.more()) c = n;
+    };
+    WRegs w0, w1;
+    XRegs x;
+    load_w(w0, wc.w(), wo, wc.c());
+    ahead(wc);
+    load_x(x, xc.x(0), xpart, xc.c());
+    ahead(xc);
+    load_w(w1, wc.w(), wo, wc.c());
+    ahead(wc);
+    auto step = [&](WRegs& w) {
+      XFrags f;
+      stage_w(lds, w, lane);
+      const bool is_wide = wide(w, lane);
+      turn(f, lds, x, lane);
+      load_x(x, xc.x(0), xpart, xc.c());
+      ahead(xc);
+      load_w(w, wc.w(), wo, wc.c());
+      ahead(wc);
+      mma<0>(acc, lds, f, is_wide, lane);
+      more_tiles<1, false>(acc, lds, cc, xpart, K, is_wide, lane);
+      done(cc);
+      cc.next();
+    };
+    while (true) {
+      step(w0);
+      if (!cc.more()) break;
+      step(w1);
+      if (!cc.more()) break;
     }
+  }
+
+  // The partial group at the cursor (its c() is the first chunk behind the whole
+  // groups).
+  template <class Cursor>
+  static __device__ __forceinline__ void finish(f32x4 (&acc)[NS][MT], char* lds, const Cursor& cc, const WOff& wo,
+                                                int64_t xpart, int64_t K, int lane) {
+    WRegs w;
+    XRegs x;
+    XFrags f;
+    load_w_rest(w, cc.w(), wo, cc.c(), K, lane);
+    load_x_rest(x, cc.x(0), xpart, cc.c(), K, lane);
+    stage_w(lds, w, lane);
+    const bool is_wide = wide(w, lane);
+    turn(f, lds, x, lane);
+    mma<0>(acc, lds, f, is_wide, lane);
+    more_tiles<1, true>(acc, lds, cc, xpart, K, is_wide, lane);
+  }
+
+  // A cursor over every `stride`-th of `n` groups of one product.
+  template <class Rows>
+  struct Line {
+    int64_t g, n, stride;
+    const WPtr* wp;
+    const Rows* rows;
+    int n_tiles;
+    __device__ __forceinline__ bool more() const { return g < n; }
+    __device__ __forceinline__ void next() { g += stride; }
+    __device__ __forceinline__ int64_t c() const { return g * UC; }
+    __device__ __forceinline__ const WPtr& w() const { return *wp; }
+    __device__ __forceinline__ XPtr x(int t) const { return (*rows)(t); }
+    __device__ __forceinline__ int tiles() const { return n_tiles; }
+  };
+
+  // Part `part` of `parts` of the sums over K, for `tiles` tiles of A whose rows
+  // rows(t) gives.  The parts take the groups in turn, the partial one too.
+  template <class Rows>
+  static __device__ __forceinline__ void run(f32x4 (&acc)[NS][MT], char* lds, const WPtr& wp, const WOff& wo,
+                                             const Rows& rows, int64_t xpart, int part, int parts, int64_t K,
+                                             int tiles, int lane) {
+    const int64_t n = groups(K);
+    stream(acc, lds, Line<Rows>{part, n, parts, &wp, &rows, tiles}, wo, xpart, K, lane, [](const Line<Rows>&) {});
+    if (rest(K) && part == (int)(n % parts))
+      finish(acc, lds, Line<Rows>{n, n + 1, parts, &wp, &rows, tiles}, wo, xpart, K, lane);
   }
 };
 
@@ -350,40 +529,41 @@ struct StripArgs {
 // C[m,n] = sum_k A[m,k] B[n,k] with MX4 B: workgroup -> (16 NS columns of C,
 // 16 MT rows), its NW waves the ranges of K.
 template <int XF, int DT, int NS, int MT, int UC, int NW>
-__global__ __launch_bounds__(64 * NW, MT < 2 ? 4 : 2) void mx4_strip_kernel(StripArgs a) {
+__global__ __launch_bounds__(64 * NW) void mx4_strip_kernel(StripArgs a) {
   using S = Strip<SW_MX4, XF, NS, MT, UC>;
   constexpr int TILES = NS * MT;
-  __shared__ f32x4 part[NW * TILES * 64];
+  __shared__ union {
+    char wave[NW][S::LDS];
+    f32x4 part[NW * TILES * 64];
+  } sh;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * (16 * NS), m0 = (int64_t)blockIdx.y * (16 * MT);
-  typename S::WPtr w;
-  typename S::XPtr x;
-  x.part = 0;
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    int64_t n = n0 + 16 * i + (lane & 15);
-    if (n >= a.N) n = a.N - 1;
-    w.w[i] = a.b + n * a.ldb;
-    w.s[i] = a.bs + n * a.ldbs;
-  }
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    int64_t m = m0 + 16 * t + (lane & 15);
-    if (m >= a.M) m = a.M - 1;
-    x.x[t] = a.a + m * a.lda;
-    x.s[t] = a.as + m * a.ldas;
-  }
+  const typename S::WPtr w{a.b + n0 * a.ldb, a.bs + n0 * a.ldbs};
+  const typename S::WOff wo = S::offsets(a.N - n0, 16, a.ldb, a.ldbs, lane);
+  const int64_t left = a.M - m0;
+  auto rows = [&](int t) {
+    int64_t m = 16 * t + (lane >> 2), ms = 16 * t + (lane < 16 ? lane : 0);
+    typename S::XPtr x;
+    if (m >= left) m = left - 1;
+    if (ms >= left) ms = left - 1;
+    x.x = a.a + m0 * a.lda;
+    x.s = S::X4 ? a.as + m0 * a.ldas : nullptr;
+    x.xo = (uint32_t)(m * a.lda) + 16 * (lane & 3);
+    x.so = (uint32_t)(ms * a.ldas);
+    return x;
+  };
   f32x4 acc[NS][MT];
   S::clear(acc);
-  const int64_t nc = S::chunks(a.K);
-  S::run(acc, w, x, nc * wave / NW, nc * (wave + 1) / NW, a.K, lane >> 4, a.M - m0 <= 16);
+  S::run(acc, sh.wave[wave], w, wo, rows, 0, wave, NW, a.K,
+         left >= 16 * MT ? MT : (int)((left + 15) / 16), lane);
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < NS; ++i)
 #pragma unroll
-    for (int t = 0; t < MT; ++t) part[(wave * TILES + i * MT + t) * 64 + lane] = acc[i][t];
+    for (int t = 0; t < MT; ++t) sh.part[(wave * TILES + i * MT + t) * 64 + lane] = acc[i][t];
   __syncthreads();
   for (int tile = wave; tile < TILES; tile += NW) {
-    const f32x4 v = sum_waves(part + tile * 64, TILES * 64, NW, lane);
+    const f32x4 v = sum_waves(sh.part + tile * 64, TILES * 64, NW, lane);
     const int i = tile / MT, t = tile % MT;
     const int64_t m = m0 + 16 * t + (lane & 15), n = n0 + 16 * i + 4 * (lane >> 4);
     if (m < a.M && n < a.N) {
@@ -392,9 +572,9 @@ __global__ __launch_bounds__(64 * NW, MT < 2 ? 4 : 2) void mx4_strip_kernel(Stri
 #pragma unroll
       for (int r = 0; r < 4; ++r) h[r] = cvt_out<DT>(v[r]);
       if (n + 4 <= a.N) {
-        __builtin_memcpy(c, h, 8);
+        gstore(c, u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16});
       } else {
-        for (int r = 0; r < 4 && n + r < a.N; ++r) c[r] = h[r];
+        for (int r = 0; r < 4 && n + r < a.N; ++r) gstore<uint16_t>(c + r, h[r]);
       }
     }
   }

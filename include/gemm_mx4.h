@@ -52,7 +52,8 @@ int gemm_mx4_dequantize(const void* data, int64_t ldd, const void* scales, int64
  * C[m,n] := sum_k A[m,k] B[n,k] for MX4 A [M, K] and MX4 B [N, K], fp32
  * accumulation, C of format fmt_c (GEMM_FMT_F16 or GEMM_FMT_BF16), row-major
  * with row stride ldc.  lda, ldb, ldsa, ldsb: row strides of the data and
- * scale arrays in bytes; data rows are 16-byte aligned (GEMM_ERR_LAYOUT).
+ * scale arrays in bytes; data rows are 16-byte aligned and, as the scales'
+ * rows, at most 2^26 bytes apart (GEMM_ERR_LAYOUT).
  * Needs gemm_mx4_workspace_bytes(M, N, K) bytes of workspace (may be 0); with
  * workspace == NULL they are allocated in stream order.
  */
@@ -66,7 +67,8 @@ size_t gemm_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * GEMM_FMT_BF16; A[m,k] at A + m*lda + k) and MX4 B [N, K]; C has A's format.
  * The weights enter the products exactly, at any scale.  A kernel for few
  * rows (the weights are read once per 64 rows of A): with many rows, quantise
- * A and call gemm_mx4.
+ * A and call gemm_mx4.  Rows of A at most 2^25 elements apart, rows of B as
+ * above (GEMM_ERR_LAYOUT).
  */
 int gemm_mx4_a16(const void* A, int32_t fmt, int64_t lda, const void* B, int64_t ldb, const void* SB,
                  int64_t ldsb, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K, void* stream);

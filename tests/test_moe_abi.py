@@ -47,6 +47,8 @@ MX = dict(mx4=1, w1_e=80 * 48, w1_n=48, S1=P[5], s1_e=80 * 3, s1_n=3, w2_e=70 * 
     (dict(ldy=69), -4),
     (dict(Y=P[0] + 2), -5), (dict(Y=P[1]), -5), (dict(Y=P[2] + 64), -5), (dict(Y=P[3]), -5),
     ({**MX, "Y": P[5] + 8}, -5), ({**MX, "Y": P[6]}, -5), (dict(ws=P[4]), -5), (dict(ws=P[3]), -5),
+    (dict(ldx=2 ** 30), -9), (dict(w1_n=2 ** 26, w1_e=2 ** 33), -9), (dict(w2_n=2 ** 27, w2_e=2 ** 35), -9),
+    ({**MX, "s1_n": 2 ** 27}, -9), ({**MX, "s2_n": 2 ** 28}, -9), (dict(I=2 ** 20 + 1), -2),
     (dict(nws=100), -6), (dict(ws=P[7] + 16), -6),
 ])
 def test_refusals(kw, code):
