@@ -73,11 +73,41 @@ bool strip_takes(const StripArgs& a) {
   return a.lda <= kMaxStripLd && a.ldas <= kMaxStripLd && a.ldb <= kMaxStripLd && a.ldbs <= kMaxStripLd;
 }
 
+// How many strips of 16 columns a wave takes, and how many rows: as many as
+// leave three quarters of the compute units a workgroup, since each further
+// strip shares the A that the wave turns through LDS and each further tile of
+// rows the weights.  Measured (us per kernel in a graph of 50; NS = strips,
+// rows x N x K):
+//   16-bit A   1 x 2048 x 7168: NS 1 5.6, NS 2 6.9;  16 x 7168 x 2048: 5.1, 4.2
+//              32 x 7168 x 7168, 32 rows a wave: NS 1 15.7, 2 11.8, 4 15.8
+//              64 x 7168 x 7168, 32 rows: NS 1 28.0, 2 20.5, 4 16.5; 64 rows,
+//              NS 2: 20.1
+//   MX4 A      16 x 7168 x 2048: NS 1 3.9, NS 2 3.6
+//              64 rows a wave, 333 x 1061 x 2050: NS 2 7.1, 4 9.1;
+//              512 x 2048 x 7168: NS 2 22.0, 4 18.2; 1024 x 2048 x 7168:
+//              NS 4 34.2, with four waves instead of eight 31.9
 template <int XF, int DT>
 int launch_strip_m(const StripArgs& a, hipStream_t s) {
   if (!strip_takes(a)) return GEMM_ERR_LAYOUT;
-  if (a.M <= 16) return launch_strip<XF, DT, 1, 1, 2, 8>(a, s);
-  return launch_strip<XF, DT, 2, 4, 1, 8>(a, s);
+  int cus = 0;
+  const int rc = device_cus(&cus);
+  if (rc) return rc;
+  const int64_t enough = 3 * (int64_t)cus / 4;
+  if (a.M <= 16) {
+    if (cdiv(a.N, 32) >= enough) return launch_strip<XF, DT, 2, 1, 1, 8>(a, s);
+    return launch_strip<XF, DT, 1, 1, XF == SX_MX4 ? 2 : 1, 8>(a, s);
+  }
+  if constexpr (XF == SX_MX4) {
+    const int64_t wgs = cdiv(a.N, 64) * cdiv(a.M, 64);
+    if (wgs < enough) return launch_strip<XF, DT, 2, 4, 1, 8>(a, s);
+    if (4 * wgs <= 5 * (int64_t)cus) return launch_strip<XF, DT, 4, 4, 1, 8>(a, s);
+    return launch_strip<XF, DT, 4, 4, 1, 4>(a, s);
+  } else {
+    const int64_t m = cdiv(a.M, 32);
+    if (cdiv(a.N, 64) * m >= enough) return launch_strip<XF, DT, 4, 2, 1, 8>(a, s);
+    if (cdiv(a.N, 32) * m >= enough) return launch_strip<XF, DT, 2, 2, 1, 8>(a, s);
+    return launch_strip<XF, DT, 1, 2, 1, 8>(a, s);
+  }
 }
 
 // The tile kernel's plan: its scale arrays, transposed, are the workspace.
@@ -95,9 +125,13 @@ TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
   return p;
 }
 
-// The tile kernel takes more than 64 rows; its lane offsets span 255 rows in
-// 32 bits.
-bool takes_tile(int64_t M, int64_t K) { return M > 64 && K <= (INT64_C(1) << 24); }
+// 256 x 256 tiles from 48 of them on (1024 x 2048 x 7168, 32 tiles: 41.3 us
+// against 31.9 by strips; 2048^3, 64 tiles: 17.5 against 21.0; 1024 x 4096 x
+// 4096, 64: 26.2 against 36.2), unless most of each tile would be empty.  Lane
+// offsets span 255 rows in 32 bits.
+bool takes_tile(int64_t M, int64_t N, int64_t K) {
+  return M > 128 && N > 128 && (double)cdiv(M, Mx4Cfg::BM) * (double)cdiv(N, Mx4Cfg::BN) >= 48 && K <= (INT64_C(1) << 24);
+}
 constexpr int64_t kMaxTileLd = INT64_C(1) << 24;
 
 template <int DT>
@@ -216,7 +250,7 @@ int gemm_mx4_dequantize(const void* data, int64_t ldd, const void* scales, int64
 }
 
 size_t gemm_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (M <= 0 || N <= 0 || K <= 0 || M > INT64_MAX / 8 || N > INT64_MAX / 8 || !takes_tile(M, K)) return 0;
+  if (M <= 0 || N <= 0 || K <= 0 || M > INT64_MAX / 8 || N > INT64_MAX / 8 || !takes_tile(M, N, K)) return 0;
   const int64_t rows = cdiv(M, 256) * 256 + cdiv(N, 256) * 256;
   int64_t bytes;
   if (__builtin_mul_overflow(4 * cdiv(K, 128), rows, &bytes)) return 0;
@@ -241,7 +275,7 @@ int gemm_mx4(const void* A, int64_t lda, const void* SA, int64_t ldsa, const voi
                     ldsb, (uint16_t*)C, ldc, M, N, K};
   hipStream_t s = (hipStream_t)stream;
   const bool f16 = fmt_c == GEMM_FMT_F16;
-  if (!takes_tile(M, K) || lda > kMaxTileLd || ldb > kMaxTileLd)
+  if (!takes_tile(M, N, K) || lda > kMaxTileLd || ldb > kMaxTileLd)
     return f16 ? launch_strip_m<SX_MX4, DT_F16>(a, s) : launch_strip_m<SX_MX4, DT_BF16>(a, s);
   const size_t need = gemm_mx4_workspace_bytes(M, N, K);
   if (need == 0) return GEMM_ERR_SHAPE;

@@ -124,7 +124,7 @@ __device__ __forceinline__ void split_parts(float v, uint16_t& hi, uint16_t& lo)
 template <int WF, int DT, int MT, int NI_, int UC>
 struct MoeUp {
   static constexpr int NI = NI_;
-  using S = Strip<WF, DT == DT_F16 ? SX_F16 : SX_BF16, 2 * NI, MT, UC>;
+  using S = Strip<WF, DT == DT_F16 ? SX_F16 : SX_BF16, 2 * NI, MT, UC, 1>;   // few experts get more than 16 tokens
   static constexpr int TILES = 2 * NI * MT;
 
   struct Shared {
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_up_kernel(MoeArgs a) 
 template <int WF, int MT, int NS_, int UC>
 struct MoeDown {
   static constexpr int NS = NS_;
-  using S = Strip<WF, WF == SW_F16 ? SX_F16P : SX_BF16P, NS, MT, UC>;
+  using S = Strip<WF, WF == SW_F16 ? SX_F16P : SX_BF16P, NS, MT, UC, 1>;
   static constexpr int kPairs = 16 * MT * kMoeTopK;
 
   struct Shared {

@@ -105,7 +105,9 @@ __device__ __forceinline__ void wave_order() {
 }
 
 // NS strips of 16 weight rows x MT tiles of 16 rows of A, UC chunks at a time.
-template <int WF, int XF, int NS_, int MT_, int UC_>
+// XT: tiles of A that run ahead; the others are fetched when they are needed
+// (see more_tiles).
+template <int WF, int XF, int NS_, int MT_, int UC_, int XT = MT_>
 struct Strip {
   static constexpr int NS = NS_, MT = MT_, UC = UC_;
   static constexpr bool W4 = WF == SW_MX4, X4 = XF == SX_MX4;
@@ -113,6 +115,7 @@ struct Strip {
   static constexpr int CK = W4 ? 128 : 32;                  // k per chunk
   static constexpr int XV = X4 ? 1 : (W4 ? 4 : 1);          // 64-byte pieces of A per chunk, row and part
   static_assert(W4 || !X4, "MX4 A takes MX4 weights");
+  static_assert(XT == 1 || XT == MT_, "one tile ahead, or all");
   // A wave's LDS: the group's weights, one chunk of one part of A, scales.
   static constexpr int X_AT = UC * NS * 1024, S_AT = X_AT + XV * 1024, XS_AT = S_AT + (W4 ? NS * 16 * UC * 4 : 0);
   static constexpr int LDS = XS_AT + (X4 ? 16 * UC * 4 : 0);
@@ -390,12 +393,19 @@ struct Strip {
       mma_tile<T, false>(acc, lds, x, lane);
   }
 
-  // Tiles 1 .. tiles-1 of A against the staged group: few calls have any, so
-  // their rows are fetched when they are needed.
+  template <int T>
+  static __device__ __forceinline__ void mma_all(f32x4 (&acc)[NS][MT], const char* lds, const XFrags* f, bool is_wide,
+                                                 int lane) {
+    mma<T>(acc, lds, f[T], is_wide, lane);
+    if constexpr (T + 1 < XT) mma_all<T + 1>(acc, lds, f, is_wide, lane);
+  }
+
+  // Tiles 1 .. tiles-1 of A against the staged group where only tile 0 runs
+  // ahead.
   template <int T, bool REST, class Cursor>
   static __device__ __forceinline__ void more_tiles(f32x4 (&acc)[NS][MT], char* lds, const Cursor& cc, int64_t xpart,
                                                     int64_t K, bool is_wide, int lane) {
-    if constexpr (T < MT) {
+    if constexpr (T < MT && XT == 1) {
       if (T < cc.tiles()) {
         XRegs b;
         XFrags x;
@@ -427,23 +437,26 @@ struct Strip {
       if (n.more()) c = n;
     };
     WRegs w0, w1;
-    XRegs x;
+    XRegs x[XT];
     load_w(w0, wc.w(), wo, wc.c());
     ahead(wc);
-    load_x(x, xc.x(0), xpart, xc.c());
+#pragma unroll
+    for (int t = 0; t < XT; ++t) load_x(x[t], xc.x(t), xpart, xc.c());
     ahead(xc);
     load_w(w1, wc.w(), wo, wc.c());
     ahead(wc);
     auto step = [&](WRegs& w) {
-      XFrags f;
+      XFrags f[XT];
       stage_w(lds, w, lane);
       const bool is_wide = wide(w, lane);
-      turn(f, lds, x, lane);
-      load_x(x, xc.x(0), xpart, xc.c());
+#pragma unroll
+      for (int t = 0; t < XT; ++t) turn(f[t], lds, x[t], lane);
+#pragma unroll
+      for (int t = 0; t < XT; ++t) load_x(x[t], xc.x(t), xpart, xc.c());
       ahead(xc);
       load_w(w, wc.w(), wo, wc.c());
       ahead(wc);
-      mma<0>(acc, lds, f, is_wide, lane);
+      mma_all<0>(acc, lds, f, is_wide, lane);
       more_tiles<1, false>(acc, lds, cc, xpart, K, is_wide, lane);
       done(cc);
       cc.next();
@@ -462,14 +475,17 @@ struct Strip {
   static __device__ __forceinline__ void finish(f32x4 (&acc)[NS][MT], char* lds, const Cursor& cc, const WOff& wo,
                                                 int64_t xpart, int64_t K, int lane) {
     WRegs w;
-    XRegs x;
-    XFrags f;
+    XFrags f[XT];
     load_w_rest(w, cc.w(), wo, cc.c(), K, lane);
-    load_x_rest(x, cc.x(0), xpart, cc.c(), K, lane);
     stage_w(lds, w, lane);
     const bool is_wide = wide(w, lane);
-    turn(f, lds, x, lane);
-    mma<0>(acc, lds, f, is_wide, lane);
+#pragma unroll
+    for (int t = 0; t < XT; ++t) {
+      XRegs x;
+      load_x_rest(x, cc.x(t), xpart, cc.c(), K, lane);
+      turn(f[t], lds, x, lane);
+    }
+    mma_all<0>(acc, lds, f, is_wide, lane);
     more_tiles<1, true>(acc, lds, cc, xpart, K, is_wide, lane);
   }
 

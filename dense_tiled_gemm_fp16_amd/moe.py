@@ -9,8 +9,8 @@ import ctypes
 
 import torch
 
-from ._lib import GEMM_OK, MoeArgs, lib
-from .mx4 import FORMATS, MX4, _error, _on, _stream, _workspace
+from ._lib import MoeArgs, lib
+from .mx4 import FORMATS, MX4, _call, _workspace
 
 MAX_TOKENS, MAX_EXPERTS, MAX_TOP_K = 64, 512, 16
 
@@ -23,8 +23,9 @@ def gemm_moe_workspace_bytes(T, E, top_k, H, I):
 def _weights(w, name):
     """(pointer, expert stride, row stride, scales pointer and strides)."""
     if isinstance(w, MX4):
-        return (w.data.data_ptr(), w.data.stride(0), w.data.stride(1), w.scales.data_ptr(), w.scales.stride(0),
-                w.scales.stride(1))
+        data, ldd, scales, lds = w._rows()
+        per_d, per_s = w._stack_strides()
+        return data, per_d, ldd, scales, per_s, lds
     if w.stride(2) != 1 and w.shape[2] > 1:
         raise ValueError(f"{name} must have unit stride along its last axis")
     return w.data_ptr(), w.stride(0), w.stride(1), 0, 0, 0
@@ -82,9 +83,6 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
                    FORMATS[x.dtype], FORMATS[logits.dtype], int(quantised), int(bool(renormalize)))
     if workspace is None:
         workspace = _workspace(lib.gemm_moe_workspace_bytes(T, E, top_k, H, I), x.device, stream)
-    rc = _on(x.device, lambda: lib.gemm_moe(ctypes.byref(args), _stream(stream, x.device),
-                                            workspace.data_ptr(),
-                                            workspace.numel() * workspace.element_size()))
-    if rc != GEMM_OK:
-        raise _error(rc)
+    _call(lib.gemm_moe, x.device, stream, (ctypes.byref(args),),
+          (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
     return out

@@ -23,20 +23,23 @@ def _error(rc):
     return GemmError(rc)
 
 
-# The current stream as an integer, without the Stream object around it.
+# The current stream as an integer, and the current device, without the checks
+# and objects of torch.cuda around them: a small call is bound by its Python.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _on(device, call):
-    """call() with `device` current."""
-    if device.index == torch.cuda.current_device():
-        return call()
-    with torch.cuda.device(device):
-        return call()
-
-
-def _stream(stream, device):
-    return _raw_stream(device.index) if stream is None else stream.cuda_stream
+def _call(fn, device, stream, before, after=()):
+    """fn(*before, stream, *after) with `device` current."""
+    index = device.index
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == _current_device():
+        rc = fn(*before, s, *after)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*before, s, *after)
+    if rc != GEMM_OK:
+        raise _error(rc)
 
 
 def _workspace(nbytes, device, stream):
@@ -126,6 +129,13 @@ class MX4:
             return p, 16 * blocks, p + self._buffer.numel() // 17 * 16, blocks
         return self._data.data_ptr(), self._data.stride(-2), self._scales.data_ptr(), self._scales.stride(-2)
 
+    def _stack_strides(self):
+        """Strides from matrix to matrix of a stack's data and scales."""
+        if self._buffer is not None:
+            rows, blocks = self.shape[-2], -(-self.K // BLOCK)
+            return 16 * rows * blocks, rows * blocks
+        return self._data.stride(0), self._scales.stride(0)
+
     def __getitem__(self, rows):
         return MX4(self.data[rows], self.scales[rows], self.K)
 
@@ -157,11 +167,8 @@ def quantize_mx4(x, out=None, stream=None):
         raise ValueError("out must be an MX4 of x's shape on its device, contiguous")
     G, sg = (shape[0], strides[0]) if len(shape) == 3 else (1, 1)
     data, _, scales, _ = out._rows()
-    rc = _on(device, lambda: lib.gemm_mx4_quantize(
-        x.data_ptr(), fmt, sg, strides[-2], strides[-1], G, shape[-2], shape[-1], data, scales,
-        _stream(stream, device)))
-    if rc != GEMM_OK:
-        raise _error(rc)
+    _call(lib.gemm_mx4_quantize, device, stream,
+          (x.data_ptr(), fmt, sg, strides[-2], strides[-1], G, shape[-2], shape[-1], data, scales))
     return out
 
 
@@ -187,10 +194,8 @@ def dequantize_mx4(q, dtype=torch.bfloat16, out=None, stream=None):
                 dequantize_mx4(q[i], dtype, out[i], stream)
             return out
         R *= shape[1]
-    rc = _on(device, lambda: lib.gemm_mx4_dequantize(
-        *q._rows(), R, q.K, out.data_ptr(), fmt, out.stride(-2), _stream(stream, device)))
-    if rc != GEMM_OK:
-        raise _error(rc)
+    _call(lib.gemm_mx4_dequantize, device, stream,
+          (*q._rows(), R, shape[-1], out.data_ptr(), fmt, out.stride(-2)))
     return out
 
 
@@ -210,33 +215,37 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
 
     workspace: gemm_mx4_workspace_bytes(M, N, K) bytes, 256-byte aligned, not
     shared with a call that may overlap; allocated here when not given."""
-    if not isinstance(b, MX4) or b.ndim != 2 or a.ndim != 2:
+    if type(b) is not MX4 or len(b.shape) != 2 or len(a.shape) != 2:
         raise ValueError("expected a matrix a and an MX4 matrix b [N, K]")
     device = b.device
-    if not b.is_cuda or a.device != device:
+    if device.type != "cuda" or a.device != device:
         raise ValueError("inputs must share one GPU device")
     (M, K), (N, Kb) = a.shape, b.shape
-    if K != Kb or min(M, N, K) <= 0:
+    if K != Kb or M <= 0 or N <= 0 or K <= 0:
         raise ValueError("incompatible or empty shape")
-    quantised = isinstance(a, MX4)
+    quantised = type(a) is MX4
     if quantised:
         dtype = dtype or torch.float16
         if dtype not in (torch.float16, torch.bfloat16):
             raise TypeError("dtype must be float16 or bfloat16")
     else:
-        if a.dtype not in (torch.float16, torch.bfloat16):
+        given, dtype = dtype, a.dtype
+        if FORMATS.get(dtype, 2) == 2:
             raise TypeError("a must be an MX4, float16 or bfloat16 matrix")
-        if dtype not in (None, a.dtype):
+        if given is not None and given != dtype:
             raise TypeError("the output of a 16-bit a has its dtype")
-        dtype = a.dtype
-        if (a.stride(1) != 1 and K > 1) or a.stride(0) <= 0:
+        lda, one = a.stride()
+        if (one != 1 and K > 1) or lda <= 0:
             raise ValueError("a must have unit stride along K and a positive row stride")
+    ldc = N
     if out is None:
         out = torch.empty((M, N), dtype=dtype, device=device)
     elif out.dtype != dtype or out.device != device or out.shape != (M, N) or \
             (out.stride(1) != 1 and N > 1) or out.stride(0) < N:
         raise ValueError("out must be a row-major [M, N] tensor of the output dtype on the inputs' device")
-    fmt, ldc = FORMATS[dtype], out.stride(0)
+    else:
+        ldc = out.stride(0)
+    fmt = FORMATS[dtype]
     if quantised:
         if workspace is None:
             need = lib.gemm_mx4_workspace_bytes(M, N, K)
@@ -244,11 +253,9 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
                 workspace = _workspace(need, device, stream)
         ws, nws = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
             if workspace is not None else (0, 0)
-        rc = _on(device, lambda: lib.gemm_mx4(*a._rows(), *b._rows(), out.data_ptr(), fmt, ldc, M, N, K,
-                                              _stream(stream, device), ws, nws))
+        _call(lib.gemm_mx4, device, stream,
+              (*a._rows(), *b._rows(), out.data_ptr(), fmt, ldc, M, N, K), (ws, nws))
     else:
-        rc = _on(device, lambda: lib.gemm_mx4_a16(a.data_ptr(), fmt, a.stride(0), *b._rows(), out.data_ptr(),
-                                                  ldc, M, N, K, _stream(stream, device)))
-    if rc != GEMM_OK:
-        raise _error(rc)
+        _call(lib.gemm_mx4_a16, device, stream,
+              (a.data_ptr(), fmt, lda, *b._rows(), out.data_ptr(), ldc, M, N, K))
     return out
