@@ -59,40 +59,58 @@ bool stack(const void* p, int64_t G, int64_t sg, int64_t R, int64_t sr, int64_t 
   return out->hi >= out->lo;
 }
 
-// Shapes of the two kernels: strips of I (NI) and columns of Y (NS) per wave,
+// Shapes of the two kernels: strips of I (NI) or of columns of Y (NS) per wave,
 // chunks per group (UC), waves per SIMD that the registers are limited to
-// (WPS).
+// (WPS).  Measured per kernel (us; bf16, H 7168, I 2048, top 8 of 64 experts;
+// up | down):
+//   1 token, 16-bit    UC 2: 84, UC 4: 131 with the registers of WPS 4
+//                      | NS 2 UC 2: 39, NS 1 UC 4: 47, NS 4 UC 2: 52
+//   64 tokens, 16-bit  UC 2: 637, UC 4: 642 | NS 2 UC 2: 332, NS 1 UC 4: 386
+//   16 tokens, MX4     NI 2 UC 2: 199, NI 1 UC 2: 221, NI 2 UC 1: 265
+//                      | NS 2 UC 1: 146, NS 1 UC 1: 200, NS 4 UC 1: 211
+//   64 tokens, MX4     NI 1 UC 2: 270, NI 1 UC 1: 331, NI 2 UC 1: spills
+//   H 2048, I 768, 4 tokens, 16-bit: down NS 1 UC 4 11.5, NS 2 UC 2 14.7: where
+//   NS 2 leaves compute units without work, NS 1 (see launch_kernels)
 template <int WF, int MT>
 struct Shape {
   static constexpr int NI = 1, UP_UC = 2, UP_WPS = MT == 1 ? 4 : 2;
-  static constexpr int NS = 2, DOWN_UC = 2, DOWN_WPS = MT == 1 ? 4 : 2;
+  static constexpr int UC_NS1 = MT == 1 ? 4 : 2, UC_NS2 = 2, DOWN_WPS = MT == 1 ? 4 : 2;
 };
 template <int MT>
 struct Shape<SW_MX4, MT> {
-  static constexpr int NI = MT == 1 ? 2 : 1, UP_UC = MT == 1 ? 2 : 1, UP_WPS = 2;
-  static constexpr int NS = 2, DOWN_UC = 1, DOWN_WPS = 2;
+  static constexpr int NI = MT == 1 ? 2 : 1, UP_UC = 2, UP_WPS = 2;
+  static constexpr int UC_NS1 = 1, UC_NS2 = 1, DOWN_WPS = 2;
 };
 
+template <int WF, int DT, int MT, int NS, int UC>
+int launch_down(MoeArgs& a, hipStream_t s) {
+  void* p[] = {&a};
+  return hipLaunchKernel((const void*)moe_down_kernel<WF, DT, MT, NS, UC, Shape<WF, MT>::DOWN_WPS>,
+                         dim3((unsigned)cdiv(a.H, 16 * NS)), dim3(64 * kMoeWaves), p, 0, s) == hipSuccess
+             ? GEMM_OK
+             : GEMM_ERR_HIP;
+}
+
 template <int WF, int DT, int MT>
-int launch_kernels(const MoeArgs& a, hipStream_t s) {
+int launch_kernels(MoeArgs& a, int cus, hipStream_t s) {
   using P = Shape<WF, MT>;
-  MoeArgs copy = a;
-  void* p[] = {&copy};
+  // Parts of H per strip of I: as few as give the device six waves per compute
+  // unit (at most min(E, T top_k) experts are in use).
+  const int64_t strips = cdiv(a.I, 16 * P::NI) * std::min(a.E, a.T * a.k);
+  a.parts = 1;
+  while (a.parts < kMoeWaves && strips * a.parts < (int64_t)6 * cus) a.parts *= 2;
+  void* p[] = {&a};
   const dim3 up((unsigned)cdiv(a.I, 16 * P::NI * (kMoeWaves / a.parts)), (unsigned)(a.by_pair ? a.T * a.k : a.E));
   if (hipLaunchKernel((const void*)moe_up_kernel<WF, DT, MT, P::NI, P::UP_UC, P::UP_WPS>, up, dim3(64 * kMoeWaves),
                       p, 0, s) != hipSuccess)
     return GEMM_ERR_HIP;
-  const dim3 down((unsigned)cdiv(a.H, 16 * P::NS));
-  if (hipLaunchKernel((const void*)moe_down_kernel<WF, DT, MT, P::NS, P::DOWN_UC, P::DOWN_WPS>, down,
-                      dim3(64 * kMoeWaves), p, 0, s) != hipSuccess)
-    return GEMM_ERR_HIP;
-  return GEMM_OK;
+  return 4 * cdiv(a.H, 32) >= 3 * (int64_t)cus ? launch_down<WF, DT, MT, 2, P::UC_NS2>(a, s)
+                                               : launch_down<WF, DT, MT, 1, P::UC_NS1>(a, s);
 }
 
 template <int WF, int DT>
-int launch_layer(const MoeArgs& a, hipStream_t s) {
-  if (a.T <= 16) return launch_kernels<WF, DT, 1>(a, s);
-  return launch_kernels<WF, DT, 4>(a, s);
+int launch_layer(MoeArgs& a, int cus, hipStream_t s) {
+  return a.T <= 16 ? launch_kernels<WF, DT, 1>(a, cus, s) : launch_kernels<WF, DT, 4>(a, cus, s);
 }
 
 }  // namespace
@@ -182,22 +200,17 @@ int gemm_moe(const gemm_moe_args* g, void* stream, void* workspace, size_t works
       if (ranges_overlap(w0, w1, r->lo, r->hi)) return GEMM_ERR_ALIAS;
     if (ranges_overlap(w0, w1, ry.lo, ry.hi)) return GEMM_ERR_ALIAS;
   }
-  // Parts of H per strip: as few as leave every compute unit two workgroups
-  // of distinct work (the device's at most min(E, T top_k) experts in use).
   int cus = 0;
   int rc = device_cus(&cus);
   if (rc) return rc;
-  const int64_t strips = cdiv(I, g->mx4 && T <= 16 ? 32 : 16) * std::min(E, T * g->top_k);
-  a.parts = 1;
-  while (a.parts < kMoeWaves && strips * a.parts < (int64_t)2 * cus * kMoeWaves) a.parts *= 2;
   if (!workspace && hipMallocAsync(&ws, (size_t)l.bytes, s) != hipSuccess) return GEMM_ERR_HIP;
   a.act = (char*)ws;
   a.tab_e = (int32_t*)((char*)ws + l.tab_e);
   a.tab_p = (float*)((char*)ws + l.tab_p);
   if (g->mx4)
-    rc = g->fmt == GEMM_FMT_F16 ? launch_layer<SW_MX4, DT_F16>(a, s) : launch_layer<SW_MX4, DT_BF16>(a, s);
+    rc = g->fmt == GEMM_FMT_F16 ? launch_layer<SW_MX4, DT_F16>(a, cus, s) : launch_layer<SW_MX4, DT_BF16>(a, cus, s);
   else
-    rc = g->fmt == GEMM_FMT_F16 ? launch_layer<SW_F16, DT_F16>(a, s) : launch_layer<SW_BF16, DT_BF16>(a, s);
+    rc = g->fmt == GEMM_FMT_F16 ? launch_layer<SW_F16, DT_F16>(a, cus, s) : launch_layer<SW_BF16, DT_BF16>(a, cus, s);
   if (!workspace && hipFreeAsync(ws, s) != hipSuccess && rc == GEMM_OK) rc = GEMM_ERR_HIP;
   return rc;
 }

@@ -266,13 +266,13 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_up_kernel(MoeArgs a) 
 // What a workgroup of moe_down takes: NS strips of 16 columns of Y.
 template <int WF, int MT, int NS_, int UC>
 struct MoeDown {
-  static constexpr int NS = NS_;
+  static constexpr int NS = NS_, NW = kMoeWaves;
   using S = Strip<WF, WF == SW_F16 ? SX_F16P : SX_BF16P, NS, MT, UC, 1>;
   static constexpr int kPairs = 16 * MT * kMoeTopK;
 
   struct Shared {
-    char wave[kMoeWaves][S::LDS];
-    float own[kMoeWaves][16 * MT][16 * NS];
+    char wave[NW][S::LDS];
+    float own[NW][16 * MT][16 * NS];
     uint32_t mask[kMoeExperts][2];     // tokens of an expert
     uint16_t active[kMoeExperts], place[kMoeExperts];
     uint16_t start[kMoeExperts + 1];
@@ -290,7 +290,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a
   constexpr int kPairs = D::kPairs;
   __shared__ typename D::Shared sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  constexpr int NT = 64 * kMoeWaves;
+  constexpr int NW = D::NW, NT = 64 * NW;
   const int pairs = a.T * a.k;
   for (int i = tid; i < a.E; i += NT) sh.mask[i][0] = sh.mask[i][1] = 0;
   for (int i = tid; i < pairs; i += NT) {
@@ -376,9 +376,9 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a
       }
     }
     __device__ __forceinline__ bool more() const { return i < n; }
-    __device__ __forceinline__ bool last() const { return g + kMoeWaves >= gpe; }   // of the wave's, in an expert
+    __device__ __forceinline__ bool last() const { return g + D::NW >= gpe; }   // of the wave's, in an expert
     __device__ __forceinline__ void next() {
-      g += kMoeWaves;
+      g += D::NW;
       at_expert();
     }
     __device__ __forceinline__ int64_t c() const { return (int64_t)g * S::UC; }
@@ -429,7 +429,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a
       });
     }
     if (S::rest(a.I))
-      for (int i = wave; i < n; i += kMoeWaves) {
+      for (int i = wave; i < n; i += NW) {
         Cursor cur{&a, &sh, h0, i, n, 0, gpe + 1, 0, 0, lane};
         cur.at_expert();
         cur.g = gpe;
@@ -442,7 +442,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a
     const int t = i / (4 * NS), g = i % (4 * NS);
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < kMoeWaves; ++w)
+    for (int w = 0; w < NW; ++w)
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[r] += sh.own[w][t][4 * g + r];
     const int64_t h = h0 + 4 * g;
