@@ -15,6 +15,11 @@ from .mx4 import FORMATS, MX4, _call, _workspace
 MAX_TOKENS, MAX_EXPERTS, MAX_TOP_K = 64, 512, 16
 
 
+def _c_layer(args, workspace, nbytes, stream):
+    # the stream comes before the workspace
+    return lib.gemm_moe(args, stream, workspace, nbytes)
+
+
 def gemm_moe_workspace_bytes(T, E, top_k, H, I):
     """Bytes of workspace gemm_moe needs for these sizes."""
     return int(lib.gemm_moe_workspace_bytes(T, E, top_k, H, I))
@@ -83,6 +88,6 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
                    FORMATS[x.dtype], FORMATS[logits.dtype], int(quantised), int(bool(renormalize)))
     if workspace is None:
         workspace = _workspace(lib.gemm_moe_workspace_bytes(T, E, top_k, H, I), x.device, stream)
-    _call(lib.gemm_moe, x.device, stream, (ctypes.byref(args),),
-          (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+    _call(x.device, stream, _c_layer, ctypes.byref(args), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return out

@@ -11,11 +11,20 @@ computation runs in the HIP library.
 """
 import torch
 
-from ._lib import GEMM_OK, lib
+from ._lib import lib
 
 # Element formats of the C calls (enum gemm_mx4_format).
 FORMATS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 BLOCK = 32
+
+# Looked up once: a decode call's time is the host's.
+_c_quantize, _c_dequantize = lib.gemm_mx4_quantize, lib.gemm_mx4_dequantize
+_c_workspace, _c_product16 = lib.gemm_mx4_workspace_bytes, lib.gemm_mx4_a16
+
+
+def _c_product(*args):
+    # the stream comes before the workspace
+    return lib.gemm_mx4(*args[:-3], args[-1], args[-3], args[-2])
 
 
 def _error(rc):
@@ -29,16 +38,16 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
 
-def _call(fn, device, stream, before, after=()):
-    """fn(*before, stream, *after) with `device` current."""
+def _call(device, stream, fn, *args):
+    """fn(*args, stream) with `device` current."""
     index = device.index
     s = _raw_stream(index) if stream is None else stream.cuda_stream
     if index == _current_device():
-        rc = fn(*before, s, *after)
+        rc = fn(*args, s)
     else:
         with torch.cuda.device(device):
-            rc = fn(*before, s, *after)
-    if rc != GEMM_OK:
+            rc = fn(*args, s)
+    if rc:
         raise _error(rc)
 
 
@@ -62,7 +71,7 @@ class MX4:
     Both have unit stride along the last axis; data rows start 16-byte aligned.
     Slices of rows and of the stack are views (q[g], q[g, r0:r1], q[r0:r1])."""
 
-    __slots__ = ("_data", "_scales", "_buffer", "K", "shape", "device")
+    __slots__ = ("_data", "_scales", "_buffer", "_ldd", "_lds", "K", "shape", "device")
 
     def __init__(self, data, scales, K):
         blocks = -(-K // BLOCK)
@@ -77,6 +86,7 @@ class MX4:
         if data.stride(-1) != 1 or (scales.stride(-1) != 1 and blocks > 1):
             raise ValueError("data and scales must have unit stride along the last axis")
         self._data, self._scales, self._buffer = data, scales, None
+        self._ldd, self._lds = data.stride(-2), scales.stride(-2)
         self.K, self.shape, self.device = K, (*data.shape[:-1], K), data.device
 
     @classmethod
@@ -89,8 +99,10 @@ class MX4:
             rows *= n
         K = shape[-1]
         q._data = q._scales = None
-        q._buffer = torch.empty(17 * rows * -(-K // BLOCK), dtype=torch.uint8, device=device)
+        q._buffer = torch.empty((17 * rows * -(-K // BLOCK),), dtype=torch.uint8, device=device)
         q.K, q.shape, q.device = K, tuple(shape), device
+        q._lds = -(-K // BLOCK)
+        q._ldd = 16 * q._lds
         return q
 
     def _split(self):
@@ -125,9 +137,9 @@ class MX4:
     def _rows(self):
         """(data pointer, row stride, scales pointer, row stride)."""
         if self._buffer is not None:
-            p, blocks = self._buffer.data_ptr(), -(-self.K // BLOCK)
-            return p, 16 * blocks, p + self._buffer.numel() // 17 * 16, blocks
-        return self._data.data_ptr(), self._data.stride(-2), self._scales.data_ptr(), self._scales.stride(-2)
+            p = self._buffer.data_ptr()
+            return p, self._ldd, p + self._buffer.numel() // 17 * 16, self._lds
+        return self._data.data_ptr(), self._ldd, self._scales.data_ptr(), self._lds
 
     def _stack_strides(self):
         """Strides from matrix to matrix of a stack's data and scales."""
@@ -167,8 +179,8 @@ def quantize_mx4(x, out=None, stream=None):
         raise ValueError("out must be an MX4 of x's shape on its device, contiguous")
     G, sg = (shape[0], strides[0]) if len(shape) == 3 else (1, 1)
     data, _, scales, _ = out._rows()
-    _call(lib.gemm_mx4_quantize, device, stream,
-          (x.data_ptr(), fmt, sg, strides[-2], strides[-1], G, shape[-2], shape[-1], data, scales))
+    _call(device, stream, _c_quantize, x.data_ptr(), fmt, sg, strides[-2], strides[-1], G, shape[-2], shape[-1],
+          data, scales)
     return out
 
 
@@ -194,8 +206,8 @@ def dequantize_mx4(q, dtype=torch.bfloat16, out=None, stream=None):
                 dequantize_mx4(q[i], dtype, out[i], stream)
             return out
         R *= shape[1]
-    _call(lib.gemm_mx4_dequantize, device, stream,
-          (*q._rows(), R, shape[-1], out.data_ptr(), fmt, out.stride(-2)))
+    data, ldd, scales, lds = q._rows()
+    _call(device, stream, _c_dequantize, data, ldd, scales, lds, R, shape[-1], out.data_ptr(), fmt, out.stride(-2))
     return out
 
 
@@ -239,23 +251,24 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
             raise ValueError("a must have unit stride along K and a positive row stride")
     ldc = N
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=device)
+        out = a.new_empty((M, N)) if not quantised else torch.empty((M, N), dtype=dtype, device=device)
     elif out.dtype != dtype or out.device != device or out.shape != (M, N) or \
             (out.stride(1) != 1 and N > 1) or out.stride(0) < N:
         raise ValueError("out must be a row-major [M, N] tensor of the output dtype on the inputs' device")
     else:
         ldc = out.stride(0)
     fmt = FORMATS[dtype]
+    bp, ldb, sp, lds = b._rows()
     if quantised:
         if workspace is None:
-            need = lib.gemm_mx4_workspace_bytes(M, N, K)
+            need = _c_workspace(M, N, K)
             if need:
                 workspace = _workspace(need, device, stream)
         ws, nws = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
             if workspace is not None else (0, 0)
-        _call(lib.gemm_mx4, device, stream,
-              (*a._rows(), *b._rows(), out.data_ptr(), fmt, ldc, M, N, K), (ws, nws))
+        ap, lda, asp, ldas = a._rows()
+        _call(device, stream, _c_product, ap, lda, asp, ldas, bp, ldb, sp, lds, out.data_ptr(), fmt, ldc, M, N, K,
+              ws, nws)
     else:
-        _call(lib.gemm_mx4_a16, device, stream,
-              (a.data_ptr(), fmt, lda, *b._rows(), out.data_ptr(), ldc, M, N, K))
+        _call(device, stream, _c_product16, a.data_ptr(), fmt, lda, bp, ldb, sp, lds, out.data_ptr(), ldc, M, N, K)
     return out
