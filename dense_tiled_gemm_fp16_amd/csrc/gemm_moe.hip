@@ -18,7 +18,7 @@ static_assert(kMoeTokens == GEMM_MOE_MAX_TOKENS && kMoeExperts == GEMM_MOE_MAX_E
 
 namespace {
 
-constexpr int64_t kMaxH = INT64_C(1) << 30, kMaxI = INT64_C(1) << 20;
+constexpr int64_t kMaxH = INT64_C(1) << 26, kMaxI = INT64_C(1) << 20;
 // The kernels reach the rows of an expert's W1, of 32 rows of W2 and of all
 // tokens by 32-bit offsets beside a 64-bit address.
 constexpr int64_t kMaxOffset = (INT64_C(1) << 32) - (INT64_C(1) << 16);

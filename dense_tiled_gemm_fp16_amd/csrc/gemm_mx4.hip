@@ -16,8 +16,6 @@ using namespace gemmf16;
 
 namespace {
 
-constexpr int64_t kMaxGrid = (INT64_C(1) << 31) - 1;
-
 int64_t elem_size(int32_t fmt) { return fmt == GEMM_FMT_F32 ? 4 : 2; }
 
 struct Range {
@@ -36,6 +34,16 @@ bool byte_rows(const void* p, int64_t rows, int64_t ld, int64_t row_bytes, Range
 }
 
 bool overlap(const Range& a, const Range& b) { return ranges_overlap(a.lo, a.hi, b.lo, b.hi); }
+
+// A launch takes fewer than 2^32 work items along x.
+bool fits_x(int64_t gx, int threads) { return gx < (INT64_C(1) << 32) / threads; }
+
+// n workgroups of 256 as a grid that a launch takes (rounded up).
+dim3 wide_grid(int64_t n) {
+  constexpr int64_t kX = INT64_C(1) << 22;
+  return n <= kX ? dim3((unsigned)n) : dim3((unsigned)kX, (unsigned)cdiv(n, kX));
+}
+constexpr int64_t kMaxWide = INT64_C(65535) << 22;
 
 int run(const void* fn, dim3 grid, int threads, void* args, hipStream_t s) {
   void* p[] = {args};
@@ -60,7 +68,6 @@ constexpr int64_t kMaxK = INT64_C(1) << 36;
 template <int XF, int DT, int NS, int MT, int UC, int NW>
 int launch_strip(const StripArgs& a, hipStream_t s) {
   const int64_t gx = cdiv(a.N, 16 * NS), gy = cdiv(a.M, 16 * MT);
-  if (gx > kMaxGrid || gy > 65535) return GEMM_ERR_SHAPE;
   StripArgs copy = a;
   return run((const void*)mx4_strip_kernel<XF, DT, NS, MT, UC, NW>, dim3((unsigned)gx, (unsigned)gy), 64 * NW,
              &copy, s);
@@ -89,6 +96,8 @@ bool strip_takes(const StripArgs& a) {
 template <int XF, int DT>
 int launch_strip_m(const StripArgs& a, hipStream_t s) {
   if (!strip_takes(a)) return GEMM_ERR_LAYOUT;
+  // The grid: fewer than 2^32 work items along x, 65535 workgroups along y.
+  if (a.N > (INT64_C(1) << 27) || cdiv(a.M, XF == SX_MX4 ? 64 : 32) > 65535) return GEMM_ERR_SHAPE;
   int cus = 0;
   const int rc = device_cus(&cus);
   if (rc) return rc;
@@ -160,7 +169,7 @@ int launch_tile(const StripArgs& a, void* ws, hipStream_t s) {
   t.sb = sb;
   t.sb_rows = p.sb_rows;
   int64_t grid;
-  if (__builtin_mul_overflow(t.k.GM, t.k.GN, &grid) || grid > kMaxGrid || gx > kMaxGrid || gy > 65535)
+  if (__builtin_mul_overflow(t.k.GM, t.k.GN, &grid) || !fits_x(grid, Mx4Cfg::NT) || !fits_x(gx, 256) || gy > 65535)
     return GEMM_ERR_SHAPE;
   const int rc = run((const void*)mx4_scales_kernel, dim3((unsigned)gx, (unsigned)gy, 2), 256, &q, s);
   if (rc) return rc;
@@ -212,8 +221,8 @@ int gemm_mx4_quantize(const void* X, int32_t fmt, int64_t ldx_g, int64_t ldx_r, 
                                 : (const void*)quantize_columns_kernel<MX_F32>;
   }
   const int64_t grid = cdiv(waves, 4);
-  if (grid > kMaxGrid) return GEMM_ERR_SHAPE;
-  return run(fn, dim3((unsigned)grid), 256, &a, (hipStream_t)stream);
+  if (grid > kMaxWide) return GEMM_ERR_SHAPE;
+  return run(fn, wide_grid(grid), 256, &a, (hipStream_t)stream);
 }
 
 int gemm_mx4_dequantize(const void* data, int64_t ldd, const void* scales, int64_t lds, int64_t R,
@@ -242,11 +251,11 @@ int gemm_mx4_dequantize(const void* data, int64_t ldd, const void* scales, int64
   a.rpw = octs <= 32 ? (int32_t)(64 / octs) : 1;
   const int64_t waves = a.rpw > 1 ? cdiv(a.R, a.rpw) : a.R * a.segs;
   const int64_t grid = cdiv(waves, 4);
-  if (grid > kMaxGrid) return GEMM_ERR_SHAPE;
+  if (grid > kMaxWide) return GEMM_ERR_SHAPE;
   const void* fn = fmt == GEMM_FMT_F16    ? (const void*)dequantize_kernel<MX_F16>
                    : fmt == GEMM_FMT_BF16 ? (const void*)dequantize_kernel<MX_BF16>
                                           : (const void*)dequantize_kernel<MX_F32>;
-  return run(fn, dim3((unsigned)grid), 256, &a, (hipStream_t)stream);
+  return run(fn, wide_grid(grid), 256, &a, (hipStream_t)stream);
 }
 
 size_t gemm_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
@@ -271,6 +280,8 @@ int gemm_mx4(const void* A, int64_t lda, const void* SA, int64_t ldsa, const voi
   int64_t span;
   if (!view_span(M, N, ldc, 1, &span) || !byte_rows(C, 1, 1, 2 * (span + 1), &rc_)) return GEMM_ERR_SHAPE;
   if (overlap(rc_, ra) || overlap(rc_, rsa) || overlap(rc_, rb) || overlap(rc_, rsb)) return GEMM_ERR_ALIAS;
+  if (M == 1) lda = ldsa = 0;   // a single row has no next one
+  if (N == 1) ldb = ldsb = 0;
   const StripArgs a{(const char*)A, lda, (const uint8_t*)SA, ldsa, (const char*)B, ldb, (const uint8_t*)SB,
                     ldsb, (uint16_t*)C, ldc, M, N, K};
   hipStream_t s = (hipStream_t)stream;
@@ -308,6 +319,8 @@ int gemm_mx4_a16(const void* A, int32_t fmt, int64_t lda, const void* B, int64_t
   const int rc = check_mx4(B, ldb, SB, ldsb, N, K, &rb, &rsb);
   if (rc) return rc;
   if (overlap(rc_, ra) || overlap(rc_, rb) || overlap(rc_, rsb)) return GEMM_ERR_ALIAS;
+  if (M == 1) lda = 0;   // a single row has no next one
+  if (N == 1) ldb = ldsb = 0;
   const StripArgs a{(const char*)A, 2 * lda, nullptr, 0, (const char*)B, ldb, (const uint8_t*)SB, ldsb,
                     (uint16_t*)C, ldc, M, N, K};
   return fmt == GEMM_FMT_F16 ? launch_strip_m<SX_F16, DT_F16>(a, (hipStream_t)stream)

@@ -114,6 +114,11 @@ __device__ __forceinline__ uint32_t to_codes(const float* f, uint32_t byte) {
   return d;
 }
 
+// The wave's number in a grid that may spill over into y.
+__device__ __forceinline__ int64_t wave_item() {
+  return ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+
 constexpr int kQuantU = 4;   // wave items of 64 lanes x 8 elements in flight
 
 // Rows with unit k stride.  Wave item w: row (or rpw rows) w / segs, octets
@@ -121,7 +126,7 @@ constexpr int kQuantU = 4;   // wave items of 64 lanes x 8 elements in flight
 template <int FMT>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
   const int lane = threadIdx.x & 63;
-  const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t w = wave_item();
   const int64_t rows = a.G * a.R, octs = 4 * a.Kb;
   int64_t row = w / a.segs, o0 = (w - row * a.segs) * (64 * kQuantU) + lane;
   bool mine = true;
@@ -170,7 +175,7 @@ template <int FMT>
 __global__ __launch_bounds__(256) void quantize_columns_kernel(QuantArgs a) {
   using E = typename MxElem<FMT>::type;
   const int lane = threadIdx.x & 63;
-  const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t w = wave_item();
   const int64_t strip = w / a.Kb, b = w - strip * a.Kb;
   const int64_t row = strip * 64 + lane;
   if (row >= a.G * a.R) return;
@@ -222,7 +227,7 @@ template <int FMT>
 __global__ __launch_bounds__(256) void dequantize_kernel(DequantArgs a) {
   constexpr int ES = FMT == MX_F32 ? 4 : 2;
   const int lane = threadIdx.x & 63;
-  const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t w = wave_item();
   const int64_t octs = (a.K + 7) / 8;
   int64_t row = w / a.segs, o0 = (w - row * a.segs) * (64 * kQuantU) + lane;
   bool mine = true;

@@ -30,10 +30,10 @@
 //                    takes the chunk.
 //
 // Weights in MX4 are widened exactly: to bfloat16 at any scale; to binary16,
-// for a binary16 A, where the scale byte is in 104 .. 140 (or below 61, where
-// the terms vanish next to binary16's least step whatever A holds).  Other
-// scales take the chunk through bfloat16, A split exactly into two bfloat16
-// parts.
+// for a binary16 A, where the scale byte is in 104 .. 140.  Other scales take
+// the chunk through bfloat16, A split exactly into two bfloat16 parts; all but
+// 0, the scale of a block of zeros: whatever nonzero codes it has (up to 2^-124)
+// vanish next to binary16's least step.
 //
 // Rows past the end read a valid row (their sums are never stored); k past K
 // enters as zero on both sides.
@@ -377,7 +377,7 @@ struct Strip {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t x = (b.s[s][u] >> (8 * i)) & 255u;
-            w = w || x > 140 || (x > 60 && x < 104);
+            w = w || x > 140 || (x > 0 && x < 104);
           }
       w = __any(w && lane < 16);
     }

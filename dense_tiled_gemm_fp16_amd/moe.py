@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from ._lib import MoeArgs, lib
-from .mx4 import FORMATS, MX4, _call, _workspace
+from .mx4 import FORMATS, MX4, _call, _given, _workspace
 
 MAX_TOKENS, MAX_EXPERTS, MAX_TOP_K = 64, 512, 16
 
@@ -88,6 +88,5 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
                    FORMATS[x.dtype], FORMATS[logits.dtype], int(quantised), int(bool(renormalize)))
     if workspace is None:
         workspace = _workspace(lib.gemm_moe_workspace_bytes(T, E, top_k, H, I), x.device, stream)
-    _call(x.device, stream, _c_layer, ctypes.byref(args), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+    _call(x.device, stream, _c_layer, ctypes.byref(args), *_given(workspace, x.device))
     return out

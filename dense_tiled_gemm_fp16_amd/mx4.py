@@ -58,6 +58,13 @@ def _workspace(nbytes, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _given(workspace, device):
+    """(pointer, bytes) of a caller's workspace."""
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 class MX4:
     """A matrix in microscaled 4-bit floating point, [R, K] or a stack
     [G, R, K], quantised along K in blocks of 32.
@@ -199,15 +206,18 @@ def dequantize_mx4(q, dtype=torch.bfloat16, out=None, stream=None):
             (out.stride(-1) != 1 and shape[-1] > 1) or (len(shape) == 3 and not out.is_contiguous()):
         raise ValueError("out must be of q's shape, of dtype, on its device, with unit column stride "
                          "(a stack contiguous)")
-    R = shape[0]
+    R, K = shape[0], shape[-1]
+    data, ldd, scales, lds = q._rows()
+    ldy = out.stride(-2)
     if len(shape) == 3:
         if not q.is_contiguous():
             for i in range(R):
                 dequantize_mx4(q[i], dtype, out[i], stream)
             return out
-        R *= shape[1]
-    data, ldd, scales, lds = q._rows()
-    _call(device, stream, _c_dequantize, data, ldd, scales, lds, R, shape[-1], out.data_ptr(), fmt, out.stride(-2))
+        # one matrix of all rows (a stack of single rows may have any row stride)
+        R, lds, ldy = R * shape[1], -(-K // BLOCK), K
+        ldd = 16 * lds
+    _call(device, stream, _c_dequantize, data, ldd, scales, lds, R, K, out.data_ptr(), fmt, ldy)
     return out
 
 
@@ -264,8 +274,7 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
             need = _c_workspace(M, N, K)
             if need:
                 workspace = _workspace(need, device, stream)
-        ws, nws = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
-            if workspace is not None else (0, 0)
+        ws, nws = _given(workspace, device) if workspace is not None else (0, 0)
         ap, lda, asp, ldas = a._rows()
         _call(device, stream, _c_product, ap, lda, asp, ldas, bp, ldb, sp, lds, out.data_ptr(), fmt, ldc, M, N, K,
               ws, nws)

@@ -58,7 +58,7 @@ typedef struct {
  * One layer.  Needs gemm_moe_workspace_bytes(T, E, top_k, H, I) bytes of
  * workspace, 256-byte aligned; with workspace == NULL they are allocated in
  * stream order.  GEMM_ERR_SHAPE: a size outside the bounds above (H up to
- * 2^30, I up to 2^20); GEMM_ERR_LAYOUT: the 2I rows of an expert's W1 or the T
+ * 2^26, I up to 2^20); GEMM_ERR_LAYOUT: the 2I rows of an expert's W1 or the T
  * rows of X span 4 GiB or more, or rows of W2 are 2^27 bytes or more apart.
  */
 int gemm_moe(const gemm_moe_args* args, void* stream, void* workspace, size_t workspace_bytes);

@@ -55,7 +55,9 @@ int gemm_mx4_dequantize(const void* data, int64_t ldd, const void* scales, int64
  * scale arrays in bytes; data rows are 16-byte aligned and, as the scales'
  * rows, at most 2^26 bytes apart (GEMM_ERR_LAYOUT).
  * Needs gemm_mx4_workspace_bytes(M, N, K) bytes of workspace (may be 0); with
- * workspace == NULL they are allocated in stream order.
+ * workspace == NULL they are allocated in stream order.  GEMM_ERR_SHAPE: more
+ * than 65535 * 64 rows of A against 128 rows of B or fewer, or more than 2^27
+ * rows of B against 128 rows of A or fewer.
  */
 int gemm_mx4(const void* A, int64_t lda, const void* SA, int64_t ldsa, const void* B, int64_t ldb,
              const void* SB, int64_t ldsb, void* C, int32_t fmt_c, int64_t ldc, int64_t M, int64_t N,
@@ -65,10 +67,11 @@ size_t gemm_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 /*
  * C[m,n] := sum_k A[m,k] B[n,k] for a 16-bit A (format fmt, GEMM_FMT_F16 or
  * GEMM_FMT_BF16; A[m,k] at A + m*lda + k) and MX4 B [N, K]; C has A's format.
- * The weights enter the products exactly, at any scale.  A kernel for few
- * rows (the weights are read once per 64 rows of A): with many rows, quantise
+ * The weights enter the products exactly, at any scale (with a binary16 A
+ * those of scale 0, below 2^-124, as zeros).  A kernel for few
+ * rows (the weights are read once per 32 rows of A): with many rows, quantise
  * A and call gemm_mx4.  Rows of A at most 2^25 elements apart, rows of B as
- * above (GEMM_ERR_LAYOUT).
+ * above (GEMM_ERR_LAYOUT); M up to 65535 * 32, N up to 2^27 (GEMM_ERR_SHAPE).
  */
 int gemm_mx4_a16(const void* A, int32_t fmt, int64_t lda, const void* B, int64_t ldb, const void* SB,
                  int64_t ldsb, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K, void* stream);

@@ -62,7 +62,11 @@ CASES = [  # T, E, k, H, I: by pair (T k < E) and by expert, one expert, all exp
     (1, 8, 2, 64, 32), (1, 1, 1, 32, 16), (1, 100, 8, 200, 48), (3, 17, 3, 70, 33), (5, 64, 4, 129, 65),
     (2, 4, 4, 96, 40), (16, 8, 2, 256, 64), (17, 5, 1, 100, 50), (33, 2, 2, 64, 130), (64, 3, 2, 72, 24),
     (64, 1, 1, 130, 31), (40, 70, 6, 33, 17), (64, 16, 16, 48, 40), (7, 512, 5, 40, 24), (1, 3, 2, 1, 1),
-    (4, 6, 2, 1030, 520)]
+    (4, 6, 2, 1030, 520),
+    # enough columns of Y (on 256 compute units) for two strips a wave
+    (3, 4, 2, 6150, 24), (40, 5, 2, 6150, 40), (64, 3, 2, 6200, 70),
+    # enough strips of I for four, two and one part of H
+    (12, 24, 4, 70, 272), (40, 24, 4, 70, 530), (40, 24, 4, 300, 1040), (12, 24, 4, 70, 1040), (12, 24, 4, 70, 2060)]
 
 
 @pytest.mark.parametrize("T,E,k,H,I", CASES)
@@ -237,3 +241,7 @@ def test_gpu_refusals():
         la.run(out=la.x)
     with pytest.raises(g.GemmError):
         la.run(workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(8, dtype=torch.uint8, device=DEV).expand(1 << 16, 8),
+               torch.empty(1 << 21, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(ValueError):
+            la.run(workspace=ws)

@@ -40,7 +40,7 @@ MX = dict(mx4=1, w1_e=80 * 48, w1_n=48, S1=P[5], s1_e=80 * 3, s1_n=3, w2_e=70 * 
     ({**MX, "S1": None}, -1), ({**MX, "S2": None}, -1),
     (dict(T=0), -2), (dict(T=65), -2), (dict(E=0), -2), (dict(E=513), -2), (dict(top_k=0), -2),
     (dict(top_k=7), -2), (dict(E=40, ldl=40, top_k=17), -2), (dict(H=0), -2), (dict(I=-1), -2),
-    (dict(H=2 ** 31), -2), (dict(w1_e=2 ** 61), -2), (dict(w2_n=2 ** 57), -2),
+    (dict(H=2 ** 31), -2), (dict(H=2 ** 26 + 1, ldx=2 ** 27, w1_n=2 ** 20, w1_e=2 ** 27, w2_e=2 ** 33, ldy=2 ** 27), -2), (dict(w1_e=2 ** 61), -2), (dict(w2_n=2 ** 57), -2),
     (dict(fmt=2), -7), (dict(fmt_logits=3), -7), (dict(mx4=2), -7),
     (dict(ldx=0), -3), (dict(ldl=-1), -3), (dict(w1_n=0), -3), (dict(w2_e=-1), -3),
     ({**MX, "w1_n": 47}, -3), ({**MX, "s1_n": 2}, -3), ({**MX, "w2_n": 16}, -3), ({**MX, "s2_n": 1}, -3),

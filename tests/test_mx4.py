@@ -171,7 +171,13 @@ def check_guard(buf, M, N):
 
 SHAPES = [(1, 1, 1), (1, 16, 32), (3, 17, 33), (5, 70, 128), (16, 33, 130), (17, 16, 256), (31, 100, 511),
           (33, 31, 1000), (64, 48, 96), (65, 20, 700), (200, 130, 257), (1, 300, 7168), (130, 257, 2048),
-          (300, 264, 1025), (257, 513, 640)]
+          (300, 264, 1025), (257, 513, 640),
+          # enough columns (on 256 compute units) for several strips a wave, K of less and of more than a group
+          (16, 6150, 161), (1, 6200, 1000), (40, 6150, 289), (33, 3100, 513), (100, 6200, 257), (100, 10300, 97),
+          # enough rows and columns for 256 x 256 tiles: whole steps only, a partial one only, both, edges of
+          # nearly empty tiles
+          (1801, 1543, 640), (1801, 1543, 33), (1543, 1801, 1025), (130, 12500, 257), (12500, 130, 96),
+          (300, 6200, 2050), (1793, 1537, 128)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -209,7 +215,8 @@ def test_product_a16(M, N, K, dtype):
     assert torch.equal(g.gemm_mx4(a, mx4(*b, K)), out)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 40, 300), (16, 33, 1000), (70, 65, 700), (300, 300, 512)])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 300), (16, 33, 1000), (70, 65, 700), (300, 300, 512),
+                                   (1700, 1800, 1000)])
 def test_products_exact_sums(M, N, K):
     """Scales of 1: every product is a multiple of 1/4 and every sum below
     2^22, so fp32 holds it exactly and one rounding remains."""
@@ -224,12 +231,12 @@ def test_products_exact_sums(M, N, K):
 
 
 @pytest.mark.parametrize("scales", [(90, 96), (60, 104), (140, 146), (0, 30), (100, 141)])
-@pytest.mark.parametrize("M", [1, 20, 50])
-def test_product_a16_far_scales(scales, M):
+@pytest.mark.parametrize("M,N", [(1, 48), (20, 48), (50, 48), (9, 6150), (40, 6150), (33, 3100)])
+def test_product_a16_far_scales(scales, M, N):
     """Weight scales outside what binary16 holds: the weights stay exact.  A
     row of one block's weights alone shows any that were rounded away."""
     rng = np.random.default_rng(scales[0])
-    N, K = 48, 300
+    K = 300
     b = ref.random_codes(rng, N, K, *scales)
     x = torch.from_numpy(rng.standard_normal((M, K)) * 2.0 ** (6 if scales[0] < 100 else -14))
     say(f"gemm_mx4 far scales {scales}")
@@ -238,8 +245,26 @@ def test_product_a16_far_scales(scales, M):
         check_product(g.gemm_mx4(a, mx4(*b, K)), host64(a), ref.values(*b, K), f"{scales} {dtype}")
 
 
-def test_products_nan_scale_stays_in_its_row():
-    M, N, K = 5, 40, 300
+@pytest.mark.parametrize("scale", [1, 30, 60, 61, 103, 104, 140, 141, 254])
+def test_infinite_activations_at_any_scale(scale):
+    """An infinity times a weight that is not zero is infinite, however small
+    the weight."""
+    N, K = 20, 160
+    codes = np.full((N, 80), 0x11, dtype=np.uint8)      # 0.5 everywhere
+    codes[3] = 0x99                                     # -0.5
+    b = mx4(codes, np.full((N, 5), scale, dtype=np.uint8), K)
+    want = torch.full((N,), float("inf"))
+    want[3] = -float("inf")
+    say(f"gemm_mx4 infinities at scale {scale}")
+    for M in (1, 20):
+        for dtype in (torch.float16, torch.bfloat16):
+            a = torch.ones((M, K), dtype=dtype, device=DEV)
+            a[-1, 70] = float("inf")
+            assert torch.equal(g.gemm_mx4(a, b)[-1].float().cpu(), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 40, 300), (1600, 1800, 300)])
+def test_products_nan_scale_stays_in_its_row(M, N, K):
     rng = np.random.default_rng(3)
     a, b = ref.random_codes(rng, M, K), ref.random_codes(rng, N, K)
     b[1][7, 4] = 255
@@ -253,8 +278,8 @@ def test_products_nan_scale_stays_in_its_row():
     assert nan[2].all() and nan[:, 7].all() and nan.sum() == N + M - 1
 
 
-def test_strided_mx4_operands():
-    M, N, K = 70, 50, 200
+@pytest.mark.parametrize("M,N,K", [(70, 50, 200), (1600, 1800, 200)])
+def test_strided_mx4_operands(M, N, K):
     rng = np.random.default_rng(11)
     a, b = ref.random_codes(rng, 2 * M, K), ref.random_codes(rng, 3 * N, K)
     qa, qb = mx4(*a, K), mx4(*b, K)
@@ -285,9 +310,9 @@ def test_linear_layer_run(M):
     check_product(y16, host64(x), ref.values(*wq, K), "linear a16")
 
 
-@pytest.mark.parametrize("M", [3, 300])
-def test_graph_replays_and_other_stream(M):
-    N, K = 136, 352
+@pytest.mark.parametrize("M,N", [(3, 136), (300, 136), (1700, 1600)])
+def test_graph_replays_and_other_stream(M, N):
+    K = 352
     rng = np.random.default_rng(M)
     x = torch.from_numpy(rng.standard_normal((M, K))).to(torch.float16).to(DEV)
     qw = mx4(*ref.random_codes(rng, N, K, 118, 124), K)
@@ -323,6 +348,97 @@ def test_graph_replays_and_other_stream(M):
             assert torch.equal(a, b)
 
 
+def test_workspace():
+    M, N, K = 1700, 1800, 200
+    rng = np.random.default_rng(12)
+    a, b = mx4(*ref.random_codes(rng, M, K), K), mx4(*ref.random_codes(rng, N, K), K)
+    need = g.gemm_mx4_workspace_bytes(M, N, K)
+    assert need > 0 and g.gemm_mx4_workspace_bytes(64, 64, K) == 0
+    buf = torch.full((need + 512,), 255, dtype=torch.uint8, device=DEV)
+    say("mx4 workspace")
+    c = g.gemm_mx4(a, b, workspace=buf[:need])
+    assert (buf[need:] == 255).all() and torch.equal(c, g.gemm_mx4(a, b))
+    for bad in (buf[:need - 1], buf[8:need + 8]):
+        with pytest.raises(g.GemmError):
+            g.gemm_mx4(a, b, workspace=bad)
+    with pytest.raises(g.GemmError):                 # over the output
+        g.gemm_mx4(a, b, out=c, workspace=c.view(torch.uint8))
+    # two products at once, each with a workspace of its own
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(g.gemm_mx4(a, b))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, c) for o in outs)
+
+
+def test_offsets_past_32_bits():
+    """Elements, codes and outputs beyond 2^32 from the base."""
+    R, K = 66000, 66560                              # 4.4e9 elements, 8.8 GB in bfloat16
+    rng = np.random.default_rng(1)
+    say("mx4 past 32 bits")
+    x = torch.full((R, K), 0.5, dtype=torch.bfloat16, device=DEV)
+    tail = inputs(rng, 3, K, torch.bfloat16)
+    x[-3:] = tail.to(DEV)
+    q = g.quantize_mx4(x)
+    check_quantized(q[R - 3:], tail)
+    y = g.dequantize_mx4(q, torch.bfloat16)
+    want = torch.from_numpy(ref.values(*ref.quantize(host64(tail)), K)).to(torch.bfloat16)
+    assert torch.equal(y[-3:].cpu(), want) and (y[R - 4] == 0.5).all()
+    del x, y
+    N = 65600                                        # C of 4.3e9 elements
+    a, b = ref.random_codes(rng, R, 64, 120, 126), ref.random_codes(rng, N, 64, 120, 126)
+    c = g.gemm_mx4(mx4(*a, 64), mx4(*b, 64), dtype=torch.bfloat16)
+    check_product(c[-2:, -300:], ref.values(a[0][-2:], a[1][-2:], 64), ref.values(b[0][-300:], b[1][-300:], 64),
+                  "last rows")
+
+
+def test_more_rows_than_one_grid_axis_takes():
+    """2^26 rows of 257: more waves than a launch has along x.  The rows of x
+    overlap (row stride 1), so few bytes describe them."""
+    R, K = (1 << 26) + 100, 257
+    rng = np.random.default_rng(6)
+    line = torch.from_numpy(rng.standard_normal(R + K - 1).astype(np.float32)).to(torch.bfloat16)
+    x = line.to(DEV).as_strided((R, K), (1, 1))
+    say("mx4 many rows")
+    q = g.quantize_mx4(x)
+    y = g.dequantize_mx4(q, torch.bfloat16)
+    for r in (0, (1 << 24) - 2, R // 2, R - 4):
+        host = line.as_strided((R, K), (1, 1))[r:r + 4].contiguous()
+        check_quantized(q[r:r + 4], host)
+        assert torch.equal(y[r:r + 4].cpu(), torch.from_numpy(ref.values(*ref.quantize(host64(host)), K)).to(torch.bfloat16))
+
+
+def test_single_rows_of_far_strided_operands():
+    """A single row has no next one: its row stride does not matter."""
+    K, N = 96, 20
+    rng = np.random.default_rng(2)
+    a, b = ref.random_codes(rng, 1, K, 120, 126), ref.random_codes(rng, N, K, 120, 126)
+    qa, qb = mx4(*a, K), mx4(*b, K)
+    far = g.MX4(qa.data.as_strided((1, 48), (1 << 30, 1)), qa.scales.as_strided((1, 3), (1 << 30, 1)), K)
+    say("mx4 single rows")
+    assert torch.equal(g.gemm_mx4(far, qb), g.gemm_mx4(qa, qb))
+    assert torch.equal(g.gemm_mx4(qb, far), g.gemm_mx4(qb, qa))
+    x = torch.from_numpy(rng.standard_normal((1, K))).to(torch.float16).to(DEV)
+    assert torch.equal(g.gemm_mx4(x.as_strided((1, K), (1 << 30, 1)), qb), g.gemm_mx4(x, qb))
+
+
+def test_stack_of_single_rows_with_any_row_stride():
+    """[G, 1, K]: the stride of an axis of one is free."""
+    G, K = 5, 100
+    data, scales = ref.random_codes(np.random.default_rng(4), G, K)
+    d, s = dev(data).view(1, G, 64).transpose(0, 1), dev(scales).view(1, G, 4).transpose(0, 1)
+    assert d.is_contiguous() and d.stride(1) == G * 64
+    q = g.MX4(d, s, K)
+    say("mx4 stack of single rows")
+    out = torch.full((1, G, K), 3.0, device=DEV).transpose(0, 1)
+    y = g.dequantize_mx4(q, torch.float32, out=out)
+    assert np.array_equal(host64(y)[:, 0], ref.values(data, scales, K))
+
+
 def test_gpu_refusals():
     x = torch.zeros(4, 64, dtype=torch.float16, device=DEV)
     q = g.quantize_mx4(x)
@@ -346,3 +462,7 @@ def test_gpu_refusals():
         g.gemm_mx4(x, q, out=x[:, :4])
     with pytest.raises(ValueError):
         g.gemm_mx4(x, g.MX4(q.data.cpu(), q.scales.cpu(), 64))
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(8, dtype=torch.uint8, device=DEV).expand(1 << 16, 8),
+               torch.empty(1 << 21, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(ValueError):
+            g.gemm_mx4(q, q, workspace=ws)

@@ -70,6 +70,7 @@ def product(A=PX, lda=48, SA=PT, ldsa=3, B=PB, ldb=48, SB=PS, ldsb=3, C=PC, fmt=
     (dict(ldb=2 ** 27), -9), (dict(ldsa=2 ** 27), -9), (dict(M=65, lda=2 ** 27), -9),
     (dict(lda=32), -3), (dict(ldsb=2), -3), (dict(lda=50), -9), (dict(B=PB + 1), -9),
     (dict(C=PX), -5), (dict(C=PT), -5), (dict(C=PB + 16), -5), (dict(C=PS), -5), (dict(ldc=2 ** 62), -2),
+    (dict(M=65535 * 64 + 1), -2), (dict(N=2 ** 27 + 1, ldc=2 ** 27 + 1), -2),
 ])
 def test_product_refusals(kw, code):
     assert product(**kw) == code
@@ -84,6 +85,7 @@ def product16(A=PX, fmt=0, lda=70, B=PB, ldb=48, SB=PS, ldsb=3, C=PC, ldc=9, M=5
     (dict(K=0), -2), (dict(fmt=2), -7), (dict(lda=0), -3), (dict(ldc=8), -4), (dict(ldb=32), -3),
     (dict(lda=2 ** 26), -9), (dict(ldsb=2 ** 27), -9),
     (dict(B=PB + 8), -9), (dict(C=PX + 2), -5), (dict(C=PS), -5), (dict(lda=2 ** 62), -2),
+    (dict(M=65535 * 32 + 1), -2), (dict(N=2 ** 27 + 1, ldc=2 ** 27 + 1), -2),
 ])
 def test_product16_refusals(kw, code):
     assert product16(**kw) == code
