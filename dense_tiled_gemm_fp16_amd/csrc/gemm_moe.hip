@@ -67,25 +67,34 @@ bool stack(const void* p, int64_t G, int64_t sg, int64_t R, int64_t sr, int64_t 
 //                      | NS 2 UC 2: 39, NS 1 UC 4: 47, NS 4 UC 2: 52
 //   64 tokens, 16-bit  UC 2: 637, UC 4: 642 | NS 2 UC 2: 332, NS 1 UC 4: 386
 //   16 tokens, MX4     NI 2 UC 2: 199, NI 1 UC 2: 221, NI 2 UC 1: 265
-//                      | NS 2 UC 1: 146, NS 1 UC 1: 200, NS 4 UC 1: 211
+//                      | few: NS 2 UC 2: 110, NS 2 UC 1: 126, NS 1 UC 1: 138,
+//                      NS 1 UC 2: 161; not few: NS 2 UC 1: 152, NS 1 UC 1: 200
 //   64 tokens, MX4     NI 1 UC 2: 270, NI 1 UC 1: 331, NI 2 UC 1: spills
-//   H 2048, I 768, 4 tokens, 16-bit: down NS 1 UC 4 11.5, NS 2 UC 2 14.7: where
-//   NS 2 leaves compute units without work, NS 1 (see launch_kernels)
+//   H 2048, I 768, 4 tokens, 16-bit: down NS 1 UC 4 11.5 (few: 9.9), NS 2 UC 2
+//   14.7: where NS 2 leaves compute units without work, NS 1 (see launch_kernels)
+// "few" is the down kernel's form for experts with few tokens each.  It pays
+// while most have four or fewer, measured by the mean over all experts, T k / E
+// (16 tokens; few | not, us): MX4 2: 110 | 152, 3: 68 | 105, 4: 75 | 100, 6: 45
+// | 51, 8: 52 | 53, 16: 44 | 36; 16-bit 2: 261 | 263, 3: 155 | 150, 6: 100 | 83.
+// With more than 16 tokens its registers and LDS cost more than it saves (64
+// tokens, mean 8, 16-bit: 439 | 325).
 template <int WF, int MT>
 struct Shape {
   static constexpr int NI = 1, UP_UC = 2, UP_WPS = MT == 1 ? 4 : 2;
-  static constexpr int UC_NS1 = MT == 1 ? 4 : 2, UC_NS2 = 2, DOWN_WPS = MT == 1 ? 4 : 2;
+  static constexpr int UC_NS1 = MT == 1 ? 4 : 2, UC_NS2 = 2, FEW_UC_NS2 = 2, DOWN_WPS = MT == 1 ? 4 : 2;
+  static constexpr int FEW_MEAN = 2;
 };
 template <int MT>
 struct Shape<SW_MX4, MT> {
   static constexpr int NI = MT == 1 ? 2 : 1, UP_UC = 2, UP_WPS = 2;
-  static constexpr int UC_NS1 = 1, UC_NS2 = 1, DOWN_WPS = 2;
+  static constexpr int UC_NS1 = 1, UC_NS2 = 1, FEW_UC_NS2 = 2, DOWN_WPS = 2;
+  static constexpr int FEW_MEAN = 4;
 };
 
-template <int WF, int DT, int MT, int NS, int UC>
+template <int WF, int DT, int MT, int NS, int UC, bool FEW>
 int launch_down(MoeArgs& a, hipStream_t s) {
   void* p[] = {&a};
-  return hipLaunchKernel((const void*)moe_down_kernel<WF, DT, MT, NS, UC, Shape<WF, MT>::DOWN_WPS>,
+  return hipLaunchKernel((const void*)moe_down_kernel<WF, DT, MT, NS, UC, Shape<WF, MT>::DOWN_WPS, FEW>,
                          dim3((unsigned)cdiv(a.H, 16 * NS)), dim3(64 * kMoeWaves), p, 0, s) == hipSuccess
              ? GEMM_OK
              : GEMM_ERR_HIP;
@@ -104,8 +113,14 @@ int launch_kernels(MoeArgs& a, int cus, hipStream_t s) {
   if (hipLaunchKernel((const void*)moe_up_kernel<WF, DT, MT, P::NI, P::UP_UC, P::UP_WPS>, up, dim3(64 * kMoeWaves),
                       p, 0, s) != hipSuccess)
     return GEMM_ERR_HIP;
-  return 4 * cdiv(a.H, 32) >= 3 * (int64_t)cus ? launch_down<WF, DT, MT, 2, P::UC_NS2>(a, s)
-                                               : launch_down<WF, DT, MT, 1, P::UC_NS1>(a, s);
+  const bool two = 4 * cdiv(a.H, 32) >= 3 * (int64_t)cus;
+  if constexpr (MT == 1) {
+    if (a.T <= 4 || a.T * a.k <= P::FEW_MEAN * a.E)
+      return two ? launch_down<WF, DT, MT, 2, P::FEW_UC_NS2, true>(a, s)
+                 : launch_down<WF, DT, MT, 1, P::UC_NS1, true>(a, s);
+  }
+  return two ? launch_down<WF, DT, MT, 2, P::UC_NS2, false>(a, s)
+             : launch_down<WF, DT, MT, 1, P::UC_NS1, false>(a, s);
 }
 
 template <int WF, int DT>

@@ -65,11 +65,11 @@ int check_mx4(const void* data, int64_t ldd, const void* scales, int64_t lds, in
 // K up to 2^36, as the 16-bit tiles: chunk counters stay far inside int64.
 constexpr int64_t kMaxK = INT64_C(1) << 36;
 
-template <int XF, int DT, int NS, int MT, int UC, int NW>
+template <int XF, int DT, int NS, int MT, int UC, int NW, bool FEW = false>
 int launch_strip(const StripArgs& a, hipStream_t s) {
   const int64_t gx = cdiv(a.N, 16 * NS), gy = cdiv(a.M, 16 * MT);
   StripArgs copy = a;
-  return run((const void*)mx4_strip_kernel<XF, DT, NS, MT, UC, NW>, dim3((unsigned)gx, (unsigned)gy), 64 * NW,
+  return run((const void*)mx4_strip_kernel<XF, DT, NS, MT, UC, NW, FEW>, dim3((unsigned)gx, (unsigned)gy), 64 * NW,
              &copy, s);
 }
 
@@ -85,7 +85,11 @@ bool strip_takes(const StripArgs& a) {
 // strip shares the A that the wave turns through LDS and each further tile of
 // rows the weights.  Measured (us per kernel in a graph of 50; NS = strips,
 // rows x N x K):
-//   16-bit A   1 x 2048 x 7168: NS 1 5.6, NS 2 6.9;  16 x 7168 x 2048: 5.1, 4.2
+//   16-bit A   up to 4 rows (FEW), bfloat16 unless said: 1 x 2048 x 7168: 4.4,
+//              without FEW 5.4; binary16: 5.3, 6.1; 1 x 7168 x 2048 binary16:
+//              NS 1 3.9, without 4.7; NS 2 4.0, 4.2; 1 x 28672 x 4096 binary16:
+//              NS 1 17.2, 19.6; NS 2 15.4, 16.6
+//              16 x 7168 x 2048: NS 1 5.1, NS 2 4.2
 //              32 x 7168 x 7168, 32 rows a wave: NS 1 15.7, 2 11.8, 4 15.8
 //              64 x 7168 x 7168, 32 rows: NS 1 28.0, 2 20.5, 4 16.5; 64 rows,
 //              NS 2: 20.1
@@ -102,6 +106,11 @@ int launch_strip_m(const StripArgs& a, hipStream_t s) {
   const int rc = device_cus(&cus);
   if (rc) return rc;
   const int64_t enough = 3 * (int64_t)cus / 4;
+  if constexpr (XF != SX_MX4) {
+    if (a.M <= 4)
+      return cdiv(a.N, 32) >= enough ? launch_strip<XF, DT, 2, 1, 1, 8, true>(a, s)
+                                     : launch_strip<XF, DT, 1, 1, 1, 8, true>(a, s);
+  }
   if (a.M <= 16) {
     if (cdiv(a.N, 32) >= enough) return launch_strip<XF, DT, 2, 1, 1, 8>(a, s);
     return launch_strip<XF, DT, 1, 1, XF == SX_MX4 ? 2 : 1, 8>(a, s);

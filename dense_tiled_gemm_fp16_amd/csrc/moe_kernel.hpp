@@ -158,16 +158,15 @@ struct MoeUp {
           wo.w[h * NI + n] = (uint32_t)((h * a.I + row) * a.w1_n) + 16 * (lane & 3);
           wo.s[h * NI + n] = (uint32_t)((h * a.I + srow) * a.s1_n);
         }
-      auto rows = [&](int t) {
-        const int p = 16 * t + (lane >> 2);
+      auto rows = [&](int p, int) {
         typename S::XPtr x;
         x.x = a.x;
-        x.xo = (uint32_t)(sh.list[p < m ? p : m - 1] * a.ldx) + 16 * (lane & 3);
+        x.xo = (uint32_t)(sh.list[p < m ? p : m - 1] * a.ldx);
         x.s = nullptr;
         x.so = 0;
         return x;
       };
-      S::run(acc, sh.wave[wave], w, wo, rows, 0, part, a.parts, a.H, tiles, lane);
+      S::run(acc, sh.wave[wave], w, wo, rows, 0, part, a.parts, a.H, m, lane);
     }
     __syncthreads();
 #pragma unroll
@@ -263,11 +262,12 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_up_kernel(MoeArgs a) 
   U::run(a, sh, e, lane, wave);
 }
 
-// What a workgroup of moe_down takes: NS strips of 16 columns of Y.
-template <int WF, int MT, int NS_, int UC>
+// What a workgroup of moe_down takes: NS strips of 16 columns of Y, 16 MT
+// tokens.  FEW: an expert seldom has more than four tokens (see Strip).
+template <int WF, int MT, int NS_, int UC, bool FEW>
 struct MoeDown {
   static constexpr int NS = NS_, NW = kMoeWaves;
-  using S = Strip<WF, WF == SW_F16 ? SX_F16P : SX_BF16P, NS, MT, UC, 1>;
+  using S = Strip<WF, WF == SW_F16 ? SX_F16P : SX_BF16P, NS, FEW ? 2 * MT : MT, UC, 1, FEW>;
   static constexpr int kPairs = 16 * MT * kMoeTopK;
 
   struct Shared {
@@ -283,9 +283,9 @@ struct MoeDown {
   };
 };
 
-template <int WF, int DT, int MT, int NS, int UC, int WPS>
+template <int WF, int DT, int MT, int NS, int UC, int WPS, bool FEW>
 __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a) {
-  using D = MoeDown<WF, MT, NS, UC>;
+  using D = MoeDown<WF, MT, NS, UC, FEW>;
   using S = typename D::S;
   constexpr int kPairs = D::kPairs;
   __shared__ typename D::Shared sh;
@@ -364,7 +364,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a
     const MoeArgs* a;
     const typename D::Shared* sh;
     int64_t h0;
-    int i, n, g, gpe, first, m, lane;     // group g of gpe of expert i of n
+    int i, n, g, gpe, first, m;     // group g of gpe of expert i of n
     __device__ __forceinline__ void at_expert() {
       while (g >= gpe && i < n) {
         g -= gpe;
@@ -386,29 +386,35 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a
       const int64_t e = __builtin_amdgcn_readfirstlane(sh->active[i]);
       return {a->w2 + e * a->w2_e + h0 * a->w2_n, a->s2 + e * a->s2_e + h0 * a->s2_n};
     }
-    __device__ __forceinline__ typename S::XPtr x(int t) const {
-      const int p = 16 * t + (lane >> 2);
+    __device__ __forceinline__ typename S::XPtr x(int p, int = 0) const {
       typename S::XPtr x;
       x.x = a->act;
-      x.xo = (sh->rows[first + (p < m ? p : m - 1)] & 0xFFFFu) * (uint32_t)a->act_row + 16 * (lane & 3);
+      x.xo = (sh->rows[first + (p < m ? p : m - 1)] & 0xFFFFu) * (uint32_t)a->act_row;
       x.s = nullptr;
       x.so = 0;
       return x;
     }
-    __device__ __forceinline__ int tiles() const { return (m + 15) / 16; }
+    __device__ __forceinline__ int rows() const { return m; }
   };
   {
     char* const lds = sh.wave[wave];
     const typename S::WOff wo = S::offsets(a.H - h0, 16, a.w2_n, a.s2_n, lane);
     const int gpe = (int)S::groups(a.I);
-    f32x4 acc[NS][MT];
+    f32x4 acc[NS][S::MT];
     S::clear(acc);
     // p times an expert's sums into the wave's accumulators.
     auto add = [&](const Cursor& cc) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int p = 16 * t + (lane & 15);
-        if (p < cc.m) {
+      for (int t = 0; t < S::MT; ++t) {
+        if constexpr (S::PACK) {
+          if (S::TR * t >= cc.m) break;
+#pragma unroll
+          for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[s][t][r] += __shfl_xor(acc[s][t][r], S::TR);
+        }
+        const int p = S::TR * t + (lane & 15);
+        if (p < cc.m && (lane & 15) < S::TR) {
           const uint32_t who = sh.rows[cc.first + p];
           const float prob = sh.prob[who & 0xFFFFu];
 #pragma unroll
@@ -422,7 +428,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a
       S::clear(acc);
     };
     if (gpe > 0) {
-      Cursor cur{&a, &sh, h0, 0, n, wave, gpe, 0, 0, lane};
+      Cursor cur{&a, &sh, h0, 0, n, wave, gpe, 0, 0};
       cur.at_expert();
       S::stream(acc, lds, cur, wo, a.act_part, a.I, lane, [&](const Cursor& cc) {
         if (cc.last()) add(cc);
@@ -430,7 +436,7 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a
     }
     if (S::rest(a.I))
       for (int i = wave; i < n; i += NW) {
-        Cursor cur{&a, &sh, h0, i, n, 0, gpe + 1, 0, 0, lane};
+        Cursor cur{&a, &sh, h0, i, n, 0, gpe + 1, 0, 0};
         cur.at_expert();
         cur.g = gpe;
         S::finish(acc, lds, cur, wo, a.act_part, a.I, lane);

@@ -106,8 +106,10 @@ __device__ __forceinline__ void wave_order() {
 
 // NS strips of 16 weight rows x MT tiles of 16 rows of A, UC chunks at a time.
 // XT: tiles of A that run ahead; the others are fetched when they are needed
-// (see more_tiles).
-template <int WF, int XF, int NS_, int MT_, int UC_, int XT = MT_>
+// (see more_tiles).  FEW: of the first tile only the first FR rows run ahead,
+// one row's pieces of the whole group side by side in a load (a quarter of the
+// loads and LDS writes), the others are fetched when there are any.
+template <int WF, int XF, int NS_, int MT_, int UC_, int XT = MT_, bool FEW_ = false>
 struct Strip {
   static constexpr int NS = NS_, MT = MT_, UC = UC_;
   static constexpr bool W4 = WF == SW_MX4, X4 = XF == SX_MX4;
@@ -116,8 +118,20 @@ struct Strip {
   static constexpr int XV = X4 ? 1 : (W4 ? 4 : 1);          // 64-byte pieces of A per chunk, row and part
   static_assert(W4 || !X4, "MX4 A takes MX4 weights");
   static_assert(XT == 1 || XT == MT_, "one tile ahead, or all");
-  // A wave's LDS: the group's weights, one chunk of one part of A, scales.
-  static constexpr int X_AT = UC * NS * 1024, S_AT = X_AT + XV * 1024, XS_AT = S_AT + (W4 ? NS * 16 * UC * 4 : 0);
+  static constexpr bool FEW = FEW_;
+  // FEW: pieces of 16 bytes per row of A in a group, rows per load, rows and
+  // loads that run ahead.
+  static constexpr int PR = 4 * UC * PL * XV, RPL = 64 / PR, FR = RPL > 4 ? RPL : 4, FL = FR / RPL;
+  static_assert(!FEW || (XT == 1 && !X4 && PR >= 8 && PR <= 64), "a load takes whole rows");
+  // FEW with two parts: a tile is 8 rows, columns c and c + 8 of the products
+  // are the first and the second part of row c (to be added in the end), so the
+  // parts share an instruction.
+  static constexpr bool PACK = FEW && PL == 2;
+  static constexpr int PM = PACK ? 1 : PL, TR = PACK ? 8 : 16;   // products per octet; rows of a tile
+  // A wave's LDS: the group's weights, one chunk of one part of A (FEW: 16 rows
+  // of the whole group), scales.
+  static constexpr int X_AT = UC * NS * 1024, S_AT = X_AT + (FEW ? TR * 16 * PR : XV * 1024),
+                       XS_AT = S_AT + (W4 ? NS * 16 * UC * 4 : 0);
   static constexpr int LDS = XS_AT + (X4 ? 16 * UC * 4 : 0);
 
   // A uniform address and the lane's 32-bit offset beside it, so that moving
@@ -133,8 +147,8 @@ struct Strip {
   struct XPtr {
     const char* x;            // uniform, as for the weights
     const uint8_t* s;
-    uint32_t xo;              // row lane / 4 of a tile, piece lane % 4
-    uint32_t so;              // scales of row lane % 16 (MX4 A)
+    uint32_t xo;              // the lane's row
+    uint32_t so;              // scales of row lane % 16 of its tile (MX4 A)
   };
 
   // Offsets of strips that start `stride` rows apart, `rows` rows from the
@@ -160,6 +174,10 @@ struct Strip {
     u32x4 x[UC][PL][XV];
     uint32_t xs[UC];
   };
+  struct XFew {
+    u32x4 x[FL];
+  };
+  using XAhead = std::conditional_t<FEW, XFew, XRegs>;
 
   static __device__ __forceinline__ int64_t chunks(int64_t K) { return (K + CK - 1) / CK; }
 
@@ -189,14 +207,15 @@ struct Strip {
       for (int s = 0; s < NS; ++s) load_dwords(b.s[s], sp + o.s[s]);
     }
   }
-  static __device__ __forceinline__ void load_x(XRegs& b, const XPtr& p, int64_t xpart, int64_t c) {
+  static __device__ __forceinline__ void load_x(XRegs& b, const XPtr& p, int64_t xpart, int64_t c, int lane) {
     const char* x = uniform_ptr(p.x + c * (64 * XV));
+    const uint32_t xo = p.xo + 16 * (lane & 3);
 #pragma unroll
     for (int u = 0; u < UC; ++u)
 #pragma unroll
       for (int q = 0; q < PL; ++q)
 #pragma unroll
-        for (int j = 0; j < XV; ++j) b.x[u][q][j] = load16(x + q * xpart + p.xo + u * (64 * XV) + 64 * j);
+        for (int j = 0; j < XV; ++j) b.x[u][q][j] = load16(x + q * xpart + xo + u * (64 * XV) + 64 * j);
     if constexpr (X4) load_dwords(b.xs, uniform_ptr((const char*)p.s + 4 * c) + p.so);
   }
 
@@ -226,14 +245,14 @@ struct Strip {
       const int64_t cc = c + u;
       if constexpr (X4) {
         const int64_t left = K - (4 * cc + piece) * 32;
-        b.x[u][0][0] = left > 0 ? mask_codes(load16(p.x + cc * 64 + p.xo), left < 32 ? (int)left : 32) : zero4();
+        b.x[u][0][0] = left > 0 ? mask_codes(load16(p.x + cc * 64 + p.xo + 16 * piece), left < 32 ? (int)left : 32) : zero4();
         b.xs[u] = scales_rest(p.s + 4 * cc + p.so, cc, K);
       } else {
 #pragma unroll
         for (int q = 0; q < PL; ++q)
 #pragma unroll
           for (int j = 0; j < XV; ++j)
-            b.x[u][q][j] = load8_rest(p.x + cc * (64 * XV) + q * xpart + p.xo + 64 * j,
+            b.x[u][q][j] = load8_rest(p.x + cc * (64 * XV) + q * xpart + p.xo + 64 * j + 16 * piece,
                                       K - (cc * CK + 32 * j + 8 * piece));
       }
     }
@@ -283,7 +302,7 @@ struct Strip {
 
   // A tile's octets of the whole group.
   struct XFrags {
-    u32x4 f[UC][PL][XV];
+    u32x4 f[UC][PM][XV];
     uint32_t s[UC];
   };
   static __device__ __forceinline__ void turn(XFrags& f, char* lds, const XRegs& b, int lane) {
@@ -300,6 +319,56 @@ struct Strip {
       for (int q = 0; q < PL; ++q) turn_x(lds, b, u, q, f.f[u][q], lane);
       if constexpr (X4) f.s[u] = *(const uint32_t*)(lds + XS_AT + ((lane & 15) * UC + u) * 4) >> (8 * (lane >> 4));
     }
+  }
+
+  // FEW: lane l takes piece l % PR of row l / PR of a load; pieces of a row count
+  // chunk, part, octet.  In LDS a row's pieces lie side by side, piece p of row
+  // r in slot p ^ (r % 8): both sides free of bank conflicts.
+  template <bool REST, class Cursor>
+  static __device__ __forceinline__ void load_few(XFew& b, const Cursor& cc, int row, int64_t xpart, int64_t K,
+                                                  int lane) {
+    const int piece = lane % PR, w = piece % (4 * XV), u = piece / (4 * XV * PL), q = piece / (4 * XV) % PL;
+    const uint32_t off = (uint32_t)(q * xpart) + u * (64 * XV) + 16 * w;
+#pragma unroll
+    for (int i = 0; i < FL; ++i) {
+      const XPtr p = cc.x(row + i * RPL + lane / PR);
+      const char* x = uniform_ptr(p.x + cc.c() * (64 * XV));
+      if constexpr (REST)
+        b.x[i] = load8_rest(x + (p.xo + off), K - ((cc.c() + u) * CK + 8 * w));
+      else
+        b.x[i] = load16(x + (p.xo + off));
+    }
+  }
+  static __device__ __forceinline__ void store_few(char* lds, const XFew& b, int row, int lane) {
+#pragma unroll
+    for (int i = 0; i < FL; ++i) {
+      const int r = row + i * RPL + lane / PR;
+      *(u32x4*)(lds + X_AT + r * (16 * PR) + ((lane % PR ^ (r & 7)) << 4)) = b.x[i];
+    }
+  }
+  // Rows `row` .. of tile t, fetched now.
+  template <bool REST, class Cursor>
+  static __device__ __forceinline__ void fetch_few(char* lds, const Cursor& cc, int t, int row, int64_t xpart,
+                                                   int64_t K, int lane) {
+    const int rows = cc.rows() - TR * t;
+    for (; row < TR && row < rows; row += FR) {
+      XFew b;
+      load_few<REST>(b, cc, TR * t + row, xpart, K, lane);
+      store_few(lds, b, row, lane);
+    }
+  }
+  static __device__ __forceinline__ void read_few(XFrags& f, const char* lds, int lane) {
+    wave_order();
+    const int r = lane & (TR - 1), g = lane >> 4, part = PACK ? (lane & 15) / TR : 0;
+#pragma unroll
+    for (int u = 0; u < UC; ++u)
+#pragma unroll
+      for (int q = 0; q < PM; ++q)
+#pragma unroll
+        for (int j = 0; j < XV; ++j) {
+          const int p = (u * PL + q + part) * (4 * XV) + (XV == 1 ? g : 4 * g + j);
+          f.f[u][q][j] = *(const u32x4*)(lds + X_AT + r * (16 * PR) + ((p ^ (r & 7)) << 4));
+        }
   }
 
   // Products of the staged group with tile T of A, no branch between the
@@ -348,7 +417,7 @@ struct Strip {
               } else {
                 const bf16x8 wf = mx4_to_bf16(w[s][j], scale_f32(sb[s]));
 #pragma unroll
-                for (int q = PL - 1; q >= 0; --q)   // the smaller part first
+                for (int q = PM - 1; q >= 0; --q)   // the smaller part first
                   acc[s][T] = mfma16(wf, as8<bf16x8>(x.f[u][q][j]), acc[s][T]);
               }
             }
@@ -357,7 +426,7 @@ struct Strip {
       } else {
         using V = std::conditional_t<WF == SW_F16, f16x8, bf16x8>;
 #pragma unroll
-        for (int q = PL - 1; q >= 0; --q)
+        for (int q = PM - 1; q >= 0; --q)
 #pragma unroll
           for (int s = 0; s < NS; ++s) acc[s][T] = mfma16(as8<V>(w[s]), as8<V>(x.f[u][q][0]), acc[s][T]);
       }
@@ -406,25 +475,37 @@ struct Strip {
   static __device__ __forceinline__ void more_tiles(f32x4 (&acc)[NS][MT], char* lds, const Cursor& cc, int64_t xpart,
                                                     int64_t K, bool is_wide, int lane) {
     if constexpr (T < MT && XT == 1) {
-      if (T < cc.tiles()) {
-        XRegs b;
+      if (TR * T < cc.rows()) {
         XFrags x;
-        if constexpr (REST)
-          load_x_rest(b, cc.x(T), xpart, cc.c(), K, lane);
-        else
-          load_x(b, cc.x(T), xpart, cc.c());
-        turn(x, lds, b, lane);
+        if constexpr (FEW) {
+          wave_order();
+          fetch_few<REST>(lds, cc, T, 0, xpart, K, lane);
+          read_few(x, lds, lane);
+        } else {
+          XRegs b;
+          if constexpr (REST)
+            load_x_rest(b, tile(cc, T, lane), xpart, cc.c(), K, lane);
+          else
+            load_x(b, tile(cc, T, lane), xpart, cc.c(), lane);
+          turn(x, lds, b, lane);
+        }
         mma<T>(acc, lds, x, is_wide, lane);
         more_tiles<T + 1, REST>(acc, lds, cc, xpart, K, is_wide, lane);
       }
     }
   }
 
+  // This lane's rows of tile t.
+  template <class Cursor>
+  static __device__ __forceinline__ XPtr tile(const Cursor& cc, int t, int lane) {
+    return cc.x(16 * t + (lane >> 2), 16 * t + (lane < 16 ? lane : 0));
+  }
+
   // Runs over a sequence of whole groups with three cursors on it, of one type:
   // one for the weights (two groups ahead), one for A (one ahead), one for the
   // products.  A cursor has bool more(), void next(), int64_t c() (the group's
-  // first chunk), WPtr w(), XPtr x(int tile), int tiles(); done(cursor) is called
-  // after each group's products.  The cursors that run ahead stop at the last
+  // first chunk), WPtr w(), XPtr x(int row, int scale_row), int rows();
+  // done(cursor) is called after each group's products.  The cursors that run ahead stop at the last
   // group and load it again.
   template <class Cursor, class Done>
   static __device__ __forceinline__ void stream(f32x4 (&acc)[NS][MT], char* lds, Cursor cc, const WOff& wo,
@@ -437,11 +518,18 @@ struct Strip {
       if (n.more()) c = n;
     };
     WRegs w0, w1;
-    XRegs x[XT];
+    XAhead x[XT];
+    auto load_ahead = [&] {
+      if constexpr (FEW) {
+        load_few<false>(x[0], xc, 0, xpart, K, lane);
+      } else {
+#pragma unroll
+        for (int t = 0; t < XT; ++t) load_x(x[t], tile(xc, t, lane), xpart, xc.c(), lane);
+      }
+    };
     load_w(w0, wc.w(), wo, wc.c());
     ahead(wc);
-#pragma unroll
-    for (int t = 0; t < XT; ++t) load_x(x[t], xc.x(t), xpart, xc.c());
+    load_ahead();
     ahead(xc);
     load_w(w1, wc.w(), wo, wc.c());
     ahead(wc);
@@ -449,10 +537,15 @@ struct Strip {
       XFrags f[XT];
       stage_w(lds, w, lane);
       const bool is_wide = wide(w, lane);
+      if constexpr (FEW) {
+        store_few(lds, x[0], 0, lane);
+        fetch_few<false>(lds, cc, 0, FR, xpart, K, lane);
+        read_few(f[0], lds, lane);
+      } else {
 #pragma unroll
-      for (int t = 0; t < XT; ++t) turn(f[t], lds, x[t], lane);
-#pragma unroll
-      for (int t = 0; t < XT; ++t) load_x(x[t], xc.x(t), xpart, xc.c());
+        for (int t = 0; t < XT; ++t) turn(f[t], lds, x[t], lane);
+      }
+      load_ahead();
       ahead(xc);
       load_w(w, wc.w(), wo, wc.c());
       ahead(wc);
@@ -479,11 +572,16 @@ struct Strip {
     load_w_rest(w, cc.w(), wo, cc.c(), K, lane);
     stage_w(lds, w, lane);
     const bool is_wide = wide(w, lane);
+    if constexpr (FEW) {
+      fetch_few<true>(lds, cc, 0, 0, xpart, K, lane);
+      read_few(f[0], lds, lane);
+    } else {
 #pragma unroll
-    for (int t = 0; t < XT; ++t) {
-      XRegs x;
-      load_x_rest(x, cc.x(t), xpart, cc.c(), K, lane);
-      turn(f[t], lds, x, lane);
+      for (int t = 0; t < XT; ++t) {
+        XRegs x;
+        load_x_rest(x, tile(cc, t, lane), xpart, cc.c(), K, lane);
+        turn(f[t], lds, x, lane);
+      }
     }
     mma_all<0>(acc, lds, f, is_wide, lane);
     more_tiles<1, true>(acc, lds, cc, xpart, K, is_wide, lane);
@@ -494,26 +592,26 @@ struct Strip {
   struct Line {
     int64_t g, n, stride;
     const WPtr* wp;
-    const Rows* rows;
-    int n_tiles;
+    const Rows* addr;
+    int n_rows;
     __device__ __forceinline__ bool more() const { return g < n; }
     __device__ __forceinline__ void next() { g += stride; }
     __device__ __forceinline__ int64_t c() const { return g * UC; }
     __device__ __forceinline__ const WPtr& w() const { return *wp; }
-    __device__ __forceinline__ XPtr x(int t) const { return (*rows)(t); }
-    __device__ __forceinline__ int tiles() const { return n_tiles; }
+    __device__ __forceinline__ XPtr x(int row, int scale_row = 0) const { return (*addr)(row, scale_row); }
+    __device__ __forceinline__ int rows() const { return n_rows; }
   };
 
-  // Part `part` of `parts` of the sums over K, for `tiles` tiles of A whose rows
-  // rows(t) gives.  The parts take the groups in turn, the partial one too.
+  // Part `part` of `parts` of the sums over K, for n_rows rows of A whose
+  // addresses addr(row, scale_row) gives.  The parts take the groups in turn, the partial one too.
   template <class Rows>
   static __device__ __forceinline__ void run(f32x4 (&acc)[NS][MT], char* lds, const WPtr& wp, const WOff& wo,
-                                             const Rows& rows, int64_t xpart, int part, int parts, int64_t K,
-                                             int tiles, int lane) {
+                                             const Rows& addr, int64_t xpart, int part, int parts, int64_t K,
+                                             int n_rows, int lane) {
     const int64_t n = groups(K);
-    stream(acc, lds, Line<Rows>{part, n, parts, &wp, &rows, tiles}, wo, xpart, K, lane, [](const Line<Rows>&) {});
+    stream(acc, lds, Line<Rows>{part, n, parts, &wp, &addr, n_rows}, wo, xpart, K, lane, [](const Line<Rows>&) {});
     if (rest(K) && part == (int)(n % parts))
-      finish(acc, lds, Line<Rows>{n, n + 1, parts, &wp, &rows, tiles}, wo, xpart, K, lane);
+      finish(acc, lds, Line<Rows>{n, n + 1, parts, &wp, &addr, n_rows}, wo, xpart, K, lane);
   }
 };
 
@@ -544,9 +642,9 @@ struct StripArgs {
 
 // C[m,n] = sum_k A[m,k] B[n,k] with MX4 B: workgroup -> (16 NS columns of C,
 // 16 MT rows), its NW waves the ranges of K.
-template <int XF, int DT, int NS, int MT, int UC, int NW>
+template <int XF, int DT, int NS, int MT, int UC, int NW, bool FEW = false>
 __global__ __launch_bounds__(64 * NW) void mx4_strip_kernel(StripArgs a) {
-  using S = Strip<SW_MX4, XF, NS, MT, UC>;
+  using S = Strip<SW_MX4, XF, NS, MT, UC, MT, FEW>;
   constexpr int TILES = NS * MT;
   __shared__ union {
     char wave[NW][S::LDS];
@@ -557,21 +655,19 @@ __global__ __launch_bounds__(64 * NW) void mx4_strip_kernel(StripArgs a) {
   const typename S::WPtr w{a.b + n0 * a.ldb, a.bs + n0 * a.ldbs};
   const typename S::WOff wo = S::offsets(a.N - n0, 16, a.ldb, a.ldbs, lane);
   const int64_t left = a.M - m0;
-  auto rows = [&](int t) {
-    int64_t m = 16 * t + (lane >> 2), ms = 16 * t + (lane < 16 ? lane : 0);
+  auto rows = [&](int row, int scale_row) {
+    const int64_t m = row < left ? row : left - 1, ms = scale_row < left ? scale_row : left - 1;
     typename S::XPtr x;
-    if (m >= left) m = left - 1;
-    if (ms >= left) ms = left - 1;
     x.x = a.a + m0 * a.lda;
     x.s = S::X4 ? a.as + m0 * a.ldas : nullptr;
-    x.xo = (uint32_t)(m * a.lda) + 16 * (lane & 3);
+    x.xo = (uint32_t)(m * a.lda);
     x.so = (uint32_t)(ms * a.ldas);
     return x;
   };
   f32x4 acc[NS][MT];
   S::clear(acc);
   S::run(acc, sh.wave[wave], w, wo, rows, 0, wave, NW, a.K,
-         left >= 16 * MT ? MT : (int)((left + 15) / 16), lane);
+         left >= 16 * MT ? 16 * MT : (int)left, lane);
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NS; ++i)

@@ -141,6 +141,22 @@ def test_unused_experts_are_not_read_into_sums():
     la.check(la.run())
 
 
+@pytest.mark.parametrize("weights", ["16", "mx4"])
+@pytest.mark.parametrize("T", [5, 8, 9, 13, 16, 48])
+@pytest.mark.parametrize("H", [100, 6150])
+def test_an_expert_of_all_tokens(T, H, weights):
+    """Few tokens per expert on the average, one expert with all of them."""
+    E = max(16, T)
+    la = Layer(T, E, 2, H, 300, "bf16", weights)
+    la.logits[:, 3] = 30.0
+    la.logits[:, 3] += torch.arange(T, device=DEV)
+    la.logits[: T // 2, 7] = 31.0
+    say(f"moe one expert of all {T} {H} {weights}")
+    y = la.run()
+    la.check(y)
+    assert torch.equal(la.run(), y)
+
+
 def test_expert_views():
     """Every second expert of a larger stack, rows with a stride of their own."""
     la = Layer(4, 10, 2, 64, 48, "bf16", "16")

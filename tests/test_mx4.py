@@ -173,7 +173,7 @@ SHAPES = [(1, 1, 1), (1, 16, 32), (3, 17, 33), (5, 70, 128), (16, 33, 130), (17,
           (33, 31, 1000), (64, 48, 96), (65, 20, 700), (200, 130, 257), (1, 300, 7168), (130, 257, 2048),
           (300, 264, 1025), (257, 513, 640),
           # enough columns (on 256 compute units) for several strips a wave, K of less and of more than a group
-          (16, 6150, 161), (1, 6200, 1000), (40, 6150, 289), (33, 3100, 513), (100, 6200, 257), (100, 10300, 97),
+          (16, 6150, 161), (1, 6200, 1000), (40, 6150, 289), (33, 3100, 513), (4, 6150, 600), (4, 70, 500), (100, 6200, 257), (100, 10300, 97),
           # enough rows and columns for 256 x 256 tiles: whole steps only, a partial one only, both, edges of
           # nearly empty tiles
           (1801, 1543, 640), (1801, 1543, 33), (1543, 1801, 1025), (130, 12500, 257), (12500, 130, 96),
