@@ -62,6 +62,23 @@ int check_mx4(const void* data, int64_t ldd, const void* scales, int64_t lds, in
   return GEMM_OK;
 }
 
+// How rows of octs octets are dealt to wave items; returns their number.
+int64_t wave_items(int64_t rows, int64_t octs, int64_t* segs, Short* few) {
+  *segs = cdiv(octs, kSlots);
+  *few = Short{};
+  if (*segs > 1 || rows == 1) return rows * *segs;
+  *few = Short{(int32_t)octs, (int32_t)(kSlots / octs), (int32_t)(65536 / octs + 1)};
+  return cdiv(rows, few->rows);
+}
+template <int FMT>
+const void* rows_kernel(const Short& few) {
+  return few.rows ? (const void*)quantize_rows_kernel<FMT, true> : (const void*)quantize_rows_kernel<FMT, false>;
+}
+template <int FMT>
+const void* back_kernel(const Short& few) {
+  return few.rows ? (const void*)dequantize_kernel<FMT, true> : (const void*)dequantize_kernel<FMT, false>;
+}
+
 // K up to 2^36, as the 16-bit tiles: chunk counters stay far inside int64.
 constexpr int64_t kMaxK = INT64_C(1) << 36;
 
@@ -206,23 +223,24 @@ int gemm_mx4_quantize(const void* X, int32_t fmt, int64_t ldx_g, int64_t ldx_r, 
   if (rc) return rc;
   if (overlap(rx, rd) || overlap(rx, rs) || overlap(rd, rs)) return GEMM_ERR_ALIAS;
 
-  QuantArgs a{X, ldx_g, ldx_r, ldx_k, G, R, K, (uint8_t*)data, (uint8_t*)scales, Kb, 1, 1};
+  QuantArgs a{X, ldx_g, ldx_r, ldx_k, G, R, K, (uint8_t*)data, (uint8_t*)scales, Kb, 1, {}};
+  if (G > 1 && ldx_g == R * ldx_r) {   // one stack of rows
+    a.G = 1;
+    a.R = rows;
+  }
   int64_t waves;
   const void* fn;
   if (ldx_k == 1) {
     // Dense rows of whole blocks are one long row.
-    if (K % kMxBlock == 0 && ldx_r == K && (G == 1 || ldx_g == R * K)) {
-      a.G = a.R = 1;
+    if (K % kMxBlock == 0 && ldx_r == K && a.G == 1) {
+      a.R = 1;
       a.K = rows * K;
       a.Kb = rows * Kb;
     }
-    const int64_t octs = 4 * a.Kb;
-    a.segs = cdiv(octs, 64 * kQuantU);
-    a.rpw = octs <= 32 ? (int32_t)(64 / octs) : 1;
-    waves = a.rpw > 1 ? cdiv(a.G * a.R, a.rpw) : a.G * a.R * a.segs;
-    fn = fmt == GEMM_FMT_F16    ? (const void*)quantize_rows_kernel<MX_F16>
-         : fmt == GEMM_FMT_BF16 ? (const void*)quantize_rows_kernel<MX_BF16>
-                                : (const void*)quantize_rows_kernel<MX_F32>;
+    waves = wave_items(a.G * a.R, 4 * a.Kb, &a.segs, &a.few);
+    fn = fmt == GEMM_FMT_F16    ? rows_kernel<MX_F16>(a.few)
+         : fmt == GEMM_FMT_BF16 ? rows_kernel<MX_BF16>(a.few)
+                                : rows_kernel<MX_F32>(a.few);
   } else {
     waves = cdiv(rows, 64) * Kb;
     fn = fmt == GEMM_FMT_F16    ? (const void*)quantize_columns_kernel<MX_F16>
@@ -249,21 +267,17 @@ int gemm_mx4_dequantize(const void* data, int64_t ldd, const void* scales, int64
   if (ry.hi < ry.lo) return GEMM_ERR_SHAPE;
   if (overlap(ry, rd) || overlap(ry, rs)) return GEMM_ERR_ALIAS;
 
-  DequantArgs a{(const uint8_t*)data, ldd, (const uint8_t*)scales, lds, R, K, Y, ldy, 1, 1};
+  DequantArgs a{(const uint8_t*)data, ldd, (const uint8_t*)scales, lds, R, K, Y, ldy, 1, {}};
   const int64_t kb = cdiv(K, kMxBlock);
   if (K % kMxBlock == 0 && ldy == K && ldd == kb * kMxBytes && lds == kb) {   // one long row
     a.R = 1;
     a.K = R * K;
   }
-  const int64_t octs = cdiv(a.K, 8);
-  a.segs = cdiv(octs, 64 * kQuantU);
-  a.rpw = octs <= 32 ? (int32_t)(64 / octs) : 1;
-  const int64_t waves = a.rpw > 1 ? cdiv(a.R, a.rpw) : a.R * a.segs;
-  const int64_t grid = cdiv(waves, 4);
+  const int64_t grid = cdiv(wave_items(a.R, cdiv(a.K, 8), &a.segs, &a.few), 4);
   if (grid > kMaxWide) return GEMM_ERR_SHAPE;
-  const void* fn = fmt == GEMM_FMT_F16    ? (const void*)dequantize_kernel<MX_F16>
-                   : fmt == GEMM_FMT_BF16 ? (const void*)dequantize_kernel<MX_BF16>
-                                          : (const void*)dequantize_kernel<MX_F32>;
+  const void* fn = fmt == GEMM_FMT_F16    ? back_kernel<MX_F16>(a.few)
+                   : fmt == GEMM_FMT_BF16 ? back_kernel<MX_BF16>(a.few)
+                                          : back_kernel<MX_F32>(a.few);
   return run(fn, wide_grid(grid), 256, &a, (hipStream_t)stream);
 }
 

@@ -7,8 +7,8 @@
 //   rows     k is the contiguous axis.  A lane takes 8 consecutive elements
 //            (one 16-byte load of a 16-bit type), four neighbouring lanes a
 //            block; the block's largest magnitude goes round the four with
-//            two lane exchanges.  A wave has U such loads in flight.  Rows
-//            shorter than a wave's 512 elements share one (rpw rows a wave).
+//            two lane exchanges.  A wave has U such loads in flight; rows
+//            of up to their 2048 elements share them.
 //   columns  any other strides: a lane owns a row and walks the 32 elements of
 //            a block, so that with rows contiguous a wave's loads cover 64
 //            consecutive elements; no lane exchange is needed.
@@ -26,6 +26,14 @@ namespace gemmf16 {
 
 enum MxFormat { MX_F16 = 0, MX_BF16 = 1, MX_F32 = 2 };
 
+// Rows of at most kSlots octets: a wave item takes `rows` of them, slot i octet
+// i % octs of row i / octs, the division by a 16-bit reciprocal (exact for
+// i < 256: i times its error stays below 1 / 256).
+constexpr int kQuantU = 4, kSlots = 64 * kQuantU;   // octets in flight: U per lane
+struct Short {
+  int32_t octs, rows, inv;
+};
+
 struct QuantArgs {
   const void* x;
   int64_t s_g, s_r, s_k;   // element strides
@@ -34,7 +42,7 @@ struct QuantArgs {
   uint8_t* scales;         // [G R, Kb]
   int64_t Kb;              // blocks per row
   int64_t segs;            // rows: wave items per row
-  int32_t rpw;             // rows: rows per wave (1 when a row fills a wave)
+  Short few;               // rows: several rows per wave item
 };
 
 template <int FMT>
@@ -119,36 +127,47 @@ __device__ __forceinline__ int64_t wave_item() {
   return ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 }
 
-constexpr int kQuantU = 4;   // wave items of 64 lanes x 8 elements in flight
+// Where a lane's u-th octet of a wave item lies.
+struct Place {
+  int64_t row, o;
+  bool ok;
+};
+template <bool SHORT>
+__device__ __forceinline__ Place place(int64_t w, int u, int lane, int64_t rows, int64_t octs, int64_t segs,
+                                       const Short& few) {
+  const int slot = 64 * u + lane;
+  Place p;
+  if constexpr (SHORT) {
+    const int sub = (slot * few.inv) >> 16;
+    p.row = w * few.rows + sub;
+    p.o = slot - sub * few.octs;
+    p.ok = sub < few.rows && p.row < rows;
+  } else {
+    p.row = w / segs;
+    p.o = (w - p.row * segs) * kSlots + slot;
+    p.ok = p.row < rows && p.o < octs;
+  }
+  return p;
+}
 
-// Rows with unit k stride.  Wave item w: row (or rpw rows) w / segs, octets
-// (w % segs) 64 U .. of it.
-template <int FMT>
+// Rows with unit k stride.  Wave item w: several rows (SHORT), or kSlots octets
+// of row w / segs.
+template <int FMT, bool SHORT>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t w = wave_item();
   const int64_t rows = a.G * a.R, octs = 4 * a.Kb;
-  int64_t row = w / a.segs, o0 = (w - row * a.segs) * (64 * kQuantU) + lane;
-  bool mine = true;
-  if (a.rpw > 1) {                     // several short rows in one wave
-    const int sub = lane / (int)octs;
-    mine = sub < a.rpw;
-    row = w * a.rpw + sub;
-    o0 = lane - sub * (int)octs;
-  }
-  if (row >= rows) mine = false;
-  const int64_t g = a.G == 1 ? 0 : row / a.R, r = row - g * a.R;
-  const char* base = (const char*)a.x + (g * a.s_g + r * a.s_r) * Oct<FMT>::ES;
-  const int nu = a.rpw > 1 ? 1 : kQuantU;
   Oct<FMT> v[kQuantU];
 #pragma unroll
   for (int u = 0; u < kQuantU; ++u) {
-    const int64_t o = o0 + 64 * u;
-    v[u].load(base, 8 * o, mine && u < nu && o < octs ? a.K - 8 * o : 0);
+    const Place p = place<SHORT>(w, u, lane, rows, octs, a.segs, a.few);
+    const int64_t g = a.G == 1 ? 0 : p.row / a.R, r = p.row - g * a.R;
+    const char* base = (const char*)a.x + (g * a.s_g + r * a.s_r) * Oct<FMT>::ES;
+    v[u].load(base, 8 * p.o, p.ok ? a.K - 8 * p.o : 0);
   }
 #pragma unroll
   for (int u = 0; u < kQuantU; ++u) {
-    const int64_t o = o0 + 64 * u;
+    const Place p = place<SHORT>(w, u, lane, rows, octs, a.segs, a.few);
     float f[8];
     uint32_t m = 0;
 #pragma unroll
@@ -163,9 +182,9 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
     n = __shfl_xor(m, 2);
     m = n > m ? n : m;
     const uint32_t s = scale_of(m);
-    if (mine && u < nu && o < octs) {
-      gstore(a.data + (row * octs + o) * 4, to_codes(f, s));
-      if ((o & 3) == 0) gstore<uint8_t>(a.scales + row * a.Kb + (o >> 2), (uint8_t)s);
+    if (p.ok) {
+      gstore(a.data + (p.row * octs + p.o) * 4, to_codes(f, s));
+      if ((p.o & 3) == 0) gstore<uint8_t>(a.scales + p.row * a.Kb + (p.o >> 2), (uint8_t)s);
     }
   }
 }
@@ -219,42 +238,30 @@ struct DequantArgs {
   void* y;
   int64_t ldy;     // elements
   int64_t segs;
-  int32_t rpw;
+  Short few;
 };
 
 // As quantize_rows_kernel: a lane turns 8 codes (4 bytes) into 8 elements.
-template <int FMT>
+template <int FMT, bool SHORT>
 __global__ __launch_bounds__(256) void dequantize_kernel(DequantArgs a) {
   constexpr int ES = FMT == MX_F32 ? 4 : 2;
   const int lane = threadIdx.x & 63;
   const int64_t w = wave_item();
   const int64_t octs = (a.K + 7) / 8;
-  int64_t row = w / a.segs, o0 = (w - row * a.segs) * (64 * kQuantU) + lane;
-  bool mine = true;
-  if (a.rpw > 1) {
-    const int sub = lane / (int)octs;
-    mine = sub < a.rpw;
-    row = w * a.rpw + sub;
-    o0 = lane - sub * (int)octs;
-  }
-  if (row >= a.R) mine = false;
-  const int nu = a.rpw > 1 ? 1 : kQuantU;
-  const uint8_t* d = a.data + row * a.ldd;
-  const uint8_t* sc = a.scales + row * a.lds;
-  char* y = (char*)a.y + row * a.ldy * ES;
   uint32_t c[kQuantU], s[kQuantU];
 #pragma unroll
   for (int u = 0; u < kQuantU; ++u) {
-    const int64_t o = o0 + 64 * u;
-    const bool ok = mine && u < nu && o < octs;
+    const Place p = place<SHORT>(w, u, lane, a.R, octs, a.segs, a.few);
     c[u] = 0;
-    if (ok) c[u] = gload<uint32_t>(d + 4 * o);
-    s[u] = ok ? gload<uint8_t>(sc + (o >> 2)) : 127;
+    if (p.ok) c[u] = gload<uint32_t>(a.data + p.row * a.ldd + 4 * p.o);
+    s[u] = p.ok ? gload<uint8_t>(a.scales + p.row * a.lds + (p.o >> 2)) : 127;
   }
 #pragma unroll
   for (int u = 0; u < kQuantU; ++u) {
-    const int64_t o = o0 + 64 * u;
-    if (!(mine && u < nu && o < octs)) continue;
+    const Place p = place<SHORT>(w, u, lane, a.R, octs, a.segs, a.few);
+    if (!p.ok) continue;
+    const int64_t o = p.o;
+    char* y = (char*)a.y + p.row * a.ldy * ES;
     const float f = scale_f32(s[u]);
     const int64_t left = a.K - 8 * o;
     char* q = y + 8 * o * ES;
