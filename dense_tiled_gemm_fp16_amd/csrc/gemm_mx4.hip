@@ -38,7 +38,7 @@ bool overlap(const Range& a, const Range& b) { return ranges_overlap(a.lo, a.hi,
 // A launch takes fewer than 2^32 work items along x.
 bool fits_x(int64_t gx, int threads) { return gx < (INT64_C(1) << 32) / threads; }
 
-// n workgroups of 256 as a grid that a launch takes (rounded up).
+// n workgroups (of up to 512) as a grid that a launch takes (rounded up).
 dim3 wide_grid(int64_t n) {
   constexpr int64_t kX = INT64_C(1) << 22;
   return n <= kX ? dim3((unsigned)n) : dim3((unsigned)kX, (unsigned)cdiv(n, kX));
@@ -228,7 +228,8 @@ int gemm_mx4_quantize(const void* X, int32_t fmt, int64_t ldx_g, int64_t ldx_r, 
     a.G = 1;
     a.R = rows;
   }
-  int64_t waves;
+  int64_t grid;
+  int threads = 256;
   const void* fn;
   if (ldx_k == 1) {
     // Dense rows of whole blocks are one long row.
@@ -237,19 +238,20 @@ int gemm_mx4_quantize(const void* X, int32_t fmt, int64_t ldx_g, int64_t ldx_r, 
       a.K = rows * K;
       a.Kb = rows * Kb;
     }
-    waves = wave_items(a.G * a.R, 4 * a.Kb, &a.segs, &a.few);
+    grid = cdiv(wave_items(a.G * a.R, 4 * a.Kb, &a.segs, &a.few), 4);
     fn = fmt == GEMM_FMT_F16    ? rows_kernel<MX_F16>(a.few)
          : fmt == GEMM_FMT_BF16 ? rows_kernel<MX_BF16>(a.few)
                                 : rows_kernel<MX_F32>(a.few);
   } else {
-    waves = cdiv(rows, 64) * Kb;
+    threads = 64 * kColBlocks;
+    a.segs = cdiv(Kb, kColBlocks);
+    grid = cdiv(rows, 64) * a.segs;
     fn = fmt == GEMM_FMT_F16    ? (const void*)quantize_columns_kernel<MX_F16>
          : fmt == GEMM_FMT_BF16 ? (const void*)quantize_columns_kernel<MX_BF16>
                                 : (const void*)quantize_columns_kernel<MX_F32>;
   }
-  const int64_t grid = cdiv(waves, 4);
   if (grid > kMaxWide) return GEMM_ERR_SHAPE;
-  return run(fn, wide_grid(grid), 256, &a, (hipStream_t)stream);
+  return run(fn, wide_grid(grid), threads, &a, (hipStream_t)stream);
 }
 
 int gemm_mx4_dequantize(const void* data, int64_t ldd, const void* scales, int64_t lds, int64_t R,

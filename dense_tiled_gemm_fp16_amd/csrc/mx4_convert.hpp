@@ -41,7 +41,7 @@ struct QuantArgs {
   uint8_t* data;           // [G R, 16 Kb]
   uint8_t* scales;         // [G R, Kb]
   int64_t Kb;              // blocks per row
-  int64_t segs;            // rows: wave items per row
+  int64_t segs;            // rows: wave items per row; columns: workgroups per strip of 64 rows
   Short few;               // rows: several rows per wave item
 };
 
@@ -189,44 +189,59 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
   }
 }
 
-// Any strides: lane -> row, wave -> (64 rows, one block).
+// Any strides: workgroup -> 64 rows x 8 blocks, wave -> a block, lane -> a row.
+// The codes change lanes through LDS, so that a store's lanes cover whole
+// 128-byte lines: eight pieces of a row side by side (piece b of row r in slot
+// b ^ r % 8 of the row).
+constexpr int kColBlocks = 8;
 template <int FMT>
-__global__ __launch_bounds__(256) void quantize_columns_kernel(QuantArgs a) {
+__global__ __launch_bounds__(64 * kColBlocks) void quantize_columns_kernel(QuantArgs a) {
   using E = typename MxElem<FMT>::type;
-  const int lane = threadIdx.x & 63;
-  const int64_t w = wave_item();
-  const int64_t strip = w / a.Kb, b = w - strip * a.Kb;
-  const int64_t row = strip * 64 + lane;
-  if (row >= a.G * a.R) return;
-  const int64_t g = a.G == 1 ? 0 : row / a.R, r = row - g * a.R;
-  const int64_t left = a.K - 32 * b;
-  const int n = left < 32 ? (int)left : 32;
-  const E* p = (const E*)a.x + g * a.s_g + r * a.s_r + 32 * b * a.s_k;
-  E e[32];
-  if (n == 32) {
+  __shared__ u32x4 codes[64][kColBlocks];
+  __shared__ uint8_t scales[64][kColBlocks];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t w = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, rows = a.G * a.R;
+  const int64_t strip = w / a.segs, b0 = (w - strip * a.segs) * kColBlocks, b = b0 + wave;
+  const int64_t row0 = strip * 64;
+  if (row0 >= rows) return;
+  if (row0 + lane < rows && b < a.Kb) {
+    const int64_t row = row0 + lane, g = a.G == 1 ? 0 : row / a.R, r = row - g * a.R;
+    const int64_t left = a.K - 32 * b;
+    const int n = left < 32 ? (int)left : 32;
+    const E* p = (const E*)a.x + g * a.s_g + r * a.s_r + 32 * b * a.s_k;
+    E e[32];
+    if (n == 32) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) e[i] = gload<E>(p + i * a.s_k);
-  } else {
+      for (int i = 0; i < 32; ++i) e[i] = gload<E>(p + i * a.s_k);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) e[i] = i < n ? gload<E>(p + i * a.s_k) : (E)0;
+      for (int i = 0; i < 32; ++i) e[i] = i < n ? gload<E>(p + i * a.s_k) : (E)0;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t q = __builtin_bit_cast(uint32_t, mx_in<FMT>(e[i])) & 0x7FFFFFFFu;
+      m = q > m ? q : m;
+    }
+    const uint32_t s = scale_of(m);
+    u32x4 out;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = mx_in<FMT>(e[8 * j + i]);
+      out[j] = to_codes(f, s);
+    }
+    codes[lane][wave ^ (lane & 7)] = out;
+    scales[lane][wave] = (uint8_t)s;
   }
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const uint32_t q = __builtin_bit_cast(uint32_t, mx_in<FMT>(e[i])) & 0x7FFFFFFFu;
-    m = q > m ? q : m;
+  __syncthreads();
+  const int r = tid / kColBlocks, c = tid % kColBlocks;
+  if (row0 + r < rows && b0 + c < a.Kb) {
+    const int64_t at = (row0 + r) * a.Kb + b0 + c;
+    store16(a.data + at * kMxBytes, codes[r][c ^ (r & 7)]);
+    gstore<uint8_t>(a.scales + at, scales[r][c]);
   }
-  const uint32_t s = scale_of(m);
-  u32x4 out;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = mx_in<FMT>(e[8 * j + i]);
-    out[j] = to_codes(f, s);
-  }
-  store16(a.data + (row * a.Kb + b) * kMxBytes, out);
-  gstore<uint8_t>(a.scales + row * a.Kb + b, (uint8_t)s);
 }
 
 struct DequantArgs {
@@ -258,6 +273,27 @@ __global__ __launch_bounds__(256) void dequantize_kernel(DequantArgs a) {
   }
 #pragma unroll
   for (int u = 0; u < kQuantU; ++u) {
+    if constexpr (FMT == MX_F32) {
+      // Half an octet is a 16-byte store: lane l takes half l % 2 of the octet
+      // that lane 32 h + l / 2 loaded, so that a store's lanes lie side by side.
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int from = 32 * h + lane / 2, half = lane & 1;
+        const Place p = place<SHORT>(w, u, from, a.R, octs, a.segs, a.few);
+        const uint32_t codes = __shfl(c[u], from) >> (16 * half);
+        const bf16x8 b = mx4_to_bf16(codes, scale_f32(__shfl(s[u], from)));
+        const int64_t left = p.ok ? a.K - 8 * p.o - 4 * half : 0;
+        float* q = (float*)a.y + p.row * a.ldy + 8 * p.o + 4 * half;
+        if (left >= 4) {
+          gstore(q, f32x4{(float)b[0], (float)b[1], (float)b[2], (float)b[3]});
+        } else {
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            if (i < left) gstore<float>(q + i, (float)b[i]);
+        }
+      }
+      continue;
+    }
     const Place p = place<SHORT>(w, u, lane, a.R, octs, a.segs, a.few);
     if (!p.ok) continue;
     const int64_t o = p.o;
@@ -273,28 +309,16 @@ __global__ __launch_bounds__(256) void dequantize_kernel(DequantArgs a) {
         for (int i = 0; i < left; ++i) gstore<uint16_t>((uint16_t*)q + i, (uint16_t)(v[i / 2] >> (16 * (i & 1))));
       }
     } else {
-      // through bfloat16 (exact) and float (exact) to the output's rounding
+      // through bfloat16 (exact) and float (exact) to binary16's rounding
       const bf16x8 b = mx4_to_bf16(c[u], f);
-      float e[8];
+      uint32_t h[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = (float)b[i];
-      if constexpr (FMT == MX_F32) {
-        if (left >= 8) {
-          gstore(q, f32x4{e[0], e[1], e[2], e[3]});
-          gstore(q + 16, f32x4{e[4], e[5], e[6], e[7]});
-        } else {
-          for (int i = 0; i < left; ++i) gstore<float>((float*)q + i, e[i]);
-        }
+      for (int i = 0; i < 4; ++i)
+        h[i] = (uint32_t)cvt_out<DT_F16>((float)b[2 * i]) | ((uint32_t)cvt_out<DT_F16>((float)b[2 * i + 1]) << 16);
+      if (left >= 8) {
+        store16(q, u32x4{h[0], h[1], h[2], h[3]});
       } else {
-        uint32_t h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          h[i] = (uint32_t)cvt_out<DT_F16>(e[2 * i]) | ((uint32_t)cvt_out<DT_F16>(e[2 * i + 1]) << 16);
-        if (left >= 8) {
-          store16(q, u32x4{h[0], h[1], h[2], h[3]});
-        } else {
-          for (int i = 0; i < left; ++i) gstore<uint16_t>((uint16_t*)q + i, (uint16_t)(h[i / 2] >> (16 * (i & 1))));
-        }
+        for (int i = 0; i < left; ++i) gstore<uint16_t>((uint16_t*)q + i, (uint16_t)(h[i / 2] >> (16 * (i & 1))));
       }
     }
   }

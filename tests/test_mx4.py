@@ -54,7 +54,7 @@ def check_quantized(q, x):
 
 
 @pytest.mark.parametrize("R,K", [(1, 1), (3, 31), (5, 32), (7, 33), (2, 64), (130, 96), (9, 255), (4, 257),
-                                 (3, 2049), (17, 4096), (1, 70000)])
+                                 (3, 2049), (17, 4096), (1, 70000), (300, 257), (40, 2048), (71, 1000), (133, 33)])
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 def test_quantize(R, K, dtype):
     x = inputs(np.random.default_rng(R * 7919 + K), R, K, TYPES[dtype])
@@ -73,12 +73,12 @@ def test_quantize(R, K, dtype):
     check_quantized(g.quantize_mx4(wide[:, ::2]), x)
 
 
-@pytest.mark.parametrize("order", ["rows", "columns", "padded"])
+@pytest.mark.parametrize("order", ["rows", "columns", "even columns", "padded"])
 def test_quantize_stack(order):
-    G, R, K = 3, 5, 70
+    G, R, K = 3, 5 if order != "even columns" else 6, 70
     x = torch.stack([inputs(np.random.default_rng(i), R, K, torch.bfloat16) for i in range(G)])
     d = x.to(DEV)
-    if order == "columns":
+    if "columns" in order:
         d = d.transpose(1, 2).contiguous().transpose(1, 2)
     elif order == "padded":
         d = torch.cat((d, torch.full_like(d, float("nan"))), dim=2)[:, :, :K]
@@ -124,7 +124,7 @@ def test_dequantize_every_scale_and_code(dtype):
                        torch.nan_to_num(want.double(), nan=-77.0))
 
 
-@pytest.mark.parametrize("R,K", [(1, 1), (2, 7), (3, 33), (65, 64), (5, 255), (3, 2051), (33, 512)])
+@pytest.mark.parametrize("R,K", [(1, 1), (2, 7), (3, 33), (65, 64), (5, 255), (3, 2051), (33, 512), (300, 257), (41, 2046), (71, 1003), (90, 4)])
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 def test_dequantize_shapes(R, K, dtype):
     rng = np.random.default_rng(R + K)
