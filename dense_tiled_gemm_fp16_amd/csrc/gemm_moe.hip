@@ -24,7 +24,7 @@ constexpr int64_t kMaxH = INT64_C(1) << 26, kMaxI = INT64_C(1) << 20;
 constexpr int64_t kMaxOffset = (INT64_C(1) << 32) - (INT64_C(1) << 16);
 
 struct Layout {
-  int64_t act_row, act_part, tab_e, tab_p, bytes;
+  int64_t act_row, act_part, tab_e, tab_p, sums, bytes;
 };
 
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -34,13 +34,24 @@ bool sizes_ok(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
          H >= 1 && H <= kMaxH && I >= 1 && I <= kMaxI;
 }
 
-Layout layout(int64_t T, int64_t k, int64_t I) {
+// Workgroups that may share a strip of 32 columns of Y: as many as the compute
+// units have room for, at most 8.
+int32_t max_splits(int64_t H, int64_t cus) {
+  int32_t p = 1;
+  while (p < 8 && 2 * p * cdiv(H, 32) <= cus) p *= 2;
+  return p;
+}
+constexpr int64_t kCus = 256;   // of the whole device; a part of it splits less
+
+Layout layout(int64_t T, int64_t k, int64_t H, int64_t I) {
   Layout l;
   l.act_row = 2 * cdiv(I, 8) * 8;
   l.act_part = up256(T * k * l.act_row);
   l.tab_e = 2 * l.act_part;
   l.tab_p = l.tab_e + up256(4 * T * k);
-  l.bytes = l.tab_p + up256(4 * T * k);
+  l.sums = l.tab_p + up256(4 * T * k);
+  const int64_t splits = max_splits(H, kCus);
+  l.bytes = l.sums + (splits > 1 ? up256(4 * splits * T * cdiv(H, 32) * 32) : 0);
   return l;
 }
 
@@ -71,7 +82,8 @@ bool stack(const void* p, int64_t G, int64_t sg, int64_t R, int64_t sr, int64_t 
 //                      NS 1 UC 2: 161; not few: NS 2 UC 1: 152, NS 1 UC 1: 200
 //   64 tokens, MX4     NI 1 UC 2: 270, NI 1 UC 1: 331, NI 2 UC 1: spills
 //   H 2048, I 768, 4 tokens, 16-bit: down NS 1 UC 4 11.5 (few: 9.9), NS 2 UC 2
-//   14.7: where NS 2 leaves compute units without work, NS 1 (see launch_kernels)
+//   14.7: where NS 2 leaves compute units without work, NS 1, or NS 2 with the
+//   sums split (see launch_kernels)
 // "few" is the down kernel's form for experts with few tokens each.  It pays
 // while most have four or fewer, measured by the mean over all experts, T k / E
 // (16 tokens; few | not, us): MX4 2: 110 | 152, 3: 68 | 105, 4: 75 | 100, 6: 45
@@ -82,22 +94,26 @@ template <int WF, int MT>
 struct Shape {
   static constexpr int NI = 1, UP_UC = 2, UP_WPS = MT == 1 ? 4 : 2;
   static constexpr int UC_NS1 = MT == 1 ? 4 : 2, UC_NS2 = 2, FEW_UC_NS2 = 2, DOWN_WPS = MT == 1 ? 4 : 2;
-  static constexpr int FEW_MEAN = 2;
+  static constexpr int FEW_MEAN = 2, SPLIT_K = 32 * 40;
 };
 template <int MT>
 struct Shape<SW_MX4, MT> {
   static constexpr int NI = MT == 1 ? 2 : 1, UP_UC = 2, UP_WPS = 2;
   static constexpr int UC_NS1 = 1, UC_NS2 = 1, FEW_UC_NS2 = 2, DOWN_WPS = 2;
-  static constexpr int FEW_MEAN = 4;
+  static constexpr int FEW_MEAN = 4, SPLIT_K = 128 * 12;
 };
 
 template <int WF, int DT, int MT, int NS, int UC, bool FEW>
 int launch_down(MoeArgs& a, hipStream_t s) {
   void* p[] = {&a};
-  return hipLaunchKernel((const void*)moe_down_kernel<WF, DT, MT, NS, UC, Shape<WF, MT>::DOWN_WPS, FEW>,
-                         dim3((unsigned)cdiv(a.H, 16 * NS)), dim3(64 * kMoeWaves), p, 0, s) == hipSuccess
-             ? GEMM_OK
-             : GEMM_ERR_HIP;
+  if (hipLaunchKernel((const void*)moe_down_kernel<WF, DT, MT, NS, UC, Shape<WF, MT>::DOWN_WPS, FEW>,
+                      dim3((unsigned)cdiv(a.H, 16 * NS), (unsigned)a.splits), dim3(64 * kMoeWaves), p, 0, s) !=
+      hipSuccess)
+    return GEMM_ERR_HIP;
+  if (a.splits > 1 && hipLaunchKernel((const void*)moe_sum_kernel<DT>,
+                                      dim3((unsigned)cdiv(a.H, 4 * 256), (unsigned)a.T), dim3(256), p, 0, s) != hipSuccess)
+    return GEMM_ERR_HIP;
+  return GEMM_OK;
 }
 
 template <int WF, int DT, int MT>
@@ -113,7 +129,22 @@ int launch_kernels(MoeArgs& a, int cus, hipStream_t s) {
   if (hipLaunchKernel((const void*)moe_up_kernel<WF, DT, MT, P::NI, P::UP_UC, P::UP_WPS>, up, dim3(64 * kMoeWaves),
                       p, 0, s) != hipSuccess)
     return GEMM_ERR_HIP;
-  const bool two = 4 * cdiv(a.H, 32) >= 3 * (int64_t)cus;
+  // Two strips of columns a wave where they give three quarters of the compute
+  // units a workgroup.  With fewer columns the (expert, group) sequence of a strip
+  // is split over workgroups that fill the device, and a third kernel adds their
+  // sums, if a wave's share without is long enough to pay for that, SPLIT_K of I
+  // (us, one strip and no split | two and split): H 2048, I 768, 48 tokens, 128
+  // experts, 16-bit: 166 | 76, MX4 123 | 54; 16 tokens, 64 experts, MX4: 47 | 23,
+  // H 4096: 48 | 31; H 1000, I 600, 10 tokens, 30 experts: 16-bit 20 | 16, MX4
+  // 19.1 | 16.4; H 2048, I 768, 4 tokens, top 2 of 16: 10.0 | 11.5; H 1400, I
+  // 500, 8 experts: 18.1 | 19.1.  (The strip's last workgroup adding the sums
+  // instead of a kernel: 120 instead of 76, its fences write the L2 back.)
+  bool two = 4 * cdiv(a.H, 32) >= 3 * (int64_t)cus;
+  a.splits = 1;
+  if (!two && std::min<int64_t>(a.E, a.T * a.k) * a.I >= (int64_t)P::SPLIT_K * kMoeWaves) {
+    a.splits = max_splits(a.H, std::min<int64_t>(cus, kCus));
+    two = a.splits > 1;
+  }
   if constexpr (MT == 1) {
     if (a.T <= 4 || a.T * a.k <= P::FEW_MEAN * a.E)
       return two ? launch_down<WF, DT, MT, 2, P::FEW_UC_NS2, true>(a, s)
@@ -133,7 +164,7 @@ int launch_layer(MoeArgs& a, int cus, hipStream_t s) {
 extern "C" {
 
 size_t gemm_moe_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I) {
-  return sizes_ok(T, E, top_k, H, I) ? (size_t)layout(T, top_k, I).bytes : 0;
+  return sizes_ok(T, E, top_k, H, I) ? (size_t)layout(T, top_k, H, I).bytes : 0;
 }
 
 int gemm_moe(const gemm_moe_args* g, void* stream, void* workspace, size_t workspace_bytes) {
@@ -172,7 +203,7 @@ int gemm_moe(const gemm_moe_args* g, void* stream, void* workspace, size_t works
   const Range* in[] = {&rx, &rl, &r1, &r2, &rs1, &rs2};
   for (const Range* r : in)
     if (ranges_overlap(ry.lo, ry.hi, r->lo, r->hi)) return GEMM_ERR_ALIAS;
-  const Layout l = layout(T, g->top_k, I);
+  const Layout l = layout(T, g->top_k, H, I);
 
   MoeArgs a;
   a.x = (const char*)g->X;
@@ -222,6 +253,8 @@ int gemm_moe(const gemm_moe_args* g, void* stream, void* workspace, size_t works
   a.act = (char*)ws;
   a.tab_e = (int32_t*)((char*)ws + l.tab_e);
   a.tab_p = (float*)((char*)ws + l.tab_p);
+  a.sums = (float*)((char*)ws + l.sums);
+  a.sums_row = cdiv(H, 32) * 32;
   if (g->mx4)
     rc = g->fmt == GEMM_FMT_F16 ? launch_layer<SW_MX4, DT_F16>(a, cus, s) : launch_layer<SW_MX4, DT_BF16>(a, cus, s);
   else

@@ -54,9 +54,12 @@ struct MoeArgs {
   int64_t act_row, act_part;   // bytes of a row, of a part
   int32_t* tab_e;              // [T top_k] expert, -1 none
   float* tab_p;                // its softmax over all experts
+  float* sums;                 // [splits][T][sums_row] of moe_down, where it is split
+  int64_t sums_row;
   int64_t H, I;
   int32_t T, E, k, fmt_l, by_pair, renormalize;
   int32_t parts;               // of H, in moe_up: 1, 2, 4 or 8
+  int32_t splits;              // of moe_down: workgroups per strip of columns
 };
 
 // Logit as an integer of the same order: NaN above all, both zeros equal.
@@ -262,6 +265,20 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_up_kernel(MoeArgs a) 
   U::run(a, sh, e, lane, wave);
 }
 
+// Four columns of a row of Y.
+template <int DT>
+__device__ __forceinline__ void store_y(const MoeArgs& a, int t, int64_t h, const f32x4& s) {
+  uint16_t* y = a.y + t * a.ldy + h;
+  uint16_t o[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) o[r] = cvt_out<DT>(s[r]);
+  if (h + 4 <= a.H) {
+    gstore(y, u32x2{o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16});
+  } else {
+    for (int r = 0; r < 4 && h + r < a.H; ++r) gstore<uint16_t>(y + r, o[r]);
+  }
+}
+
 // What a workgroup of moe_down takes: NS strips of 16 columns of Y, 16 MT
 // tokens.  FEW: an expert seldom has more than four tokens (see Strip).
 template <int WF, int MT, int NS_, int UC, bool FEW>
@@ -355,16 +372,18 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a
   }
   __syncthreads();
 
-  // The whole groups of chunks of all experts, dealt to the waves in turn (a
-  // row's neighbouring pieces are then read at about the same time), loads
-  // running ahead across experts; then the partial groups, if I has one.
+  // The whole groups of chunks of all experts, dealt to the waves of all
+  // workgroups of the strip in turn (a row's neighbouring pieces are then read
+  // at about the same time), loads running ahead across experts; then the
+  // partial groups, if I has one.
+  const int first_wave = blockIdx.y * NW + wave, waves = a.splits * NW;
   const int64_t h0 = (int64_t)blockIdx.x * (16 * NS);
   const int n = __builtin_amdgcn_readfirstlane(sh.n_active);
   struct Cursor {
     const MoeArgs* a;
     const typename D::Shared* sh;
     int64_t h0;
-    int i, n, g, gpe, first, m;     // group g of gpe of expert i of n
+    int i, n, g, gpe, waves, first, m;     // group g of gpe of expert i of n
     __device__ __forceinline__ void at_expert() {
       while (g >= gpe && i < n) {
         g -= gpe;
@@ -376,9 +395,9 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a
       }
     }
     __device__ __forceinline__ bool more() const { return i < n; }
-    __device__ __forceinline__ bool last() const { return g + D::NW >= gpe; }   // of the wave's, in an expert
+    __device__ __forceinline__ bool last() const { return g + waves >= gpe; }   // of the wave's, in an expert
     __device__ __forceinline__ void next() {
-      g += D::NW;
+      g += waves;
       at_expert();
     }
     __device__ __forceinline__ int64_t c() const { return (int64_t)g * S::UC; }
@@ -428,15 +447,15 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a
       S::clear(acc);
     };
     if (gpe > 0) {
-      Cursor cur{&a, &sh, h0, 0, n, wave, gpe, 0, 0};
+      Cursor cur{&a, &sh, h0, 0, n, first_wave, gpe, waves, 0, 0};
       cur.at_expert();
       S::stream(acc, lds, cur, wo, a.act_part, a.I, lane, [&](const Cursor& cc) {
         if (cc.last()) add(cc);
       });
     }
     if (S::rest(a.I))
-      for (int i = wave; i < n; i += NW) {
-        Cursor cur{&a, &sh, h0, i, n, 0, gpe + 1, 0, 0};
+      for (int i = first_wave; i < n; i += waves) {
+        Cursor cur{&a, &sh, h0, i, n, 0, gpe + 1, waves, 0, 0};
         cur.at_expert();
         cur.g = gpe;
         S::finish(acc, lds, cur, wo, a.act_part, a.I, lane);
@@ -444,24 +463,34 @@ __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a
       }
   }
   __syncthreads();
+  // The waves' sums in order.
   for (int i = tid; i < a.T * (4 * NS); i += NT) {
     const int t = i / (4 * NS), g = i % (4 * NS);
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    f32x4 s{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < NW; ++w)
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[r] += sh.own[w][t][4 * g + r];
-    const int64_t h = h0 + 4 * g;
-    uint16_t* y = a.y + t * a.ldy + h;
-    uint16_t o[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) o[r] = cvt_out<DT>(s[r]);
-    if (h + 4 <= a.H) {
-      gstore(y, u32x2{o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16});
-    } else {
-      for (int r = 0; r < 4 && h + r < a.H; ++r) gstore<uint16_t>(y + r, o[r]);
-    }
+    if (a.splits == 1)
+      store_y<DT>(a, t, h0 + 4 * g, s);
+    else
+      gstore(a.sums + ((int64_t)blockIdx.y * a.T + t) * a.sums_row + h0 + 4 * g, s);
   }
+}
+
+// The splits' sums in order: thread -> four columns of a token.
+template <int DT>
+__global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
+  const int t = blockIdx.y;
+  const int64_t h = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (h >= a.H) return;
+  f32x4 s{0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < a.splits; ++p) {
+    const f32x4 v = gload<f32x4>(a.sums + ((int64_t)p * a.T + t) * a.sums_row + h);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[r] += v[r];
+  }
+  store_y<DT>(a, t, h, s);
 }
 
 }  // namespace gemmf16

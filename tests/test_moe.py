@@ -65,6 +65,8 @@ CASES = [  # T, E, k, H, I: by pair (T k < E) and by expert, one expert, all exp
     (4, 6, 2, 1030, 520),
     # enough columns of Y (on 256 compute units) for two strips a wave
     (3, 4, 2, 6150, 24), (40, 5, 2, 6150, 40), (64, 3, 2, 6200, 70),
+    # long sequences of experts per column: split over 2, 4 and 8 workgroups
+    (9, 64, 8, 4090, 210), (48, 64, 8, 2000, 300), (16, 64, 4, 1000, 333), (64, 64, 8, 36, 200), (30, 40, 6, 3000, 257),
     # enough strips of I for four, two and one part of H
     (12, 24, 4, 70, 272), (40, 24, 4, 70, 530), (40, 24, 4, 300, 1040), (12, 24, 4, 70, 1040), (12, 24, 4, 70, 2060)]
 
@@ -207,11 +209,11 @@ def test_router_product_into_layer():
         x = (x + y).contiguous()
 
 
-@pytest.mark.parametrize("T,E", [(2, 40), (20, 8)])
+@pytest.mark.parametrize("T,E,H,I", [(2, 40, 136, 72), (20, 8, 136, 72), (32, 64, 520, 333)])
 @pytest.mark.parametrize("weights", ["16", "mx4"])
-def test_graph_replays_and_other_stream(T, E, weights):
-    la = Layer(T, E, 2, 136, 72, "bf16", weights)
-    say(f"moe graph {T} {E} {weights}")
+def test_graph_replays_and_other_stream(T, E, H, I, weights):
+    la = Layer(T, E, 2, H, I, "bf16", weights)
+    say(f"moe graph {T} {E} {H} {I} {weights}")
     eager = la.run()
     side = torch.cuda.Stream(DEV)
     side.wait_stream(torch.cuda.current_stream())
