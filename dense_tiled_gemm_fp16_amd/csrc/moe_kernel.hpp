@@ -124,10 +124,11 @@ __device__ __forceinline__ void split_parts(float v, uint16_t& hi, uint16_t& lo)
 
 // What a wave of moe_up takes: NI strips of 16 rows of I (gate and up: 2 NI
 // strips of W1), UC chunks at a time.
-template <int WF, int DT, int MT, int NI_, int UC>
+template <int WF, int DT, int MT, int NI_, int UC, bool ONCE>
 struct MoeUp {
   static constexpr int NI = NI_;
-  using S = Strip<WF, DT == DT_F16 ? SX_F16 : SX_BF16, 2 * NI, MT, UC, 1>;   // few experts get more than 16 tokens
+  using S = Strip<WF, DT == DT_F16 ? SX_F16 : SX_BF16, 2 * NI, MT, UC, 1, false,
+                  ONCE>;   // few experts get more than 16 tokens
   static constexpr int TILES = 2 * NI * MT;
 
   struct Shared {
@@ -155,10 +156,14 @@ struct MoeUp {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
-          int64_t row = 16 * n + (lane >> 2), srow = 16 * n + (lane < 16 ? lane : 0);
-          if (row >= a.I - i0) row = a.I - i0 - 1;
+#pragma unroll
+          for (int j = 0; j < UC; ++j) {
+            int64_t row = 16 * n + S::w_row(j, lane);
+            if (row >= a.I - i0) row = a.I - i0 - 1;
+            wo.w[h * NI + n][j] = (uint32_t)((h * a.I + row) * a.w1_n) + 16 * (lane % S::WP);
+          }
+          int64_t srow = 16 * n + (lane < 16 ? lane : 0);
           if (srow >= a.I - i0) srow = a.I - i0 - 1;
-          wo.w[h * NI + n] = (uint32_t)((h * a.I + row) * a.w1_n) + 16 * (lane & 3);
           wo.s[h * NI + n] = (uint32_t)((h * a.I + srow) * a.s1_n);
         }
       auto rows = [&](int p, int) {
@@ -200,9 +205,9 @@ struct MoeUp {
 
 // Grid (groups of strips of rows of I, experts or pairs).  DT: format of X; MT:
 // tiles of 16 tokens that T needs.
-template <int WF, int DT, int MT, int NI, int UC, int WPS>
+template <int WF, int DT, int MT, int NI, int UC, int WPS, bool ONCE>
 __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_up_kernel(MoeArgs a) {
-  using U = MoeUp<WF, DT, MT, NI, UC>;
+  using U = MoeUp<WF, DT, MT, NI, UC, ONCE>;
   __shared__ typename U::Shared sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slot = blockIdx.y;
@@ -281,10 +286,10 @@ __device__ __forceinline__ void store_y(const MoeArgs& a, int t, int64_t h, cons
 
 // What a workgroup of moe_down takes: NS strips of 16 columns of Y, 16 MT
 // tokens.  FEW: an expert seldom has more than four tokens (see Strip).
-template <int WF, int MT, int NS_, int UC, bool FEW>
+template <int WF, int MT, int NS_, int UC, bool FEW, bool ONCE>
 struct MoeDown {
   static constexpr int NS = NS_, NW = kMoeWaves;
-  using S = Strip<WF, WF == SW_F16 ? SX_F16P : SX_BF16P, NS, FEW ? 2 * MT : MT, UC, 1, FEW>;
+  using S = Strip<WF, WF == SW_F16 ? SX_F16P : SX_BF16P, NS, FEW ? 2 * MT : MT, UC, 1, FEW, ONCE>;
   static constexpr int kPairs = 16 * MT * kMoeTopK;
 
   struct Shared {
@@ -300,9 +305,9 @@ struct MoeDown {
   };
 };
 
-template <int WF, int DT, int MT, int NS, int UC, int WPS, bool FEW>
+template <int WF, int DT, int MT, int NS, int UC, int WPS, bool FEW, bool ONCE>
 __global__ __launch_bounds__(64 * kMoeWaves, WPS) void moe_down_kernel(MoeArgs a) {
-  using D = MoeDown<WF, MT, NS, UC, FEW>;
+  using D = MoeDown<WF, MT, NS, UC, FEW, ONCE>;
   using S = typename D::S;
   constexpr int kPairs = D::kPairs;
   __shared__ typename D::Shared sh;

@@ -60,6 +60,21 @@ __device__ __forceinline__ T as8(u32x4 v) {
   return __builtin_bit_cast(T, v);
 }
 
+// Weights are read once.  Where a load's lanes cover whole lines and the last
+// cache could not keep them until the next call they need not stay in any
+// (ONCE): the layer's first kernel, 16-bit, 64 tokens 593 us instead of 632, 16
+// tokens 554 instead of 584, its second at 16 tokens 250 instead of 263.  Half
+// lines (UC 1) are fetched twice that way: 719 instead of 590.  No gain for MX4
+// (16 tokens 201 | 199, 2 tokens 57 | 50) or UC 4 (13 | 12).
+template <bool ONCE>
+__device__ __forceinline__ u32x4 load_weights(const void* p) {
+  typedef u32x4 Any __attribute__((aligned(1)));
+  if constexpr (ONCE)
+    return __builtin_nontemporal_load((const GEMM_GLOBAL Any*)p);
+  else
+    return load16(p);
+}
+
 // The first n of the eight 16-bit elements at p, the others zero.
 __device__ __forceinline__ u32x4 load8_rest(const char* p, int64_t n) {
   if (n >= 8) return load16(p);
@@ -109,7 +124,7 @@ __device__ __forceinline__ void wave_order() {
 // (see more_tiles).  FEW: of the first tile only the first FR rows run ahead,
 // one row's pieces of the whole group side by side in a load (a quarter of the
 // loads and LDS writes), the others are fetched when there are any.
-template <int WF, int XF, int NS_, int MT_, int UC_, int XT = MT_, bool FEW_ = false>
+template <int WF, int XF, int NS_, int MT_, int UC_, int XT = MT_, bool FEW_ = false, bool ONCE = false>
 struct Strip {
   static constexpr int NS = NS_, MT = MT_, UC = UC_;
   static constexpr bool W4 = WF == SW_MX4, X4 = XF == SX_MX4;
@@ -118,6 +133,7 @@ struct Strip {
   static constexpr int XV = X4 ? 1 : (W4 ? 4 : 1);          // 64-byte pieces of A per chunk, row and part
   static_assert(W4 || !X4, "MX4 A takes MX4 weights");
   static_assert(XT == 1 || XT == MT_, "one tile ahead, or all");
+  static_assert(!ONCE || UC == 2, "a row's piece of a load is a line");
   static constexpr bool FEW = FEW_;
   // FEW: pieces of 16 bytes per row of A in a group, rows per load, rows and
   // loads that run ahead.
@@ -134,6 +150,14 @@ struct Strip {
                        XS_AT = S_AT + (W4 ? NS * 16 * UC * 4 : 0);
   static constexpr int LDS = XS_AT + (X4 ? 16 * UC * 4 : 0);
 
+  // A group's weights: WP pieces of 16 bytes a row, WR rows a load, so that the
+  // lanes of one load cover whole lines.  In LDS a row's pieces lie side by side.
+  static constexpr int WP = 4 * UC, WR = 64 / WP;
+  static __device__ __forceinline__ int w_row(int i, int lane) { return i * WR + lane / WP; }
+  static __device__ __forceinline__ int w_slot(int r, int piece) {
+    return r * (16 * WP) + ((piece ^ (UC == 1 ? fa(r) : r & 7)) << 4);
+  }
+
   // A uniform address and the lane's 32-bit offset beside it, so that moving
   // along K or to another expert is scalar arithmetic.
   struct WPtr {
@@ -141,7 +165,7 @@ struct Strip {
     const uint8_t* s;         // its scales (MX4)
   };
   struct WOff {
-    uint32_t w[NS];           // row lane / 4 of each strip, piece lane % 4
+    uint32_t w[NS][UC];       // row w_row(i, lane) of each strip, piece lane % WP
     uint32_t s[NS];           // scales of row lane for lanes 0 .. 15, of row 0 for the others (MX4)
   };
   struct XPtr {
@@ -157,10 +181,14 @@ struct Strip {
     WOff o;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      int64_t r = i * stride + (lane >> 2), q = i * stride + (lane < 16 ? lane : 0);
-      if (r >= rows) r = rows - 1;
+#pragma unroll
+      for (int j = 0; j < UC; ++j) {
+        int64_t r = i * stride + w_row(j, lane);
+        if (r >= rows) r = rows - 1;
+        o.w[i][j] = (uint32_t)(r * ld) + 16 * (lane % WP);
+      }
+      int64_t q = i * stride + (lane < 16 ? lane : 0);
       if (q >= rows) q = rows - 1;
-      o.w[i] = (uint32_t)(r * ld) + 16 * (lane & 3);
       o.s[i] = (uint32_t)(q * lds);
     }
     return o;
@@ -200,7 +228,7 @@ struct Strip {
 #pragma unroll
     for (int u = 0; u < UC; ++u)
 #pragma unroll
-      for (int s = 0; s < NS; ++s) b.w[u][s] = load16(w + o.w[s] + 64 * u);
+      for (int s = 0; s < NS; ++s) b.w[u][s] = load_weights<ONCE>(w + o.w[s][u]);
     if constexpr (W4) {
       const char* sp = uniform_ptr((const char*)p.s + 4 * c);
 #pragma unroll
@@ -222,20 +250,19 @@ struct Strip {
   // The last, partial group of a row: chunks c .. , zeros past K.
   static __device__ __forceinline__ void load_w_rest(WRegs& b, const WPtr& p, const WOff& o, int64_t c, int64_t K,
                                                      int lane) {
-    const int piece = lane & 3;
+    const int64_t k0 = c * CK + (W4 ? 32 : 8) * (lane % WP);   // of the lane's piece
 #pragma unroll
-    for (int u = 0; u < UC; ++u) {
-      const int64_t cc = c + u;
+    for (int u = 0; u < UC; ++u)
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
+        const char* w = p.w + c * 64 + o.w[s][u];
         if constexpr (W4) {
-          b.w[u][s] = (4 * cc + piece) * 32 < K ? load16(p.w + cc * 64 + o.w[s]) : zero4();
-          b.s[s][u] = scales_rest(p.s + 4 * cc + o.s[s], cc, K);
+          b.w[u][s] = k0 < K ? load16(w) : zero4();
+          b.s[s][u] = scales_rest(p.s + 4 * (c + u) + o.s[s], c + u, K);
         } else {
-          b.w[u][s] = load8_rest(p.w + cc * 64 + o.w[s], K - (cc * 32 + 8 * piece));
+          b.w[u][s] = load8_rest(w, K - k0);
         }
       }
-    }
   }
   static __device__ __forceinline__ void load_x_rest(XRegs& b, const XPtr& p, int64_t xpart, int64_t c, int64_t K,
                                                      int lane) {
@@ -269,11 +296,11 @@ struct Strip {
   // A group's weights and scales into the wave's LDS.
   static __device__ __forceinline__ void stage_w(char* lds, const WRegs& b, int lane) {
     wave_order();
-    const int r = lane >> 2, at = r * 64 + (((lane & 3) ^ fa(r)) << 4);
 #pragma unroll
     for (int u = 0; u < UC; ++u)
 #pragma unroll
-      for (int s = 0; s < NS; ++s) *(u32x4*)(lds + (u * NS + s) * 1024 + at) = b.w[u][s];
+      for (int s = 0; s < NS; ++s)
+        *(u32x4*)(lds + s * (1024 * UC) + w_slot(w_row(u, lane), lane % WP)) = b.w[u][s];
     if constexpr (W4) {
       if (lane < 16) {
 #pragma unroll
@@ -383,7 +410,7 @@ struct Strip {
       uint32_t sb[NS];
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        w[s] = *(const u32x4*)(lds + (u * NS + s) * 1024 + r * 64 + ((g ^ fa(r)) << 4));
+        w[s] = *(const u32x4*)(lds + s * (1024 * UC) + w_slot(r, 4 * u + g));
         if constexpr (W4) sb[s] = (*(const uint32_t*)(lds + S_AT + ((s * 16 + r) * UC + u) * 4) >> (8 * g)) & 255u;
       }
       if constexpr (X4) {

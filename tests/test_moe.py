@@ -88,6 +88,17 @@ def test_layer(T, E, k, H, I, dtype, weights):
     assert torch.equal(la.run(), y)                    # the same bits again
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(3, 4, 2, 6150, 1000), (16, 8, 4, 6150, 500), (20, 8, 2, 6150, 500),
+                                       (20, 32, 4, 2000, 400), (2, 4, 2, 5000, 1200)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_layer_with_weights_past_the_cache(T, E, k, H, I, dtype):
+    la = Layer(T, E, k, H, I, dtype, "16")
+    say(f"moe T={T} E={E} k={k} H={H} I={I} {dtype}")
+    y = la.run()
+    la.check(y)
+    assert torch.equal(la.run(), y)
+
+
 @pytest.mark.parametrize("logits", ["f16", "bf16"])
 @pytest.mark.parametrize("T,E", [(2, 40), (30, 12)])
 def test_ties_and_logit_types(logits, T, E):
