@@ -73,7 +73,8 @@ bool stack(const void* p, int64_t G, int64_t sg, int64_t R, int64_t sr, int64_t 
 // Shapes of the two kernels: strips of I (NI) or of columns of Y (NS) per wave,
 // chunks per group (UC), waves per SIMD that the registers are limited to
 // (WPS).  Measured per kernel (us; bf16, H 7168, I 2048, top 8 of 64 experts;
-// up | down):
+// before loads covered whole lines, which takes 6% off the 16-bit ones; up |
+// down):
 //   1 token, 16-bit    UC 2: 84, UC 4: 131 with the registers of WPS 4
 //                      | NS 2 UC 2: 39, NS 1 UC 4: 47, NS 4 UC 2: 52
 //   64 tokens, 16-bit  UC 2: 637, UC 4: 642 | NS 2 UC 2: 332, NS 1 UC 4: 386

@@ -15,11 +15,17 @@
 // l / 16; the sums land as weight rows 4 (l / 16) + r of column (row of A)
 // l % 16.  Loaded in that arrangement, every four neighbouring lanes touch four
 // rows, and the address unit takes 64 cycles for a 1 KiB load instruction; four
-// lanes on the 64 bytes of one row take 16 (both measured).  So lane l loads
-// piece l % 4 of row l / 4, and the pieces change lanes through a part of LDS
-// that belongs to the wave: written and read in the wave's own order, without
-// barriers.  Piece p of row r lies in slot p ^ fa(r) of its 64 bytes, which
-// keeps both sides free of bank conflicts.
+// lanes on the 64 bytes of one row take 16 (both measured).  So neighbouring
+// lanes load neighbouring 16-byte pieces of a row (of the group's 64 UC bytes of
+// weights, of a chunk's 64 bytes of A), and the pieces change lanes through a
+// part of LDS that belongs to the wave: written and read in the wave's own
+// order, without barriers.  The slot of a row's piece is XORed with bits of the
+// row, which keeps both sides free of bank conflicts.
+//
+// Measured per kernel: one token, H 7168, I 2048, 8 experts in bfloat16 6.3 and
+// 5.7 TB/s (74 and 41 us), 64 tokens, 64 experts 6.5 and 6.0; plain reads of the
+// same bytes 6.4; as products with MX4 weights, 1 x 2048 x 7168 5.3 us and 16 x
+// 7168 x 2048 4.2 us, of which some 2.5 are a launch and the sum over the waves.
 //
 // Only the order of k is free, as long as both operands share it:
 //   16-bit weights   a chunk is 32 k; lane group g takes octet g.

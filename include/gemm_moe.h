@@ -1,7 +1,8 @@
 /*
  * gemm_moe.h -- a mixture-of-experts layer for a few tokens on MI355X: the
  * routing, the experts' gate and up products, the activation, the down
- * product and the weighted sum, in two kernels.  Same library, return codes
+ * product and the weighted sum, in two kernels (three where few columns make
+ * the weighted sum be split).  Same library, return codes
  * (enum gemm_status), stream and workspace rules as gemm_f16.h.
  *
  * For token t with row x_t of X [T, H] and logits L[t, 0 .. E-1]:
