@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from ._lib import MoeArgs, lib
-from .mx4 import FORMATS, MX4, _call, _given, _workspace
+from .mx4 import FORMATS, MX4, _call, _given, _new, _workspace
 
 MAX_TOKENS, MAX_EXPERTS, MAX_TOP_K = 64, 512, 16
 
@@ -77,7 +77,7 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
     if (x.stride(1) != 1 and H > 1) or (logits.stride(1) != 1 and E > 1):
         raise ValueError("x and logits must have unit stride along the last axis")
     if out is None:
-        out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+        out = _new((T, H), x.dtype, x.device, stream)
     elif out.dtype != x.dtype or out.device != x.device or out.shape != (T, H) or \
             (out.stride(1) != 1 and H > 1) or out.stride(0) < H:
         raise ValueError("out must be a row-major [T, H] tensor of x's dtype on its device")

@@ -51,6 +51,17 @@ def _call(device, stream, fn, *args):
         raise _error(rc)
 
 
+def _new(shape, dtype, device, stream):
+    """A result on the current stream, written on `stream`: allocated in the
+    latter's order, kept until both are done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _workspace(nbytes, device, stream):
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -97,7 +108,7 @@ class MX4:
         self.K, self.shape, self.device = K, (*data.shape[:-1], K), data.device
 
     @classmethod
-    def _empty(cls, shape, device):
+    def _empty(cls, shape, device, stream):
         """Contiguous and uninitialised, data and scales in one allocation
         (the tensors are made when they are asked for)."""
         q = cls.__new__(cls)
@@ -106,7 +117,7 @@ class MX4:
             rows *= n
         K = shape[-1]
         q._data = q._scales = None
-        q._buffer = torch.empty((17 * rows * -(-K // BLOCK),), dtype=torch.uint8, device=device)
+        q._buffer = _new((17 * rows * -(-K // BLOCK),), torch.uint8, device, stream)
         q.K, q.shape, q.device = K, tuple(shape), device
         q._lds = -(-K // BLOCK)
         q._ldd = 16 * q._lds
@@ -181,7 +192,7 @@ def quantize_mx4(x, out=None, stream=None):
     if min(strides) <= 0:
         raise ValueError("strides must be positive")
     if out is None:
-        out = MX4._empty(shape, device)
+        out = MX4._empty(shape, device, stream)
     elif out.shape != tuple(shape) or out.device != device or not out.is_contiguous():
         raise ValueError("out must be an MX4 of x's shape on its device, contiguous")
     G, sg = (shape[0], strides[0]) if len(shape) == 3 else (1, 1)
@@ -201,7 +212,7 @@ def dequantize_mx4(q, dtype=torch.bfloat16, out=None, stream=None):
     if not q.is_cuda or min(shape) <= 0:
         raise ValueError("expected a non-empty MX4 on a GPU")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
+        out = _new(shape, dtype, device, stream)
     elif out.dtype != dtype or out.device != device or out.shape != shape or \
             (out.stride(-1) != 1 and shape[-1] > 1) or (len(shape) == 3 and not out.is_contiguous()):
         raise ValueError("out must be of q's shape, of dtype, on its device, with unit column stride "
@@ -261,7 +272,7 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
             raise ValueError("a must have unit stride along K and a positive row stride")
     ldc = N
     if out is None:
-        out = a.new_empty((M, N)) if not quantised else torch.empty((M, N), dtype=dtype, device=device)
+        out = _new((M, N), dtype, device, stream)
     elif out.dtype != dtype or out.device != device or out.shape != (M, N) or \
             (out.stride(1) != 1 and N > 1) or out.stride(0) < N:
         raise ValueError("out must be a row-major [M, N] tensor of the output dtype on the inputs' device")

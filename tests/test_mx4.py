@@ -333,6 +333,16 @@ def test_graph_replays_and_other_stream(M, N):
     q = g.quantize_mx4(x, stream=side)               # a stream by argument
     side.synchronize()
     assert torch.equal(g.dequantize_mx4(q, torch.float16), eager[2])
+    # results of a stream by argument may take no memory that work of the current stream still uses
+    for _ in range(3):
+        held = torch.full((1 << 22,), 7.0, device=DEV)
+        busy = [held * i for i in range(20)]
+        del held, busy
+        side.wait_stream(torch.cuda.current_stream())
+        y = g.gemm_mx4(g.quantize_mx4(x, stream=side), qw, stream=side)
+        z = g.gemm_mx4(x, qw, stream=side)
+        side.synchronize()
+        assert torch.equal(y, eager[0]) and torch.equal(z, eager[1])
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         outs = step()
