@@ -365,9 +365,10 @@ __device__ __forceinline__ void store8_any(uint16_t* dst, u32x4 v) {
 // their tiles together that burst cost about 10 us per 256 x 256 tile (5%
 // of the 131072 x 2048 x 7168 product); staged, it costs about half of that.
 // Rows past M are not stored; nor are the columns past N of an 8-column chunk
-// that crosses N.  With C 16-byte aligned and ldc % 8 == 0 every chunk is one
-// 16-byte store; otherwise each chunk takes the widest stores its address
-// allows (the 16 lanes of one row share that choice).
+// that crosses N.  With C 16-byte aligned, ldc % 8 == 0 and no such chunk among
+// the wave's columns every chunk is one 16-byte store; otherwise each whole
+// chunk takes the widest stores its address allows (the 16 lanes of one row
+// share that choice) and a crossing one is stored column by column.
 //
 // In a 32 x 32 block lane l holds, per group g of 4 registers, columns
 // 8 g + 4 (l / 32) .. + 3 of row l % 32.  Packed to binary16 pairs, one lane
@@ -405,7 +406,7 @@ __device__ __forceinline__ void store_tile_staged(const KArgs& a, const f32x16 (
   const int64_t mr = a.M - (m0 + wm * CF::WTM), nc = a.N - (n0 + wn * CF::WTN);
   const int rows = mr < 0 ? 0 : (mr > CF::WTM ? CF::WTM : (int)mr);
   const int cols = nc < 0 ? 0 : (nc > CF::WTN ? CF::WTN : (int)nc);
-  if (((uintptr_t)a.C & 15u) == 0 && (a.ldc & 7) == 0) {
+  if (((uintptr_t)a.C & 15u) == 0 && (a.ldc & 7) == 0 && (cols & 7) == 0) {
 #pragma unroll
     for (int it = 0; it < CF::WTM / 4; ++it) {
       const int r = 4 * it + lane / 16, c = lane % 16;
