@@ -263,7 +263,9 @@ struct Strip {
       for (int s = 0; s < NS; ++s) {
         const char* w = p.w + c * 64 + o.w[s][u];
         if constexpr (W4) {
-          b.w[u][s] = k0 < K ? load16(w) : zero4();
+          // a code behind K may stand for more than bfloat16 holds, and an
+          // infinity times the zero that it meets would be NaN
+          b.w[u][s] = k0 < K ? mask_codes(load16(w), K - k0 < 32 ? (int)(K - k0) : 32) : zero4();
           b.s[s][u] = scales_rest(p.s + 4 * (c + u) + o.s[s], c + u, K);
         } else {
           b.w[u][s] = load8_rest(w, K - k0);
