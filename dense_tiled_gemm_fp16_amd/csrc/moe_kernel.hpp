@@ -121,13 +121,17 @@ __device__ __forceinline__ float softmax_weight(const MoeArgs& a, int t, int e, 
   return expf(load_logit(a, t, e) - m) / s;
 }
 
-// silu(g) u as two parts of the format the down product takes.
-template <bool F16>
+// silu(g) u as two bfloat16 parts, what the down product takes: fp32 does not
+// enter the 16-bit matrix instructions, and two parts keep 2^-16 of a value (the
+// output keeps 2^-8 or 2^-11) over fp32's whole range.  Beside binary16 weights
+// too, which the down product then splits (4 tokens, top 2 of 16, H 2048, I 768:
+// the layer 27.1 us, with binary16 parts 25.0; 64 tokens, top 8 of 64, H 7168, I
+// 2048: 926 and 878): binary16 parts keep more of a value near 1, but their least
+// step is 2^-24 and they end at 65504, while silu(g) u may lie below and above.
 __device__ __forceinline__ void split_parts(float v, uint16_t& hi, uint16_t& lo) {
-  constexpr int DT = F16 ? DT_F16 : DT_BF16;
-  hi = cvt_out<DT>(v);
-  const float r = v - cvt_in<DT>(hi);
-  lo = cvt_out<DT>(r == r && fabsf(r) <= fabsf(v) ? r : 0.0f);   // nothing beside an infinity or a NaN
+  hi = cvt_out<DT_BF16>(v);
+  const float r = v - cvt_in<DT_BF16>(hi);
+  lo = cvt_out<DT_BF16>(r == r && fabsf(r) <= fabsf(v) ? r : 0.0f);   // nothing beside an infinity or a NaN
 }
 
 // What a wave of moe_up takes: NI strips of 16 rows of I (gate and up: 2 NI
@@ -202,7 +206,7 @@ struct MoeUp {
         uint16_t hi[4], lo[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          split_parts<WF == SW_F16>(gate[r] / (1.0f + expf(-gate[r])) * up[r], hi[r], lo[r]);
+          split_parts(gate[r] / (1.0f + expf(-gate[r])) * up[r], hi[r], lo[r]);
         char* q = a.act + (token * a.k + sh.rank[token]) * a.act_row + 2 * i;
         gstore(q, u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16});
         gstore(q + a.act_part, u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16});
@@ -297,7 +301,7 @@ __device__ __forceinline__ void store_y(const MoeArgs& a, int t, int64_t h, cons
 template <int WF, int MT, int NS_, int UC, bool FEW, bool ONCE>
 struct MoeDown {
   static constexpr int NS = NS_, NW = kMoeWaves;
-  using S = Strip<WF, WF == SW_F16 ? SX_F16P : SX_BF16P, NS, FEW ? 2 * MT : MT, UC, 1, FEW, ONCE>;
+  using S = Strip<WF, SX_BF16P, NS, FEW ? 2 * MT : MT, UC, 1, FEW, ONCE>;
   static constexpr int kPairs = 16 * MT * kMoeTopK;
 
   struct Shared {

@@ -39,7 +39,8 @@
 // for a binary16 A, where the scale byte is in 104 .. 140.  Other scales take
 // the chunk through bfloat16, A split exactly into two bfloat16 parts; all but
 // 0, the scale of a block of zeros: whatever nonzero codes it has (up to 2^-124)
-// vanish next to binary16's least step.
+// vanish next to binary16's least step.  Binary16 weights that meet an A in
+// bfloat16 parts are split exactly into two such parts too.
 //
 // Rows past the end read a valid row (their sums are never stored); k past K
 // enters as zero on both sides.
@@ -51,9 +52,9 @@
 namespace gemmf16 {
 
 enum StripW { SW_F16 = 0, SW_BF16 = 1, SW_MX4 = 2 };
-// A operand: 16-bit rows, two 16-bit parts whose sum is the value (rows xp
+// A operand: 16-bit rows, two bfloat16 parts whose sum is the value (rows xp
 // bytes apart), or MX4 rows.
-enum StripX { SX_F16 = 0, SX_BF16 = 1, SX_F16P = 2, SX_BF16P = 3, SX_MX4 = 4 };
+enum StripX { SX_F16 = 0, SX_BF16 = 1, SX_BF16P = 2, SX_MX4 = 3 };
 
 __device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -107,14 +108,16 @@ __device__ __forceinline__ void settle(f32x4 (&a)[N][MT], int t) {
   }
 }
 
-// binary16 -> two bfloat16 parts, exactly: 11 significant bits as 8 + 3.
+// binary16 -> two bfloat16 parts, exactly: 11 significant bits as 8 + 3.  An
+// infinity leaves no rest, or with FINITE (inputs that are) a NaN.
+template <bool FINITE>
 __device__ __forceinline__ void split_bf16(f16x8 x, bf16x8& hi, bf16x8& lo) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float f = (float)x[i];
     hi[i] = (__bf16)f;
     const float r = f - (float)hi[i];
-    lo[i] = (__bf16)(r == r ? r : 0.0f);   // an infinity leaves no rest
+    lo[i] = (__bf16)(FINITE || r == r ? r : 0.0f);
   }
 }
 
@@ -134,7 +137,7 @@ template <int WF, int XF, int NS_, int MT_, int UC_, int XT = MT_, bool FEW_ = f
 struct Strip {
   static constexpr int NS = NS_, MT = MT_, UC = UC_;
   static constexpr bool W4 = WF == SW_MX4, X4 = XF == SX_MX4;
-  static constexpr int PL = (XF == SX_F16P || XF == SX_BF16P) ? 2 : 1;
+  static constexpr int PL = XF == SX_BF16P ? 2 : 1;
   static constexpr int CK = W4 ? 128 : 32;                  // k per chunk
   static constexpr int XV = X4 ? 1 : (W4 ? 4 : 1);          // 64-byte pieces of A per chunk, row and part
   static_assert(W4 || !X4, "MX4 A takes MX4 weights");
@@ -435,7 +438,7 @@ struct Strip {
         for (int j = 0; j < 4; ++j) {
           if constexpr (XF == SX_F16 && WIDE) {
             bf16x8 hi, lo;
-            split_bf16(as8<f16x8>(x.f[u][0][j]), hi, lo);
+            split_bf16<false>(as8<f16x8>(x.f[u][0][j]), hi, lo);
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
               const bf16x8 wf = mx4_to_bf16(w[s][j], scale_f32(sb[s]));
@@ -444,7 +447,6 @@ struct Strip {
             }
             __builtin_amdgcn_sched_barrier(0);   // one octet's registers at a time
           } else {
-            static_assert(XF != SX_F16P, "MX4 weights take bfloat16 parts");
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
               if constexpr (XF == SX_F16) {
@@ -457,6 +459,18 @@ struct Strip {
               }
             }
           }
+        }
+      } else if constexpr (WF == SW_F16 && XF == SX_BF16P) {
+        bf16x8 hi[NS], lo[NS];
+#pragma unroll
+        for (int s = 0; s < NS; ++s) split_bf16<true>(as8<f16x8>(w[s]), hi[s], lo[s]);
+#pragma unroll
+        for (int q = PM - 1; q >= 0; --q) {   // the smaller parts first
+          const bf16x8 xf = as8<bf16x8>(x.f[u][q][0]);
+#pragma unroll
+          for (int s = 0; s < NS; ++s) acc[s][T] = mfma16(lo[s], xf, acc[s][T]);
+#pragma unroll
+          for (int s = 0; s < NS; ++s) acc[s][T] = mfma16(hi[s], xf, acc[s][T]);
         }
       } else {
         using V = std::conditional_t<WF == SW_F16, f16x8, bf16x8>;

@@ -50,8 +50,7 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
     with renormalize=False that of all.  A token of -inf logits alone, such as
     a padded row of a batch, gets zeros.
 
-    Sums are fp32, and silu(g) * u keeps 16 significant bits or more; with
-    float16 weights it has to stay inside float16's range.
+    Sums are fp32, and silu(g) * u keeps 16 significant bits at any magnitude.
 
     workspace: gemm_moe_workspace_bytes(T, E, top_k, H, I) bytes, 256-byte
     aligned, not shared with a call that may overlap; allocated here when not
