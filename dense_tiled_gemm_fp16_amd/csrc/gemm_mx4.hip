@@ -145,19 +145,21 @@ int launch_strip_m(const StripArgs& a, hipStream_t s) {
   }
 }
 
-// The tile kernel's plan: its scale arrays, transposed, are the workspace.
+// The tile kernel's plan: its scale arrays, transposed, are the workspace; the
+// grids of the kernel that transposes them (gx, gy) and of the tiles.
 struct TilePlan {
-  int64_t steps, sa_rows, sb_rows;
-  size_t bytes;
+  int64_t steps, sa_rows, sb_rows, gx, gy, grid;
 };
 
-TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
-  TilePlan p;
-  p.steps = cdiv(K, 128);
-  p.sa_rows = cdiv(M, Mx4Cfg::BM) * Mx4Cfg::BM;
-  p.sb_rows = cdiv(N, Mx4Cfg::BN) * Mx4Cfg::BN;
-  p.bytes = (size_t)(4 * p.steps * (p.sa_rows + p.sb_rows));
-  return p;
+// False for more workgroups than a launch takes.
+bool tile_plan(int64_t M, int64_t N, int64_t K, TilePlan* p) {
+  p->steps = cdiv(K, 128);
+  p->sa_rows = cdiv(M, Mx4Cfg::BM) * Mx4Cfg::BM;
+  p->sb_rows = cdiv(N, Mx4Cfg::BN) * Mx4Cfg::BN;
+  p->gx = cdiv(std::max(p->sa_rows, p->sb_rows), 64);
+  p->gy = cdiv(p->steps, 16);
+  return !__builtin_mul_overflow(p->sa_rows / Mx4Cfg::BM, p->sb_rows / Mx4Cfg::BN, &p->grid) &&
+         fits_x(p->grid, Mx4Cfg::NT) && fits_x(p->gx, 256) && p->gy <= 65535;
 }
 
 // 256 x 256 tiles from 48 of them on (1024 x 2048 x 7168, 32 tiles: 41.3 us
@@ -170,13 +172,11 @@ bool takes_tile(int64_t M, int64_t N, int64_t K) {
 constexpr int64_t kMaxTileLd = INT64_C(1) << 24;
 
 template <int DT>
-int launch_tile(const StripArgs& a, void* ws, hipStream_t s) {
-  const TilePlan p = tile_plan(a.M, a.N, a.K);
+int launch_tile(const StripArgs& a, const TilePlan& p, void* ws, hipStream_t s) {
   uint32_t* sa = (uint32_t*)ws;
   uint32_t* sb = sa + p.steps * p.sa_rows;
   Mx4ScaleArgs q{{a.as, a.bs}, {a.ldas, a.ldbs}, {a.M, a.N}, {p.sa_rows, p.sb_rows}, {sa, sb},
                  cdiv(a.K, kMxBlock), p.steps};
-  const int64_t gx = cdiv(std::max(p.sa_rows, p.sb_rows), 64), gy = cdiv(p.steps, 16);
   Mx4TileArgs t{};
   t.k.A = (const uint16_t*)a.a;
   t.k.lda_m = a.lda;
@@ -194,12 +194,9 @@ int launch_tile(const StripArgs& a, void* ws, hipStream_t s) {
   t.sa_rows = p.sa_rows;
   t.sb = sb;
   t.sb_rows = p.sb_rows;
-  int64_t grid;
-  if (__builtin_mul_overflow(t.k.GM, t.k.GN, &grid) || !fits_x(grid, Mx4Cfg::NT) || !fits_x(gx, 256) || gy > 65535)
-    return GEMM_ERR_SHAPE;
-  const int rc = run((const void*)mx4_scales_kernel, dim3((unsigned)gx, (unsigned)gy, 2), 256, &q, s);
+  const int rc = run((const void*)mx4_scales_kernel, dim3((unsigned)p.gx, (unsigned)p.gy, 2), 256, &q, s);
   if (rc) return rc;
-  return run((const void*)mx4_tile_kernel<DT>, dim3((unsigned)grid), Mx4Cfg::NT, &t, s);
+  return run((const void*)mx4_tile_kernel<DT>, dim3((unsigned)p.grid), Mx4Cfg::NT, &t, s);
 }
 
 }  // namespace
@@ -314,7 +311,8 @@ int gemm_mx4(const void* A, int64_t lda, const void* SA, int64_t ldsa, const voi
   if (!takes_tile(M, N, K) || lda > kMaxTileLd || ldb > kMaxTileLd)
     return f16 ? launch_strip_m<SX_MX4, DT_F16>(a, s) : launch_strip_m<SX_MX4, DT_BF16>(a, s);
   const size_t need = gemm_mx4_workspace_bytes(M, N, K);
-  if (need == 0) return GEMM_ERR_SHAPE;
+  TilePlan plan;
+  if (need == 0 || !tile_plan(M, N, K, &plan)) return GEMM_ERR_SHAPE;
   void* ws = workspace;
   if (workspace) {
     if (workspace_bytes < need || ((uintptr_t)workspace & 255u)) return GEMM_ERR_WORKSPACE;
@@ -324,7 +322,7 @@ int gemm_mx4(const void* A, int64_t lda, const void* SA, int64_t ldsa, const voi
   } else if (hipMallocAsync(&ws, need, s) != hipSuccess) {
     return GEMM_ERR_HIP;
   }
-  rc = f16 ? launch_tile<DT_F16>(a, ws, s) : launch_tile<DT_BF16>(a, ws, s);
+  rc = f16 ? launch_tile<DT_F16>(a, plan, ws, s) : launch_tile<DT_BF16>(a, plan, ws, s);
   if (!workspace && hipFreeAsync(ws, s) != hipSuccess && rc == GEMM_OK) rc = GEMM_ERR_HIP;
   return rc;
 }

@@ -56,8 +56,8 @@ int gemm_mx4_dequantize(const void* data, int64_t ldd, const void* scales, int64
  * rows, at most 2^26 bytes apart (GEMM_ERR_LAYOUT).
  * Needs gemm_mx4_workspace_bytes(M, N, K) bytes of workspace (may be 0); with
  * workspace == NULL they are allocated in stream order.  GEMM_ERR_SHAPE: more
- * than 65535 * 64 rows of A against 128 rows of B or fewer, or more than 2^27
- * rows of B against 128 rows of A or fewer.
+ * than 65535 * 64 rows of A against 128 rows of B or fewer, more than 2^27
+ * rows of B against 128 rows of A or fewer, or 2^23 tiles of 256 x 256 and more.
  */
 int gemm_mx4(const void* A, int64_t lda, const void* SA, int64_t ldsa, const void* B, int64_t ldb,
              const void* SB, int64_t ldsb, void* C, int32_t fmt_c, int64_t ldc, int64_t M, int64_t N,
