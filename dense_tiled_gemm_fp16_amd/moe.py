@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from ._lib import MoeArgs, lib
-from .mx4 import FORMATS, MX4, _call, _given, _new, _workspace
+from .mx4 import FORMATS, MX4, _call, _given, _keep, _new, _workspace
 
 MAX_TOKENS, MAX_EXPERTS, MAX_TOP_K = 64, 512, 16
 
@@ -52,6 +52,8 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
 
     Sums are fp32, and silu(g) * u keeps 16 significant bits at any magnitude.
 
+    stream: the stream to run on instead of the current one (as in mx4.py).
+
     workspace: gemm_moe_workspace_bytes(T, E, top_k, H, I) bytes, 256-byte
     aligned, not shared with a call that may overlap; allocated here when not
     given."""
@@ -88,4 +90,5 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
     if workspace is None:
         workspace = _workspace(lib.gemm_moe_workspace_bytes(T, E, top_k, H, I), x.device, stream)
     _call(x.device, stream, _c_layer, ctypes.byref(args), *_given(workspace, x.device))
+    _keep(stream, x, logits, w_gate_up, w_down, out, workspace)
     return out

@@ -8,6 +8,11 @@ computation runs in the HIP library.
     gemm_mx4(a, b)                -> C [M, N] = a . b^T, b MX4 [N, K], a MX4 [M, K]
                                      or float16 / bfloat16 [M, K]
     gemm_mx4_workspace_bytes(M, N, K)
+
+Each call only enqueues its kernels, on the inputs' device's current stream or
+on the one given as `stream`.  In the latter case it is the caller's to have
+that stream wait for what the inputs come from, and whoever reads the result
+for that stream; the tensors themselves may be dropped right after the call.
 """
 import torch
 
@@ -67,6 +72,17 @@ def _workspace(nbytes, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _keep(stream, *used):
+    """Tensors and MX4s that a call on a stream by argument uses: the caller may
+    drop them right after the call, and then their memory is not handed out
+    again before the stream is done with them."""
+    if stream is not None:
+        for u in used:
+            for t in u._tensors() if isinstance(u, MX4) else (u,):
+                if t is not None:
+                    t.record_stream(stream)
 
 
 def _given(workspace, device):
@@ -159,6 +175,9 @@ class MX4:
             return p, self._ldd, p + self._buffer.numel() // 17 * 16, self._lds
         return self._data.data_ptr(), self._ldd, self._scales.data_ptr(), self._lds
 
+    def _tensors(self):
+        return (self._buffer,) if self._buffer is not None else (self._data, self._scales)
+
     def _stack_strides(self):
         """Strides from matrix to matrix of a stack's data and scales."""
         if self._buffer is not None:
@@ -199,6 +218,7 @@ def quantize_mx4(x, out=None, stream=None):
     data, _, scales, _ = out._rows()
     _call(device, stream, _c_quantize, x.data_ptr(), fmt, sg, strides[-2], strides[-1], G, shape[-2], shape[-1],
           data, scales)
+    _keep(stream, x, out)
     return out
 
 
@@ -229,6 +249,7 @@ def dequantize_mx4(q, dtype=torch.bfloat16, out=None, stream=None):
         R, lds, ldy = R * shape[1], -(-K // BLOCK), K
         ldd = 16 * lds
     _call(device, stream, _c_dequantize, data, ldd, scales, lds, R, K, out.data_ptr(), fmt, ldy)
+    _keep(stream, q, out)
     return out
 
 
@@ -291,4 +312,5 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
               ws, nws)
     else:
         _call(device, stream, _c_product16, a.data_ptr(), fmt, lda, bp, ldb, sp, lds, out.data_ptr(), ldc, M, N, K)
+    _keep(stream, a, b, out, workspace)
     return out
