@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from ._lib import MoeArgs, lib
-from .mx4 import FORMATS, MX4, _call, _given, _keep, _new, _workspace
+from .mx4 import FORMATS, MX4, _call, _check_stream, _given, _keep, _new, _workspace
 
 MAX_TOKENS, MAX_EXPERTS, MAX_TOP_K = 64, 512, 16
 
@@ -68,6 +68,7 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
         raise TypeError("16-bit weights must have x's dtype")
     if not x.is_cuda or len({x.device, logits.device, w_gate_up.device, w_down.device}) != 1:
         raise ValueError("inputs must share one GPU device")
+    _check_stream(stream, x.device)
     T, H = x.shape
     E, H2, I = w_down.shape
     if logits.shape != (T, E) or w_gate_up.shape != (E, 2 * I, H) or H2 != H or min(T, H, E, I) <= 0:

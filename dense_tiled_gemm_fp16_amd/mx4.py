@@ -43,6 +43,11 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
 
+def _check_stream(stream, device):
+    if stream is not None and stream.device != device:
+        raise ValueError("stream must be one of the inputs' device")
+
+
 def _call(device, stream, fn, *args):
     """fn(*args, stream) with `device` current."""
     index = device.index
@@ -210,6 +215,7 @@ def quantize_mx4(x, out=None, stream=None):
         raise ValueError("empty shape")
     if min(strides) <= 0:
         raise ValueError("strides must be positive")
+    _check_stream(stream, device)
     if out is None:
         out = MX4._empty(shape, device, stream)
     elif out.shape != tuple(shape) or out.device != device or not out.is_contiguous():
@@ -231,6 +237,7 @@ def dequantize_mx4(q, dtype=torch.bfloat16, out=None, stream=None):
         raise TypeError("dtype must be float16, bfloat16 or float32")
     if not q.is_cuda or min(shape) <= 0:
         raise ValueError("expected a non-empty MX4 on a GPU")
+    _check_stream(stream, device)
     if out is None:
         out = _new(shape, dtype, device, stream)
     elif out.dtype != dtype or out.device != device or out.shape != shape or \
@@ -274,6 +281,7 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
     device = b.device
     if device.type != "cuda" or a.device != device:
         raise ValueError("inputs must share one GPU device")
+    _check_stream(stream, device)
     (M, K), (N, Kb) = a.shape, b.shape
     if K != Kb or M <= 0 or N <= 0 or K <= 0:
         raise ValueError("incompatible or empty shape")

@@ -1,6 +1,7 @@
 """A stream by argument: what the call reads there stays what it was until the
 stream has read it, although the caller drops its last reference right after
-the call, and what it writes is not handed out before it is written."""
+the call, and what it writes is not handed out before it is written.  A stream
+of another device is refused."""
 import pytest
 import torch
 
@@ -90,3 +91,20 @@ def test_outputs_and_workspaces_of_a_stream_by_argument():
         assert all((t == 9).all() for t in again), give
         if give == "workspace":
             assert torch.equal(y, g.gemm_mx4(a, b))
+
+
+class Elsewhere:
+    """The handle of the default stream, said to be another device's."""
+    device = torch.device("cuda:1")
+    cuda_stream = 0
+
+
+def test_stream_of_another_device():
+    x = randn(8, 64)
+    q = g.quantize_mx4(x)
+    say("stream of another device")
+    for call in (lambda s: g.quantize_mx4(x, stream=s), lambda s: g.dequantize_mx4(q, stream=s),
+                 lambda s: g.gemm_mx4(q, q, stream=s), lambda s: g.gemm_mx4(x, q, stream=s),
+                 lambda s: g.gemm_moe(x, randn(8, 2), randn(2, 32, 64), randn(2, 64, 16), 1, stream=s)):
+        with pytest.raises(ValueError):
+            call(Elsewhere())
