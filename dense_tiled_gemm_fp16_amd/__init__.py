@@ -17,6 +17,11 @@ device memory and the current stream.
                                       products with 4-bit weights (mx4.py)
     gemm_moe(x, logits, w_gate_up, w_down, top_k)
                                    -> a mixture-of-experts layer for a few tokens (moe.py)
+
+Each call only enqueues its kernels, on the inputs' device's current stream or
+on the one given as `stream`.  In the latter case it is the caller's to have
+that stream wait for what the inputs come from, and whoever reads the result
+for that stream; the tensors themselves may be dropped right after the call.
 """
 import ctypes
 
@@ -25,7 +30,7 @@ import torch
 from ._lib import (GEMM_OK, LIB_PATH, PATHS, STATUS, VARIANTS, Opts, PlanInfo, lib, make_opts,
                    status_string)
 from .moe import gemm_moe, gemm_moe_workspace_bytes
-from .mx4 import MX4, dequantize_mx4, gemm_mx4, gemm_mx4_workspace_bytes, quantize_mx4
+from .mx4 import MX4, _keep, _new, dequantize_mx4, gemm_mx4, gemm_mx4_workspace_bytes, quantize_mx4
 
 __all__ = ["gemm", "gemm_raw", "gemm_noalloc", "gemm_grouped", "pack_b", "gemm_packed", "PackedB", "plan",
            "workspace_bytes", "GemmError", "LIB_PATH",
@@ -39,7 +44,7 @@ class GemmError(RuntimeError):
         self.status = rc
 
 
-def _check(a, b, out):
+def _check(a, b, out, stream=None):
     # Argument checks in the spirit of the Triton article's wrapper (section
     # "addresses and bounds in one short kernel"); the library re-validates.
     if a.ndim != 2 or b.ndim != 2:
@@ -61,7 +66,7 @@ def _check(a, b, out):
     if min(a.stride() + b.stride()) <= 0:
         raise ValueError("strides must be positive")
     if out is None:
-        out = torch.empty((m, n), device=a.device, dtype=out_dtype)
+        out = _new((m, n), out_dtype, a.device, stream)
     else:
         if out.dtype != out_dtype or out.device != a.device or out.shape != (m, n):
             raise ValueError("out must be an [M, N] tensor of the output dtype on the inputs' device")
@@ -99,19 +104,19 @@ def gemm(a, b, out=None, workspace=None, variant="auto", split_k=0, panel=0, til
          stream=None):
     """C = a @ b with fp32 accumulation, output in the inputs' format (float16
     or bfloat16), computed by libgemmf16."""
-    m, n, k, out = _check(a, b, out)
+    m, n, k, out = _check(a, b, out, stream)
     opts = make_opts(variant, split_k, panel, tile)
-    if stream is None:
-        stream = torch.cuda.current_stream(a.device)
+    s = torch.cuda.current_stream(a.device) if stream is None else stream
     ws_ptr, ws_bytes = 0, 0
     if workspace is not None:
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     with torch.cuda.device(a.device):
         rc = _fn(a, "gemm_f16_ex", b)(a.data_ptr(), a.stride(0), a.stride(1), b.data_ptr(),
                                    b.stride(0), b.stride(1), out.data_ptr(), out.stride(0), m, n,
-                                   k, stream.cuda_stream, ws_ptr, ws_bytes, ctypes.byref(opts))
+                                   k, s.cuda_stream, ws_ptr, ws_bytes, ctypes.byref(opts))
     if rc != GEMM_OK:
         raise GemmError(rc)
+    _keep(stream, a, b, out, workspace)
     return out
 
 
@@ -121,15 +126,15 @@ def gemm_noalloc(a, b, out, stream=None):
     the size limit and for calls that overlap on one GPU)."""
     if a.dtype != torch.float16 or b.dtype != torch.float16 or out is None:
         raise TypeError("gemm_noalloc takes float16 a, b and a float16 out")
-    m, n, k, out = _check(a, b, out)
-    if stream is None:
-        stream = torch.cuda.current_stream(a.device)
+    m, n, k, out = _check(a, b, out, stream)
+    s = torch.cuda.current_stream(a.device) if stream is None else stream
     with torch.cuda.device(a.device):
         rc = lib.gemm_f16_noalloc(a.data_ptr(), a.stride(0), a.stride(1), b.data_ptr(), b.stride(0),
                                   b.stride(1), out.data_ptr(), out.stride(0), m, n, k,
-                                  stream.cuda_stream)
+                                  s.cuda_stream)
     if rc != GEMM_OK:
         raise GemmError(rc)
+    _keep(stream, a, b, out)
     return out
 
 
@@ -155,12 +160,11 @@ def gemm_grouped(a, b, offsets, out=None, workspace=None, stream=None):
     if kb != k or min(m, n, k, g) <= 0 or offsets.shape != (g + 1,) or offsets.stride(0) != 1:
         raise ValueError("incompatible or empty shape, or offsets not a contiguous [G + 1] vector")
     if out is None:
-        out = torch.empty((m, n), device=a.device, dtype=c_dtype)
+        out = _new((m, n), c_dtype, a.device, stream)
     elif out.dtype != c_dtype or out.device != a.device or out.shape != (m, n) or out.stride(1) != 1:
         raise ValueError("out must be a row-major [M, N] tensor of the output format (float16 for FP8 "
                          "inputs) on the inputs' device")
-    if stream is None:
-        stream = torch.cuda.current_stream(a.device)
+    s = torch.cuda.current_stream(a.device) if stream is None else stream
     ws_ptr, ws_bytes = 0, 0
     if workspace is not None:
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -169,12 +173,13 @@ def gemm_grouped(a, b, offsets, out=None, workspace=None, stream=None):
                 b.stride(2), out.data_ptr(), out.stride(0), offsets.data_ptr(), g, m, n, k)
         if f8:
             rc = lib.gemm_f8_grouped(*args, F8_FORMATS[a.dtype], F8_FORMATS[b.dtype],
-                                     stream.cuda_stream, ws_ptr, ws_bytes)
+                                     s.cuda_stream, ws_ptr, ws_bytes)
         else:
             fn = lib.gemm_f16_grouped if a.dtype == torch.float16 else lib.gemm_bf16_grouped
-            rc = fn(*args, stream.cuda_stream, ws_ptr, ws_bytes)
+            rc = fn(*args, s.cuda_stream, ws_ptr, ws_bytes)
     if rc != GEMM_OK:
         raise GemmError(rc)
+    _keep(stream, a, b, offsets, out, workspace)
     return out
 
 
@@ -216,14 +221,14 @@ def pack_b(b, stream=None):
     nbytes = int(lib.gemm_f16_packed_b_bytes(K, N))
     if nbytes == 0:
         raise ValueError("empty or oversized shape")
-    data = torch.empty(nbytes, dtype=torch.uint8, device=b.device)
-    if stream is None:
-        stream = torch.cuda.current_stream(b.device)
+    data = _new(nbytes, torch.uint8, b.device, stream)
+    s = torch.cuda.current_stream(b.device) if stream is None else stream
     with torch.cuda.device(b.device):
         rc = lib.gemm_f16_pack_b(b.data_ptr(), b.stride(0), b.stride(1), K, N, data.data_ptr(),
-                                 stream.cuda_stream)
+                                 s.cuda_stream)
     if rc != GEMM_OK:
         raise GemmError(rc)
+    _keep(stream, b)
     return PackedB(data, K, N)
 
 
@@ -235,14 +240,14 @@ def gemm_packed(a, packed, out=None, stream=None):
         raise ValueError("a and the packed B must share the GPU and K")
     m, n = a.shape[0], packed.N
     if out is None:
-        out = torch.empty((m, n), device=a.device, dtype=torch.float16)
+        out = _new((m, n), torch.float16, a.device, stream)
     elif out.dtype != torch.float16 or out.shape != (m, n) or out.stride(1) != 1:
         raise ValueError("out must be a row-major float16 [M, N] tensor")
-    if stream is None:
-        stream = torch.cuda.current_stream(a.device)
+    s = torch.cuda.current_stream(a.device) if stream is None else stream
     with torch.cuda.device(a.device):
         rc = lib.gemm_f16_packed(a.data_ptr(), a.stride(0), a.stride(1), packed.data.data_ptr(),
-                                 out.data_ptr(), out.stride(0), m, n, packed.K, stream.cuda_stream)
+                                 out.data_ptr(), out.stride(0), m, n, packed.K, s.cuda_stream)
     if rc != GEMM_OK:
         raise GemmError(rc)
+    _keep(stream, a, packed.data, out)
     return out

@@ -52,8 +52,6 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
 
     Sums are fp32, and silu(g) * u keeps 16 significant bits at any magnitude.
 
-    stream: the stream to run on instead of the current one (as in mx4.py).
-
     workspace: gemm_moe_workspace_bytes(T, E, top_k, H, I) bytes, 256-byte
     aligned, not shared with a call that may overlap; allocated here when not
     given."""

@@ -9,10 +9,7 @@ computation runs in the HIP library.
                                      or float16 / bfloat16 [M, K]
     gemm_mx4_workspace_bytes(M, N, K)
 
-Each call only enqueues its kernels, on the inputs' device's current stream or
-on the one given as `stream`.  In the latter case it is the caller's to have
-that stream wait for what the inputs come from, and whoever reads the result
-for that stream; the tensors themselves may be dropped right after the call.
+A stream by argument: as the package says.
 """
 import torch
 

@@ -108,3 +108,57 @@ def test_stream_of_another_device():
                  lambda s: g.gemm_moe(x, randn(8, 2), randn(2, 32, 64), randn(2, 64, 16), 1, stream=s)):
         with pytest.raises(ValueError):
             call(Elsewhere())
+
+
+# ---- the 16-bit and FP8 products, by the same rules
+
+def offsets(*rows):
+    return torch.tensor(rows, dtype=torch.int64, device=DEV)
+
+
+SMALL, BIG = 512, 16384     # BIG: plans that pack B into a workspace of the library
+OLDER = {
+    "gemm": (lambda: (randn(600, K), randn(K, SMALL)), lambda a, b, stream: g.gemm(a, b, stream=stream)),
+    "gemm f8": (lambda: (randn(64, K).to(torch.float8_e4m3fn), randn(SMALL, K).to(torch.float8_e4m3fn)),
+                lambda a, b, stream: g.gemm(a, b.t(), stream=stream)),
+    "gemm packing": (lambda: (randn(BIG, 256), randn(SMALL, 256)), lambda a, b, stream: g.gemm(a, b.t(), stream=stream)),
+    "noalloc": (lambda: (randn(600, K), randn(K, SMALL)),
+                lambda a, b, stream: g.gemm_noalloc(a, b, noalloc_out(stream), stream=stream)),
+    "grouped": (lambda: (randn(600, K), randn(3, K, SMALL), offsets(0, 100, 400, 600)),
+                lambda a, b, o, stream: g.gemm_grouped(a, b, o, stream=stream)),
+    "pack": (lambda: (randn(K, SMALL),), lambda b, stream: g.pack_b(b, stream=stream).data),
+    "packed": (lambda: (randn(300, K), g.pack_b(randn(K, SMALL)).data),
+               lambda a, d, stream: g.gemm_packed(a, g.PackedB(d, K, SMALL), stream=stream)),
+}
+
+
+def noalloc_out(stream):
+    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+        return torch.empty(600, SMALL, dtype=torch.float16, device=DEV)
+
+
+@pytest.mark.parametrize("name", list(OLDER))
+def test_inputs_of_older_calls(name):
+    make, call = OLDER[name]
+    say(f"stream inputs {name}")
+    want, got = dropped(torch.cuda.Stream(DEV), make, call)
+    assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("name", [n for n in OLDER if n != "noalloc"])
+def test_results_of_older_calls_take_no_memory_in_use(name):
+    """The result is written by the side stream while the current one is still
+    busy with what was freed there."""
+    make, call = OLDER[name]
+    side = torch.cuda.Stream(DEV)
+    inputs = make()
+    want = call(*inputs, stream=None)
+    say(f"stream results {name}")
+    torch.cuda.synchronize()
+    held = torch.empty(want.numel() * want.element_size(), dtype=torch.uint8, device=DEV)
+    torch.cuda._sleep(CYCLES)
+    held.fill_(9)                        # after the sleep; the memory is free for the next caller at once
+    del held
+    got = call(*inputs, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
