@@ -30,7 +30,8 @@ import torch
 from ._lib import (GEMM_OK, LIB_PATH, PATHS, STATUS, VARIANTS, Opts, PlanInfo, lib, make_opts,
                    status_string)
 from .moe import gemm_moe, gemm_moe_workspace_bytes
-from .mx4 import MX4, _keep, _new, dequantize_mx4, gemm_mx4, gemm_mx4_workspace_bytes, quantize_mx4
+from .mx4 import (MX4, _check_stream, _keep, _new, dequantize_mx4, gemm_mx4, gemm_mx4_workspace_bytes,
+                  quantize_mx4)
 
 __all__ = ["gemm", "gemm_raw", "gemm_noalloc", "gemm_grouped", "pack_b", "gemm_packed", "PackedB", "plan",
            "workspace_bytes", "GemmError", "LIB_PATH",
@@ -51,6 +52,7 @@ def _check(a, b, out, stream=None):
         raise ValueError("expected two matrices")
     if not a.is_cuda or not b.is_cuda or a.device != b.device:
         raise ValueError("inputs must share one GPU device")
+    _check_stream(stream, a.device)
     if a.dtype in F8_FORMATS or b.dtype in F8_FORMATS:
         if a.dtype not in F8_FORMATS or b.dtype not in F8_FORMATS:
             raise TypeError("FP8 inputs must both be float8_e4m3fn or float8_e5m2")
@@ -150,6 +152,7 @@ def gemm_grouped(a, b, offsets, out=None, workspace=None, stream=None):
         raise ValueError("expected a [M, K] matrix and a [G, K, N] stack")
     if not (a.is_cuda and b.is_cuda and offsets.is_cuda) or len({a.device, b.device, offsets.device}) != 1:
         raise ValueError("inputs must share one GPU device")
+    _check_stream(stream, a.device)
     f8 = a.dtype in F8_FORMATS and b.dtype in F8_FORMATS
     if not (f8 or (a.dtype in (torch.float16, torch.bfloat16) and b.dtype == a.dtype)) or \
             offsets.dtype != torch.int64:
@@ -217,6 +220,7 @@ def pack_b(b, stream=None):
     """Pack a static float16 B [K, N] (any positive strides) for gemm_packed."""
     if b.ndim != 2 or not b.is_cuda or b.dtype != torch.float16:
         raise ValueError("expected a float16 [K, N] matrix on a GPU")
+    _check_stream(stream, b.device)
     K, N = b.shape
     nbytes = int(lib.gemm_f16_packed_b_bytes(K, N))
     if nbytes == 0:
@@ -236,6 +240,7 @@ def gemm_packed(a, packed, out=None, stream=None):
     """C = a @ B for a float16 a [M, K] (K-contiguous rows) and B packed by pack_b."""
     if a.ndim != 2 or not a.is_cuda or a.dtype != torch.float16:
         raise ValueError("expected a float16 [M, K] matrix on a GPU")
+    _check_stream(stream, a.device)
     if packed.data.device != a.device or a.shape[1] != packed.K:
         raise ValueError("a and the packed B must share the GPU and K")
     m, n = a.shape[0], packed.N

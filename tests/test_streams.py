@@ -162,3 +162,14 @@ def test_results_of_older_calls_take_no_memory_in_use(name):
     got = call(*inputs, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+
+
+def test_older_calls_on_a_stream_of_another_device():
+    a, b = randn(64, 64), randn(64, 64)
+    p = g.pack_b(b)
+    say("older calls, stream of another device")
+    for call in (lambda s: g.gemm(a, b, stream=s), lambda s: g.gemm_noalloc(a, b, torch.empty_like(a), stream=s),
+                 lambda s: g.gemm_grouped(a, b[None], offsets(0, 64), stream=s), lambda s: g.pack_b(b, stream=s),
+                 lambda s: g.gemm_packed(a, p, stream=s)):
+        with pytest.raises(ValueError):
+            call(Elsewhere())
