@@ -5,8 +5,9 @@
 // instructions, and what one 16-byte load brings.  The packed converts
 // (v_cvt_scalef32_pk_*) work on one byte = two codes at a time; the code to
 // bfloat16 convert is exact for every scale byte (measured over all 256 x 16,
-// subnormal scales and the NaN scale included), the one to binary16 for scale
-// bytes 104 .. 140 and, below 61, gives zeros.
+// subnormal scales and the NaN scale included; values of 2^128 and more, at scale
+// bytes 253 and 254, become infinite), the one to binary16 for scale bytes 104 ..
+// 140 and, below 61, gives zeros.
 #pragma once
 
 #include <cstring>

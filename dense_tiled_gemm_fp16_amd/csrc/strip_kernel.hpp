@@ -35,7 +35,8 @@
 //                    instructions; with an MX4 A one scaled 128-k instruction
 //                    takes the chunk.
 //
-// Weights in MX4 are widened exactly: to bfloat16 at any scale; to binary16,
+// Weights in MX4 are widened exactly: to bfloat16 at any scale (values of 2^128
+// and more, which the quantiser does not give, become infinite there); to binary16,
 // for a binary16 A, where the scale byte is in 104 .. 140.  Other scales take
 // the chunk through bfloat16, A split exactly into two bfloat16 parts; all but
 // 0, the scale of a block of zeros: whatever nonzero codes it has (up to 2^-124)

@@ -269,7 +269,8 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
     a an MX4 [M, K]: C in dtype (float16, the default, or bfloat16), on the
     scaled 4-bit matrix instructions.
     a float16 or bfloat16 [M, K] with unit stride along K: C in a's dtype, the
-    weights exact; made for few rows (beyond some 64, quantise a first).
+    weights exact (below 2^128, as all of a quantised tensor are); made for few
+    rows (beyond some 64, quantise a first).
 
     workspace: gemm_mx4_workspace_bytes(M, N, K) bytes, 256-byte aligned, not
     shared with a call that may overlap; allocated here when not given."""

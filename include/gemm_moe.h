@@ -12,7 +12,7 @@
  *            or over all experts
  *     (g, u) = the first and the last I of W1[e] x_t,  W1[e] [2I, H]
  *     y_t  = sum over e in S_t of p_te W2[e] (silu(g) * u),  W2[e] [H, I]
- * with silu(g) = g / (1 + exp(-g)).  A token whose logits are all -inf gets
+ * with silu(g) = g / (1 + exp(-g)).  MX4 weights enter as in gemm_mx4_a16.  A token whose logits are all -inf gets
  * zeros.  Sums are fp32; silu(g) * u is carried as two bfloat16 parts (off by
  * at most 2^-16 of its value, at any magnitude), and Y is rounded once.  Results are deterministic: experts are added in ascending
  * order, without atomics on floating-point values; the order of a token's sums

@@ -67,8 +67,12 @@ size_t gemm_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 /*
  * C[m,n] := sum_k A[m,k] B[n,k] for a 16-bit A (format fmt, GEMM_FMT_F16 or
  * GEMM_FMT_BF16; A[m,k] at A + m*lda + k) and MX4 B [N, K]; C has A's format.
- * The weights enter the products exactly, at any scale (with a binary16 A
- * those of scale 0, below 2^-124, as zeros).  A kernel for few
+ * The weights enter the products exactly, at any scale, with two exceptions:
+ * beside a binary16 A those of scale 0, below 2^-124, count as zeros, and
+ * values of 2^128 and more (codes of 4 and 6 at scale 253, of 2 and more at
+ * scale 254, neither of which the quantiser gives) are past the range: the
+ * outputs of their row are infinite or NaN.  (gemm_mx4 takes those exactly too.)
+ * A kernel for few
  * rows (the weights are read once per 32 rows of A): with many rows, quantise
  * A and call gemm_mx4.  Rows of A at most 2^25 elements apart, rows of B as
  * above (GEMM_ERR_LAYOUT); M up to 65535 * 32, N up to 2^27 (GEMM_ERR_SHAPE).

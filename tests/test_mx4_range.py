@@ -117,3 +117,30 @@ def test_mx4_products_at_extreme_scales(sa, sb, M, N):
     want = av @ bv.T
     tol = ref.product_tolerance(want, np.abs(av) @ np.abs(bv).T, K + 8, info.eps, info.smallest_normal * info.eps)
     assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("M", [1, 20, 40])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_weights_past_fp32_beside_16_bits(M, dtype):
+    """Scales 253 and 254, which the quantiser never gives: values below 2^128
+    are exact, the others infinite when dequantised, and no finite output hides
+    them."""
+    K = 32
+    x = torch.full((M, K), 2.0 ** -14, dtype=dtype, device=DEV)
+    data, scales = np.zeros((16, 16), dtype=np.uint8), np.full((16, 1), 253, dtype=np.uint8)
+    data[:, 3] = np.arange(16)                # code n of weight row n at k = 6
+    say(f"mx4 largest scales {M} {dtype}")
+    for scale in (253, 254):
+        scales[:] = scale
+        q = mx4(data, scales, K)
+        values = g.dequantize_mx4(q, torch.float32)[:, 6].double().cpu()
+        exact = torch.from_numpy(ref.values(data, scales, K)[:, 6])
+        assert torch.equal(values, torch.where(exact.abs() < 2.0 ** 128, exact, exact * torch.inf))
+        want = (values * 2.0 ** -14).to(dtype).expand(M, 16)
+        got = g.gemm_mx4(x, q).cpu()
+        held = torch.isfinite(values)
+        assert torch.equal(got[:, held], want[:, held]) and not torch.isfinite(got[:, ~held]).any()
+    # the product of two MX4 matrices multiplies the scales first
+    small = mx4(np.full((M, 16), 0x22, dtype=np.uint8), np.full((M, 1), 27, dtype=np.uint8), K)   # 1.0 at 2^-100
+    got = g.gemm_mx4(small, q, dtype=torch.bfloat16).double().cpu()
+    assert torch.equal(got, (exact * 2.0 ** -100).expand(M, 16))
