@@ -52,7 +52,8 @@ def _check(a, b, out, stream=None):
         raise ValueError("expected two matrices")
     if not a.is_cuda or not b.is_cuda or a.device != b.device:
         raise ValueError("inputs must share one GPU device")
-    _check_stream(stream, a.device)
+    if stream is not None:
+        _check_stream(stream, a.device)
     if a.dtype in F8_FORMATS or b.dtype in F8_FORMATS:
         if a.dtype not in F8_FORMATS or b.dtype not in F8_FORMATS:
             raise TypeError("FP8 inputs must both be float8_e4m3fn or float8_e5m2")
@@ -118,7 +119,8 @@ def gemm(a, b, out=None, workspace=None, variant="auto", split_k=0, panel=0, til
                                    k, s.cuda_stream, ws_ptr, ws_bytes, ctypes.byref(opts))
     if rc != GEMM_OK:
         raise GemmError(rc)
-    _keep(stream, a, b, out, workspace)
+    if stream is not None:
+        _keep(stream, a, b, out, workspace)
     return out
 
 
@@ -136,7 +138,8 @@ def gemm_noalloc(a, b, out, stream=None):
                                   s.cuda_stream)
     if rc != GEMM_OK:
         raise GemmError(rc)
-    _keep(stream, a, b, out)
+    if stream is not None:
+        _keep(stream, a, b, out)
     return out
 
 
@@ -152,7 +155,8 @@ def gemm_grouped(a, b, offsets, out=None, workspace=None, stream=None):
         raise ValueError("expected a [M, K] matrix and a [G, K, N] stack")
     if not (a.is_cuda and b.is_cuda and offsets.is_cuda) or len({a.device, b.device, offsets.device}) != 1:
         raise ValueError("inputs must share one GPU device")
-    _check_stream(stream, a.device)
+    if stream is not None:
+        _check_stream(stream, a.device)
     f8 = a.dtype in F8_FORMATS and b.dtype in F8_FORMATS
     if not (f8 or (a.dtype in (torch.float16, torch.bfloat16) and b.dtype == a.dtype)) or \
             offsets.dtype != torch.int64:
@@ -182,7 +186,8 @@ def gemm_grouped(a, b, offsets, out=None, workspace=None, stream=None):
             rc = fn(*args, s.cuda_stream, ws_ptr, ws_bytes)
     if rc != GEMM_OK:
         raise GemmError(rc)
-    _keep(stream, a, b, offsets, out, workspace)
+    if stream is not None:
+        _keep(stream, a, b, offsets, out, workspace)
     return out
 
 
@@ -220,7 +225,8 @@ def pack_b(b, stream=None):
     """Pack a static float16 B [K, N] (any positive strides) for gemm_packed."""
     if b.ndim != 2 or not b.is_cuda or b.dtype != torch.float16:
         raise ValueError("expected a float16 [K, N] matrix on a GPU")
-    _check_stream(stream, b.device)
+    if stream is not None:
+        _check_stream(stream, b.device)
     K, N = b.shape
     nbytes = int(lib.gemm_f16_packed_b_bytes(K, N))
     if nbytes == 0:
@@ -232,7 +238,8 @@ def pack_b(b, stream=None):
                                  s.cuda_stream)
     if rc != GEMM_OK:
         raise GemmError(rc)
-    _keep(stream, b)
+    if stream is not None:
+        _keep(stream, b)
     return PackedB(data, K, N)
 
 
@@ -240,7 +247,8 @@ def gemm_packed(a, packed, out=None, stream=None):
     """C = a @ B for a float16 a [M, K] (K-contiguous rows) and B packed by pack_b."""
     if a.ndim != 2 or not a.is_cuda or a.dtype != torch.float16:
         raise ValueError("expected a float16 [M, K] matrix on a GPU")
-    _check_stream(stream, a.device)
+    if stream is not None:
+        _check_stream(stream, a.device)
     if packed.data.device != a.device or a.shape[1] != packed.K:
         raise ValueError("a and the packed B must share the GPU and K")
     m, n = a.shape[0], packed.N
@@ -254,5 +262,6 @@ def gemm_packed(a, packed, out=None, stream=None):
                                  out.data_ptr(), out.stride(0), m, n, packed.K, s.cuda_stream)
     if rc != GEMM_OK:
         raise GemmError(rc)
-    _keep(stream, a, packed.data, out)
+    if stream is not None:
+        _keep(stream, a, packed.data, out)
     return out

@@ -66,7 +66,8 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
         raise TypeError("16-bit weights must have x's dtype")
     if not x.is_cuda or len({x.device, logits.device, w_gate_up.device, w_down.device}) != 1:
         raise ValueError("inputs must share one GPU device")
-    _check_stream(stream, x.device)
+    if stream is not None:
+        _check_stream(stream, x.device)
     T, H = x.shape
     E, H2, I = w_down.shape
     if logits.shape != (T, E) or w_gate_up.shape != (E, 2 * I, H) or H2 != H or min(T, H, E, I) <= 0:
@@ -89,5 +90,6 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
     if workspace is None:
         workspace = _workspace(lib.gemm_moe_workspace_bytes(T, E, top_k, H, I), x.device, stream)
     _call(x.device, stream, _c_layer, ctypes.byref(args), *_given(workspace, x.device))
-    _keep(stream, x, logits, w_gate_up, w_down, out, workspace)
+    if stream is not None:
+        _keep(stream, x, logits, w_gate_up, w_down, out, workspace)
     return out

@@ -41,7 +41,7 @@ _current_device = torch._C._cuda_getDevice
 
 
 def _check_stream(stream, device):
-    if stream is not None and stream.device != device:
+    if stream.device != device:
         raise ValueError("stream must be one of the inputs' device")
 
 
@@ -80,11 +80,10 @@ def _keep(stream, *used):
     """Tensors and MX4s that a call on a stream by argument uses: the caller may
     drop them right after the call, and then their memory is not handed out
     again before the stream is done with them."""
-    if stream is not None:
-        for u in used:
-            for t in u._tensors() if isinstance(u, MX4) else (u,):
-                if t is not None:
-                    t.record_stream(stream)
+    for u in used:
+        for t in u._tensors() if isinstance(u, MX4) else (u,):
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _given(workspace, device):
@@ -212,7 +211,8 @@ def quantize_mx4(x, out=None, stream=None):
         raise ValueError("empty shape")
     if min(strides) <= 0:
         raise ValueError("strides must be positive")
-    _check_stream(stream, device)
+    if stream is not None:
+        _check_stream(stream, device)
     if out is None:
         out = MX4._empty(shape, device, stream)
     elif out.shape != tuple(shape) or out.device != device or not out.is_contiguous():
@@ -221,7 +221,8 @@ def quantize_mx4(x, out=None, stream=None):
     data, _, scales, _ = out._rows()
     _call(device, stream, _c_quantize, x.data_ptr(), fmt, sg, strides[-2], strides[-1], G, shape[-2], shape[-1],
           data, scales)
-    _keep(stream, x, out)
+    if stream is not None:
+        _keep(stream, x, out)
     return out
 
 
@@ -234,7 +235,8 @@ def dequantize_mx4(q, dtype=torch.bfloat16, out=None, stream=None):
         raise TypeError("dtype must be float16, bfloat16 or float32")
     if not q.is_cuda or min(shape) <= 0:
         raise ValueError("expected a non-empty MX4 on a GPU")
-    _check_stream(stream, device)
+    if stream is not None:
+        _check_stream(stream, device)
     if out is None:
         out = _new(shape, dtype, device, stream)
     elif out.dtype != dtype or out.device != device or out.shape != shape or \
@@ -253,7 +255,8 @@ def dequantize_mx4(q, dtype=torch.bfloat16, out=None, stream=None):
         R, lds, ldy = R * shape[1], -(-K // BLOCK), K
         ldd = 16 * lds
     _call(device, stream, _c_dequantize, data, ldd, scales, lds, R, K, out.data_ptr(), fmt, ldy)
-    _keep(stream, q, out)
+    if stream is not None:
+        _keep(stream, q, out)
     return out
 
 
@@ -279,7 +282,8 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
     device = b.device
     if device.type != "cuda" or a.device != device:
         raise ValueError("inputs must share one GPU device")
-    _check_stream(stream, device)
+    if stream is not None:
+        _check_stream(stream, device)
     (M, K), (N, Kb) = a.shape, b.shape
     if K != Kb or M <= 0 or N <= 0 or K <= 0:
         raise ValueError("incompatible or empty shape")
@@ -318,5 +322,6 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
               ws, nws)
     else:
         _call(device, stream, _c_product16, a.data_ptr(), fmt, lda, bp, ldb, sp, lds, out.data_ptr(), ldc, M, N, K)
-    _keep(stream, a, b, out, workspace)
+    if stream is not None:
+        _keep(stream, a, b, out, workspace)
     return out
