@@ -80,12 +80,12 @@ def gemm_moe(x, logits, w_gate_up, w_down, top_k, renormalize=True, out=None, wo
     if out is None:
         out = _new((T, H), x.dtype, x.device, stream)
     elif out.dtype != x.dtype or out.device != x.device or out.shape != (T, H) or \
-            (out.stride(1) != 1 and H > 1) or out.stride(0) < H:
+            (out.stride(1) != 1 and H > 1) or (out.stride(0) < H and T > 1):
         raise ValueError("out must be a row-major [T, H] tensor of x's dtype on its device")
     p1, e1, n1, s1, se1, sn1 = _weights(w_gate_up, "w_gate_up")
     p2, e2, n2, s2, se2, sn2 = _weights(w_down, "w_down")
     args = MoeArgs(x.data_ptr(), x.stride(0), logits.data_ptr(), logits.stride(0), p1, e1, n1, s1, se1, sn1,
-                   p2, e2, n2, s2, se2, sn2, out.data_ptr(), out.stride(0), T, E, H, I, top_k,
+                   p2, e2, n2, s2, se2, sn2, out.data_ptr(), out.stride(0) if T > 1 else H, T, E, H, I, top_k,
                    FORMATS[x.dtype], FORMATS[logits.dtype], int(quantised), int(bool(renormalize)))
     if workspace is None:
         workspace = _workspace(lib.gemm_moe_workspace_bytes(T, E, top_k, H, I), x.device, stream)

@@ -245,7 +245,7 @@ def dequantize_mx4(q, dtype=torch.bfloat16, out=None, stream=None):
                          "(a stack contiguous)")
     R, K = shape[0], shape[-1]
     data, ldd, scales, lds = q._rows()
-    ldy = out.stride(-2)
+    ldy = out.stride(-2) if R > 1 else K      # a single row has no next one
     if len(shape) == 3:
         if not q.is_contiguous():
             for i in range(R):
@@ -305,9 +305,9 @@ def gemm_mx4(a, b, out=None, dtype=None, workspace=None, stream=None):
     if out is None:
         out = _new((M, N), dtype, device, stream)
     elif out.dtype != dtype or out.device != device or out.shape != (M, N) or \
-            (out.stride(1) != 1 and N > 1) or out.stride(0) < N:
+            (out.stride(1) != 1 and N > 1) or (out.stride(0) < N and M > 1):
         raise ValueError("out must be a row-major [M, N] tensor of the output dtype on the inputs' device")
-    else:
+    elif M > 1:
         ldc = out.stride(0)
     fmt = FORMATS[dtype]
     bp, ldb, sp, lds = b._rows()
