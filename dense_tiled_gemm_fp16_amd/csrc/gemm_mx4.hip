@@ -189,7 +189,7 @@ int launch_tile(const StripArgs& a, const TilePlan& p, void* ws, hipStream_t s) 
   t.k.K = a.K;
   t.k.GM = cdiv(a.M, Mx4Cfg::BM);
   t.k.GN = cdiv(a.N, Mx4Cfg::BN);
-  t.k.panel = 8;   // 32768 x 2048 x 7168: 228 us, 236 with 4, 235 with 16; within 1% on squares
+  t.k.panel = 8;   // 32768 x 2048 x 7168, one run: 228 us, 236 with 4, 235 with 16; within 1% on squares
   t.sa = sa;
   t.sa_rows = p.sa_rows;
   t.sb = sb;

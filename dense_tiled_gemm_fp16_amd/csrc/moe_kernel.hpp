@@ -16,7 +16,7 @@
 //
 //   moe_up    wave -> (expert, 16 rows of I, a part of H): gate and up strips
 //             of 16 rows each; the parts of H meet in LDS; silu(g) u, two
-//             16-bit parts per value, into row (token, slot).  The waves of a
+//             bfloat16 parts per value, into row (token, slot).  The waves of a
 //             workgroup are kMoeWaves / parts neighbouring strips times the
 //             parts: as few parts as still fill the device, so that a wave
 //             streams long rows and the workgroup's waves meet A in L1.  With
@@ -33,10 +33,12 @@
 //             workgroups, `splits` of them share the sequence of a strip, and
 //             moe_sum adds their sums in order.
 //
-// Measured (us, H 7168, I 2048, top 8 of 64 experts; what the weights take at
-// the 6.4 TB/s of plain reads in brackets): bfloat16, 1 token 74 + 41 (73 + 37),
-// 64 tokens 576 + 311 (587 + 294); MX4, 16 tokens 200 + 112 (139 + 69), where
-// scale bytes fetched more than once, LDS and conversions take the rest.
+// Measured (us, medians of a kernel trace, H 7168, I 2048, top 8 of 64 experts;
+// what the weights take at the 6.4 TB/s of plain reads in brackets): bfloat16, 1
+// token 75 + 43 (73 + 37), 64 tokens 592 + 324 (587 + 294; binary16 592 + 397, see
+// split_parts); MX4, 16 tokens 208 + 135 (139 + 69), where scale bytes fetched
+// more than once, LDS and conversions take the rest, 64 tokens 285 + 215 (156 +
+// 78).  In a graph the layer takes 118, 879, 309 and 464.
 #pragma once
 
 #include "strip_kernel.hpp"
@@ -124,9 +126,9 @@ __device__ __forceinline__ float softmax_weight(const MoeArgs& a, int t, int e, 
 // silu(g) u as two bfloat16 parts, what the down product takes: fp32 does not
 // enter the 16-bit matrix instructions, and two parts keep 2^-16 of a value (the
 // output keeps 2^-8 or 2^-11) over fp32's whole range.  Beside binary16 weights
-// too, which the down product then splits (4 tokens, top 2 of 16, H 2048, I 768:
-// the layer 27.1 us, with binary16 parts 25.0; 64 tokens, top 8 of 64, H 7168, I
-// 2048: 926 and 878): binary16 parts keep more of a value near 1, but their least
+// too, which the down product then splits (4 tokens, top 2 of 16, H 2048, I 768,
+// in a graph: the layer 27.1 us, with binary16 parts 25.0; 64 tokens, top 8 of 64,
+// H 7168, I 2048: 926 to 945 and 878): binary16 parts keep more of a value near 1, but their least
 // step is 2^-24 and they end at 65504, while silu(g) u may lie below and above.
 __device__ __forceinline__ void split_parts(float v, uint16_t& hi, uint16_t& lo) {
   hi = cvt_out<DT_BF16>(v);

@@ -15,7 +15,8 @@
 //            through LDS to be stored in whole lines.
 //
 // Measured (us; TB/s read plus written; a copy reaches 4.7): 32768 x 7168 rows
-// from bfloat16 104 to 113 (5.3 to 5.7), to bfloat16 108 to 121 (4.9 to 5.5);
+// from bfloat16 and back 239 in a graph (5.0), in a kernel trace 113 to 129 (4.6 to
+// 5.3) and 108 to 114 (5.2 to 5.5);
 // fp32 201 (5.3) and 195 (5.5; two 16-byte stores per lane, 32 bytes apart,
 // instead of side by side: 272); columns of bfloat16 131 (4.5; each lane storing
 // its own 16 bytes: 176); 30000 x 333 padded rows 9.6 each (a wave per row: 16.8

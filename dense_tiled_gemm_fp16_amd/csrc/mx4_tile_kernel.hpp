@@ -24,10 +24,12 @@
 // first transposes both scale arrays to [steps][rows] dwords, so that a step's
 // scales are 2 KiB of consecutive bytes: eight 256-byte DMA instructions.
 //
-// Measured: 32768 x 2048 x 7168 in 228 to 240 us (4.0 to 4.2 PFLOP/s; binary16's
-// main kernel 1.3 on it), 4096^3 41 us (3.4), scales 6 and 4 us of that order.
-// Four waves of 128 x 128, with two thirds of the LDS reads, took 264 us: it is
-// not the LDS but the clock that the matrix core's power leaves.
+// Measured: 32768 x 2048 x 7168 in 272 us after the quantiser (median of a kernel
+// trace, the least 254), 253 with the scales' kernel call after call in a graph
+// (3.8 PFLOP/s; binary16's main kernel 1.3), 228 to 240 on another machine; 4096^3
+// 42 us (3.3).  The scales take 7 and 4 us of it.  Four waves of 128 x 128, with two
+// thirds of the LDS reads, took 264 us beside 243 in one run: it is not the LDS but
+// the clock that the matrix core's power leaves.
 //
 // k past K: the last step, if K is no multiple of 128, is filled through
 // registers, codes of A past K zeroed.

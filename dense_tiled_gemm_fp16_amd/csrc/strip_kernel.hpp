@@ -22,10 +22,11 @@
 // order, without barriers.  The slot of a row's piece is XORed with bits of the
 // row, which keeps both sides free of bank conflicts.
 //
-// Measured per kernel: one token, H 7168, I 2048, 8 experts in bfloat16 6.3 and
-// 5.7 TB/s (74 and 41 us), 64 tokens, 64 experts 6.5 and 6.0; plain reads of the
-// same bytes 6.4; as products with MX4 weights, 1 x 2048 x 7168 5.3 us and 16 x
-// 7168 x 2048 4.2 us, of which some 2.5 are a launch and the sum over the waves.
+// Measured per kernel (medians of a kernel trace): one token, H 7168, I 2048, 8
+// experts in bfloat16 6.3 and 5.5 TB/s (75 and 43 us), 64 tokens, 64 experts 6.4
+// and 5.8; plain reads of the same bytes 6.4; as products with MX4 weights, in a
+// graph, 1 x 2048 x 7168 5.5 us and 16 x 7168 x 2048 4.4 us, of which some 2.5 are
+// a launch and the sum over the waves.
 //
 // Only the order of k is free, as long as both operands share it:
 //   16-bit weights   a chunk is 32 k; lane group g takes octet g.
@@ -94,8 +95,8 @@ __device__ __forceinline__ u32x4 load8_rest(const char* p, int64_t n) {
 
 // Wait states after matrix instructions, tied to their sums.  The compiler
 // counts the cycles a result needs before other instructions may read it within
-// a basic block, but leaves them out where the reader, often only a register
-// move, is the first of the next block: a group's sums pass through here
+// a basic block, but has left them out where the reader, often only a register
+// move, was the first of the next block: a group's sums pass through here
 // before any branch.  (16 states; the longest instruction here needs 12.)
 template <int N, int MT>
 __device__ __forceinline__ void settle(f32x4 (&a)[N][MT], int t) {
