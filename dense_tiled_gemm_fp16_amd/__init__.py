@@ -17,6 +17,16 @@ device memory and the current stream.
                                       products with 4-bit weights (mx4.py)
     gemm_moe(x, logits, w_gate_up, w_down, top_k)
                                    -> a mixture-of-experts layer for a few tokens (moe.py)
+    quantize_f8(x), gemm_f8_scaled(a, a_scales, b, b_scales)
+                                   -> 8-bit floating point with a scale for each block of
+                                      128, and products of it (f8_scaled.py)
+    rms_norm_f8(x, weight), rms_norm_backward(dy, h, weight)
+                                   -> the norm that feeds them, with the residual's
+                                      addition, and its gradients (norm.py)
+    moe_sort(experts, E), moe_gather(x, order), moe_combine(y, order, weights),
+    moe_combine_backward(dout, y, order, weights)
+                                   -> tokens sorted by expert for gemm_grouped, and back
+                                      (moe_rows.py)
 
 Each call only enqueues its kernels, on the inputs' device's current stream or
 on the one given as `stream`.  In the latter case it is the caller's to have
@@ -29,14 +39,19 @@ import torch
 
 from ._lib import (GEMM_OK, LIB_PATH, PATHS, STATUS, VARIANTS, Opts, PlanInfo, lib, make_opts,
                    status_string)
+from .f8_scaled import gemm_f8_scaled, gemm_f8_scaled_workspace_bytes, quantize_f8
 from .moe import gemm_moe, gemm_moe_workspace_bytes
+from .moe_rows import MoeOrder, moe_combine, moe_combine_backward, moe_gather, moe_sort, moe_sort_workspace_bytes
 from .mx4 import (MX4, _check_stream, _keep, _new, dequantize_mx4, gemm_mx4, gemm_mx4_workspace_bytes,
                   quantize_mx4)
+from .norm import rms_norm_backward, rms_norm_backward_workspace_bytes, rms_norm_f8
 
 __all__ = ["gemm", "gemm_raw", "gemm_noalloc", "gemm_grouped", "pack_b", "gemm_packed", "PackedB", "plan",
            "workspace_bytes", "GemmError", "LIB_PATH",
            "VARIANTS", "MX4", "quantize_mx4", "dequantize_mx4", "gemm_mx4", "gemm_mx4_workspace_bytes",
-           "gemm_moe", "gemm_moe_workspace_bytes"]
+           "gemm_moe", "gemm_moe_workspace_bytes", "quantize_f8", "gemm_f8_scaled",
+           "gemm_f8_scaled_workspace_bytes", "rms_norm_f8", "rms_norm_backward", "rms_norm_backward_workspace_bytes",
+           "MoeOrder", "moe_sort", "moe_sort_workspace_bytes", "moe_gather", "moe_combine", "moe_combine_backward"]
 
 
 class GemmError(RuntimeError):

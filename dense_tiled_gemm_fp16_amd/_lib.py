@@ -33,6 +33,13 @@ EXPORTS_MX4 = ["gemm_mx4_quantize", "gemm_mx4_dequantize", "gemm_mx4", "gemm_mx4
                "gemm_mx4_a16"]
 # Entry points of include/gemm_moe.h.
 EXPORTS_MOE = ["gemm_moe", "gemm_moe_workspace_bytes"]
+# Entry points of include/gemm_f8_scaled.h.
+EXPORTS_F8S = ["gemm_f8s_quantize", "gemm_f8s", "gemm_f8s_workspace_bytes"]
+# Entry points of include/rms_norm_f8.h.
+EXPORTS_NORM = ["gemm_rms_norm_f8", "gemm_rms_norm_backward", "gemm_rms_norm_backward_workspace_bytes"]
+# Entry points of include/gemm_moe_rows.h.
+EXPORTS_MOE_ROWS = ["gemm_moe_sort", "gemm_moe_sort_workspace_bytes", "gemm_moe_gather", "gemm_moe_combine",
+                    "gemm_moe_combine_backward"]
 
 
 class Opts(ctypes.Structure):
@@ -55,6 +62,13 @@ class MoeArgs(ctypes.Structure):   # gemm_moe_args
                 ("W2", vp), ("w2_e", i64), ("w2_n", i64), ("S2", vp), ("s2_e", i64), ("s2_n", i64),
                 ("Y", vp), ("ldy", i64), ("T", i64), ("E", i64), ("H", i64), ("I", i64), ("top_k", i32),
                 ("fmt", i32), ("fmt_logits", i32), ("mx4", i32), ("renormalize", i32)]
+
+
+class F8sArgs(ctypes.Structure):   # gemm_f8s_args
+    _fields_ = [("A", vp), ("lda", i64), ("SA", vp), ("lsa_m", i64), ("lsa_k", i64),
+                ("B", vp), ("ldb", i64), ("SB", vp), ("lsb_n", i64), ("lsb_k", i64),
+                ("C", vp), ("ldc", i64), ("M", i64), ("N", i64), ("K", i64),
+                ("fmt_a", i32), ("fmt_b", i32), ("b_block_rows", i32), ("fmt_c", i32)]
 
 
 def _load():
@@ -128,6 +142,32 @@ def _load():
     lib.gemm_moe.restype = ctypes.c_int
     lib.gemm_moe_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
     lib.gemm_moe_workspace_bytes.restype = sz
+    lib.gemm_f8s_quantize.argtypes = [vp, i32, i64, i64, i64, i64, i32, vp, i32, i64, vp, i64, i64, vp]
+    lib.gemm_f8s_quantize.restype = ctypes.c_int
+    lib.gemm_f8s.argtypes = [ctypes.POINTER(F8sArgs), vp, vp, sz]
+    lib.gemm_f8s.restype = ctypes.c_int
+    lib.gemm_f8s_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.gemm_f8s_workspace_bytes.restype = sz
+    f32 = ctypes.c_float
+    lib.gemm_rms_norm_f8.argtypes = [vp, i64, vp, i64, i32, vp, i32, f32, vp, i64, vp, i32, i64, vp, i64, i64,
+                                     i64, i64, vp]
+    lib.gemm_rms_norm_f8.restype = ctypes.c_int
+    lib.gemm_rms_norm_backward.argtypes = [vp, i64, vp, i64, i32, vp, i32, f32, vp, i64, vp, i64, vp, i64, i64,
+                                           vp, vp, sz]
+    lib.gemm_rms_norm_backward.restype = ctypes.c_int
+    lib.gemm_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.gemm_rms_norm_backward_workspace_bytes.restype = sz
+    lib.gemm_moe_sort.argtypes = [vp, i32, i64, i64, i32, i32, vp, vp, vp, vp, vp, sz]
+    lib.gemm_moe_sort.restype = ctypes.c_int
+    lib.gemm_moe_sort_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.gemm_moe_sort_workspace_bytes.restype = sz
+    lib.gemm_moe_gather.argtypes = [vp, i64, i32, vp, vp, i32, vp, i64, i64, i32, i64, vp]
+    lib.gemm_moe_gather.restype = ctypes.c_int
+    lib.gemm_moe_combine.argtypes = [vp, i64, i32, vp, vp, i32, i64, vp, i64, i64, i32, i64, vp]
+    lib.gemm_moe_combine.restype = ctypes.c_int
+    lib.gemm_moe_combine_backward.argtypes = [vp, i64, vp, i64, i32, vp, vp, i32, vp, i32, i64, vp, i64, vp, i64,
+                                              i64, i32, i64, vp]
+    lib.gemm_moe_combine_backward.restype = ctypes.c_int
     lib.gemm_f16_status_string.argtypes = [ctypes.c_int]
     lib.gemm_f16_status_string.restype = ctypes.c_char_p
     lib.gemm_f16_version.argtypes = []

@@ -1,0 +1,149 @@
+// Host side of include/gemm_f8_scaled.h: argument validation and launches of
+// the quantiser and of the products scaled by blocks.  Everything is checked
+// before the first HIP call, so on any error nothing is enqueued.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/gemm_f8_scaled.h"
+#include "f8s_convert.hpp"
+#include "f8s_tiles.hpp"
+#include "host_launch.hpp"
+
+using namespace gemmf16;
+
+namespace {
+
+int64_t elem_size(int32_t fmt) { return fmt == GEMM_FMT_F32 ? 4 : 2; }
+
+// K up to 2^36, as the other products.
+constexpr int64_t kMaxK = INT64_C(1) << 36;
+
+// How rows of octs octets are dealt to wave items; returns their number.
+int64_t wave_items(int64_t rows, int64_t octs, int64_t* segs, Short* few) {
+  *segs = cdiv(octs, kSlots);
+  *few = Short{};
+  if (*segs > 1 || rows == 1) return rows * *segs;
+  *few = Short{(int32_t)octs, (int32_t)(kSlots / octs), (int32_t)(65536 / octs + 1)};
+  return cdiv(rows, few->rows);
+}
+
+template <int FMT, int F8>
+const void* rows_fn(bool few) {
+  return few ? (const void*)f8_rows_kernel<FMT, F8, true> : (const void*)f8_rows_kernel<FMT, F8, false>;
+}
+template <int FMT, int F8>
+const void* tiles_fn(bool square, bool along_k) {
+  return !square ? (const void*)f8_tiles_kernel<FMT, F8, false, false>
+         : along_k ? (const void*)f8_tiles_kernel<FMT, F8, true, true>
+                   : (const void*)f8_tiles_kernel<FMT, F8, true, false>;
+}
+template <int F8>
+const void* quant_fn(int32_t fmt, bool tiles, bool square, bool along_k, bool few) {
+  if (tiles)
+    return fmt == GEMM_FMT_F16    ? tiles_fn<MX_F16, F8>(square, along_k)
+           : fmt == GEMM_FMT_BF16 ? tiles_fn<MX_BF16, F8>(square, along_k)
+                                  : tiles_fn<MX_F32, F8>(square, along_k);
+  return fmt == GEMM_FMT_F16 ? rows_fn<MX_F16, F8>(few) : fmt == GEMM_FMT_BF16 ? rows_fn<MX_BF16, F8>(few) : rows_fn<MX_F32, F8>(few);
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_f8s_quantize(const void* X, int32_t fmt, int64_t ldx_r, int64_t ldx_k, int64_t R, int64_t K,
+                      int32_t block_rows, void* data, int32_t fmt8, int64_t ldd, float* scales, int64_t lds_r,
+                      int64_t lds_k, void* stream) {
+  if (!X || !data || !scales) return GEMM_ERR_NULL;
+  if (R <= 0 || K <= 0 || K > kMaxK) return GEMM_ERR_SHAPE;
+  if (fmt < GEMM_FMT_F16 || fmt > GEMM_FMT_F32 || fmt8 < 0 || fmt8 > 1 || (block_rows != 1 && block_rows != 128))
+    return GEMM_ERR_OPTS;
+  if (ldx_r <= 0 || ldx_k <= 0 || lds_r <= 0 || lds_k <= 0) return GEMM_ERR_STRIDE;
+  if (ldd < K) return GEMM_ERR_LDC;
+  const int64_t kb = cdiv(K, kF8Block), sr = cdiv(R, block_rows);
+  Range rx, rd, rs;
+  if (!byte_view(X, R, K, ldx_r, ldx_k, elem_size(fmt), &rx) || !byte_rows(data, R, ldd, K, &rd) ||
+      !byte_view(scales, sr, kb, lds_r, lds_k, 4, &rs))
+    return GEMM_ERR_SHAPE;
+  if ((uintptr_t)scales & 3u) return GEMM_ERR_LAYOUT;
+  if (overlap(rx, rd) || overlap(rx, rs) || overlap(rd, rs)) return GEMM_ERR_ALIAS;
+
+  F8QuantArgs a{X, ldx_r, ldx_k, R, K, (uint8_t*)data, ldd, scales, lds_r, lds_k, 1, {}};
+  const bool tiles = block_rows == 128 || (ldx_k != 1 && K > 1);
+  int64_t grid;
+  if (tiles) {
+    a.segs = kb;
+    if (__builtin_mul_overflow(kb, cdiv(R, kF8Block), &grid)) return GEMM_ERR_SHAPE;
+  } else {
+    // Dense rows of whole blocks are one long row.
+    if (K % kF8Block == 0 && ldx_r == K && ldd == K && lds_k == 1 && lds_r == kb) {
+      a.R = 1;
+      a.K = R * K;
+    }
+    grid = cdiv(wave_items(a.R, 16 * cdiv(a.K, kF8Block), &a.segs, &a.few), 4);
+  }
+  if (grid > kMaxWide) return GEMM_ERR_SHAPE;
+  const bool along_k = ldx_k == 1 || K == 1;
+  const void* fn = fmt8 == 0 ? quant_fn<F8_E4M3>(fmt, tiles, block_rows == 128, along_k, a.few.rows > 0)
+                             : quant_fn<F8_E5M2>(fmt, tiles, block_rows == 128, along_k, a.few.rows > 0);
+  return run(fn, wide_grid(grid), 256, &a, (hipStream_t)stream);
+}
+
+size_t gemm_f8s_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return 0;
+}
+
+int gemm_f8s(const gemm_f8s_args* p, void* stream, void* workspace, size_t workspace_bytes) {
+  if (!p) return GEMM_ERR_NULL;
+  const gemm_f8s_args& q = *p;
+  const int64_t M = q.M, N = q.N, K = q.K;
+  if (!q.A || !q.SA || !q.B || !q.SB || !q.C) return GEMM_ERR_NULL;
+  if (M <= 0 || N <= 0 || K <= 0 || K > kMaxK) return GEMM_ERR_SHAPE;
+  if (q.fmt_a < 0 || q.fmt_a > 1 || q.fmt_b < 0 || q.fmt_b > 1 || (q.b_block_rows != 1 && q.b_block_rows != 128) ||
+      q.fmt_c < GEMM_FMT_F16 || q.fmt_c > GEMM_FMT_F32)
+    return GEMM_ERR_OPTS;
+  if (q.lda <= 0 || q.ldb <= 0 || q.lsa_m <= 0 || q.lsa_k <= 0 || q.lsb_n <= 0 || q.lsb_k <= 0) return GEMM_ERR_STRIDE;
+  if ((M > 1 && q.lda < K) || (N > 1 && q.ldb < K)) return GEMM_ERR_STRIDE;
+  if (q.ldc < N) return GEMM_ERR_LDC;
+  const int64_t kb = cdiv(K, kF8Block), nb = cdiv(N, q.b_block_rows);
+  Range ra, rsa, rb, rsb, rc;
+  if (!byte_rows(q.A, M, q.lda, K, &ra) || !byte_rows(q.B, N, q.ldb, K, &rb) ||
+      !byte_view(q.SA, M, kb, q.lsa_m, q.lsa_k, 4, &rsa) || !byte_view(q.SB, nb, kb, q.lsb_n, q.lsb_k, 4, &rsb) ||
+      !byte_view(q.C, M, N, q.ldc, 1, elem_size(q.fmt_c), &rc))
+    return GEMM_ERR_SHAPE;
+  if (((uintptr_t)q.A & 15u) || (M > 1 && q.lda % 16 != 0) || ((uintptr_t)q.B & 15u) || (N > 1 && q.ldb % 16 != 0) ||
+      ((uintptr_t)q.SA & 3u) || ((uintptr_t)q.SB & 3u) || ((uintptr_t)q.C % elem_size(q.fmt_c)))
+    return GEMM_ERR_LAYOUT;
+  if (overlap(rc, ra) || overlap(rc, rsa) || overlap(rc, rb) || overlap(rc, rsb)) return GEMM_ERR_ALIAS;
+  F8sArgs a{};
+  a.A = (const char*)q.A;
+  a.lda = M > 1 ? q.lda : 0;
+  a.SA = q.SA;
+  a.sa_m = q.lsa_m;
+  a.sa_k = q.lsa_k;
+  a.B = (const char*)q.B;
+  a.ldb = N > 1 ? q.ldb : 0;
+  a.SB = q.SB;
+  a.sb_n = q.lsb_n;
+  a.sb_k = q.lsb_k;
+  a.C = q.C;
+  a.ldc = q.ldc;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.out = q.fmt_c;
+  a.shift = q.b_block_rows == 128 ? 7 : 0;
+  a.panel = 8;
+  a.splits = 1;
+  a.GM = cdiv(M, 128);
+  a.GN = cdiv(N, 128);
+  int64_t grid;
+  if (__builtin_mul_overflow(a.GM, a.GN, &grid) || !fits_x(grid, 256)) return GEMM_ERR_SHAPE;
+  (void)workspace;
+  (void)workspace_bytes;
+  return run(f8s_tile_fn(F8S_TILE_128, q.fmt_a, q.fmt_b, a.shift == 0), dim3((unsigned)grid), 256, &a, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -7,7 +7,7 @@
 #include <cstdint>
 
 #include "../../include/gemm_mx4.h"
-#include "host_util.hpp"
+#include "host_launch.hpp"
 #include "mx4_convert.hpp"
 #include "mx4_tile_kernel.hpp"
 #include "strip_kernel.hpp"
@@ -17,38 +17,6 @@ using namespace gemmf16;
 namespace {
 
 int64_t elem_size(int32_t fmt) { return fmt == GEMM_FMT_F32 ? 4 : 2; }
-
-struct Range {
-  uintptr_t lo, hi;
-};
-
-// Byte range of rows x row_bytes bytes with row stride ld; false on overflow.
-bool byte_rows(const void* p, int64_t rows, int64_t ld, int64_t row_bytes, Range* r) {
-  int64_t a;
-  if (__builtin_mul_overflow(rows - 1, ld, &a) || __builtin_add_overflow(a, row_bytes, &a) ||
-      a > INT64_MAX / 2)
-    return false;
-  r->lo = (uintptr_t)p;
-  r->hi = r->lo + (uintptr_t)a;
-  return r->hi >= r->lo;
-}
-
-bool overlap(const Range& a, const Range& b) { return ranges_overlap(a.lo, a.hi, b.lo, b.hi); }
-
-// A launch takes fewer than 2^32 work items along x.
-bool fits_x(int64_t gx, int threads) { return gx < (INT64_C(1) << 32) / threads; }
-
-// n workgroups (of up to 512) as a grid that a launch takes (rounded up).
-dim3 wide_grid(int64_t n) {
-  constexpr int64_t kX = INT64_C(1) << 22;
-  return n <= kX ? dim3((unsigned)n) : dim3((unsigned)kX, (unsigned)cdiv(n, kX));
-}
-constexpr int64_t kMaxWide = INT64_C(65535) << 22;
-
-int run(const void* fn, dim3 grid, int threads, void* args, hipStream_t s) {
-  void* p[] = {args};
-  return hipLaunchKernel(fn, grid, dim3((unsigned)threads), p, 0, s) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
-}
 
 // Data and scale arrays of an MX4 matrix of `rows` rows.
 int check_mx4(const void* data, int64_t ldd, const void* scales, int64_t lds, int64_t rows, int64_t K,

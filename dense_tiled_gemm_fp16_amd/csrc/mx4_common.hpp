@@ -41,6 +41,16 @@ __device__ __forceinline__ void gstore(void* p, T v) {
 __device__ __forceinline__ u32x4 load16(const void* p) { return gload<u32x4>(p); }
 __device__ __forceinline__ void store16(void* p, u32x4 v) { gstore<u32x4>(p, v); }
 
+// n bytes (0 .. 16) at p, zeros behind them; nothing past them is read.
+__device__ __forceinline__ u32x4 load_bytes(const char* p, int64_t n) {
+  if (n >= 16) return load16(p);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 15; ++e)
+    if (e < n) w[e / 4] |= (uint32_t)gload<uint8_t>(p + e) << (8 * (e % 4));
+  return u32x4{w[0], w[1], w[2], w[3]};
+}
+
 // n (1, 2 or 4) dwords.
 template <int N>
 __device__ __forceinline__ void load_dwords(uint32_t (&d)[N], const void* p) {

@@ -1,0 +1,5 @@
+#include "f8s_tiles.hpp"
+
+namespace gemmf16 {
+GEMM_F8S_TILES(F8_E5M2, F8_E4M3)
+}  // namespace gemmf16

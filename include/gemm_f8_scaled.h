@@ -1,0 +1,73 @@
+/*
+ * gemm_f8_scaled.h -- 8-bit floating point (OCP E4M3 and E5M2) with a float32
+ * scale for each block of 128, on MI355X: quantisation and products.  Same
+ * library, return codes (enum gemm_status), stream and workspace rules as
+ * gemm_f16.h.
+ *
+ * A matrix [R, K] is R rows of K bytes (row stride in bytes) and its scales:
+ *     row blocks     one for each 128 consecutive elements of a row, [R, ceil(K/128)]
+ *     square blocks  one for each 128 rows x 128 elements, [ceil(R/128), ceil(K/128)]
+ * at any positive strides (in elements).  An element's value is its 8-bit value
+ * times its block's scale; the last block of a row or column may be shorter.
+ *
+ * Results are deterministic: sums run in a fixed order, without atomics.
+ */
+#ifndef GEMM_F8_SCALED_H
+#define GEMM_F8_SCALED_H
+
+#include "gemm_mx4.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * Quantise X[r,k] at X + r*ldx_r + k*ldx_k (elements of format fmt, enum
+ * gemm_mx4_format; positive strides) along k, into 8-bit elements of format
+ * fmt8 (0 E4M3, 1 E5M2) at data + r*ldd + k (ldd >= K) and scales at scales +
+ * (r / block_rows) * lds_r + (k / 128) * lds_k, block_rows 1 or 128.
+ *
+ * With m the block's largest magnitude and L the format's largest value (448,
+ * 57344), m' = max(m, L 2^-126), the scale is m' / L rounded to float32, and an
+ * element x becomes x L / m' rounded to nearest, ties to even (for a 16-bit x
+ * that quotient is rounded once; for a float32 x it is first rounded to float32).
+ * A block that holds an infinity or a NaN gets a NaN scale and zero elements.
+ * Nothing past a row's K bytes is written.
+ */
+int gemm_f8s_quantize(const void* X, int32_t fmt, int64_t ldx_r, int64_t ldx_k, int64_t R, int64_t K,
+                      int32_t block_rows, void* data, int32_t fmt8, int64_t ldd, float* scales, int64_t lds_r,
+                      int64_t lds_k, void* stream);
+
+/*
+ * C[m,n] := sum_k A[m,k] B[n,k] (values with their scales), float32 sums, C of
+ * format fmt_c (enum gemm_mx4_format), row-major with row stride ldc.
+ * A [M, K] of 8-bit format fmt_a in row blocks, scale of block b of row m at
+ * SA + m*lsa_m + b*lsa_k; B [N, K] of fmt_b in row blocks (b_block_rows 1) or
+ * square blocks (128), scale at SB + (n / b_block_rows)*lsb_n + b*lsb_k.
+ * lda, ldb: row strides in bytes; rows start 16-byte aligned (GEMM_ERR_LAYOUT).
+ * Needs gemm_f8s_workspace_bytes(M, N, K) bytes of workspace (may be 0), 256-byte
+ * aligned; with workspace == NULL they are allocated in stream order.
+ */
+typedef struct gemm_f8s_args {
+  const void* A;
+  int64_t lda;
+  const float* SA;
+  int64_t lsa_m, lsa_k;
+  const void* B;
+  int64_t ldb;
+  const float* SB;
+  int64_t lsb_n, lsb_k;
+  void* C;
+  int64_t ldc;
+  int64_t M, N, K;
+  int32_t fmt_a, fmt_b, b_block_rows, fmt_c;
+} gemm_f8s_args;
+
+int gemm_f8s(const gemm_f8s_args* args, void* stream, void* workspace, size_t workspace_bytes);
+size_t gemm_f8s_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* GEMM_F8_SCALED_H */
