@@ -39,7 +39,7 @@ import torch
 
 from ._lib import (GEMM_OK, LIB_PATH, PATHS, STATUS, VARIANTS, Opts, PlanInfo, lib, make_opts,
                    status_string)
-from .f8_scaled import gemm_f8_scaled, gemm_f8_scaled_workspace_bytes, quantize_f8
+from .f8_scaled import gemm_f8_scaled, quantize_f8
 from .moe import gemm_moe, gemm_moe_workspace_bytes
 from .moe_rows import MoeOrder, moe_combine, moe_combine_backward, moe_gather, moe_sort, moe_sort_workspace_bytes
 from .mx4 import (MX4, _check_stream, _keep, _new, dequantize_mx4, gemm_mx4, gemm_mx4_workspace_bytes,
@@ -50,7 +50,7 @@ __all__ = ["gemm", "gemm_raw", "gemm_noalloc", "gemm_grouped", "pack_b", "gemm_p
            "workspace_bytes", "GemmError", "LIB_PATH",
            "VARIANTS", "MX4", "quantize_mx4", "dequantize_mx4", "gemm_mx4", "gemm_mx4_workspace_bytes",
            "gemm_moe", "gemm_moe_workspace_bytes", "quantize_f8", "gemm_f8_scaled",
-           "gemm_f8_scaled_workspace_bytes", "rms_norm_f8", "rms_norm_backward", "rms_norm_backward_workspace_bytes",
+           "rms_norm_f8", "rms_norm_backward", "rms_norm_backward_workspace_bytes",
            "MoeOrder", "moe_sort", "moe_sort_workspace_bytes", "moe_gather", "moe_combine", "moe_combine_backward"]
 
 

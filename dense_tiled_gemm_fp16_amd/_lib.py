@@ -34,7 +34,7 @@ EXPORTS_MX4 = ["gemm_mx4_quantize", "gemm_mx4_dequantize", "gemm_mx4", "gemm_mx4
 # Entry points of include/gemm_moe.h.
 EXPORTS_MOE = ["gemm_moe", "gemm_moe_workspace_bytes"]
 # Entry points of include/gemm_f8_scaled.h.
-EXPORTS_F8S = ["gemm_f8s_quantize", "gemm_f8s", "gemm_f8s_workspace_bytes"]
+EXPORTS_F8S = ["gemm_f8s_quantize", "gemm_f8s"]
 # Entry points of include/rms_norm_f8.h.
 EXPORTS_NORM = ["gemm_rms_norm_f8", "gemm_rms_norm_backward", "gemm_rms_norm_backward_workspace_bytes"]
 # Entry points of include/gemm_moe_rows.h.
@@ -68,7 +68,7 @@ class F8sArgs(ctypes.Structure):   # gemm_f8s_args
     _fields_ = [("A", vp), ("lda", i64), ("SA", vp), ("lsa_m", i64), ("lsa_k", i64),
                 ("B", vp), ("ldb", i64), ("SB", vp), ("lsb_n", i64), ("lsb_k", i64),
                 ("C", vp), ("ldc", i64), ("M", i64), ("N", i64), ("K", i64),
-                ("fmt_a", i32), ("fmt_b", i32), ("b_block_rows", i32), ("fmt_c", i32)]
+                ("fmt_a", i32), ("fmt_b", i32), ("b_block_rows", i32), ("fmt_c", i32), ("variant", i32)]
 
 
 def _load():
@@ -144,10 +144,8 @@ def _load():
     lib.gemm_moe_workspace_bytes.restype = sz
     lib.gemm_f8s_quantize.argtypes = [vp, i32, i64, i64, i64, i64, i32, vp, i32, i64, vp, i64, i64, vp]
     lib.gemm_f8s_quantize.restype = ctypes.c_int
-    lib.gemm_f8s.argtypes = [ctypes.POINTER(F8sArgs), vp, vp, sz]
+    lib.gemm_f8s.argtypes = [ctypes.POINTER(F8sArgs), vp]
     lib.gemm_f8s.restype = ctypes.c_int
-    lib.gemm_f8s_workspace_bytes.argtypes = [i64, i64, i64]
-    lib.gemm_f8s_workspace_bytes.restype = sz
     f32 = ctypes.c_float
     lib.gemm_rms_norm_f8.argtypes = [vp, i64, vp, i64, i32, vp, i32, f32, vp, i64, vp, i32, i64, vp, i64, i64,
                                      i64, i64, vp]

@@ -10,12 +10,12 @@
 // beside it as long as the result is not awaited: a group of four instructions
 // is issued before the first result is used.
 //
-//   LDS    S stages of 128 k: BM rows of A and BN rows of B, 128 bytes each,
-//          16-byte chunk c of row r in slot c ^ f8(r), and a dword of scale for
-//          each row.  All comes by LDS-DMA (8 whole lines an instruction; the
-//          scales as one dword a lane, so that any strides will do): step t + S
-//          - 1 is issued into the stage of step t - 1 behind the one barrier of
-//          step t.
+//   LDS    S stages of 128 k: BM rows of A and BN rows of B, 128 bytes each, the
+//          16-byte chunks of a row permuted against bank conflicts, and a dword
+//          of scale for each row.  All comes by LDS-DMA (8 whole lines an
+//          instruction; the scales as one dword a lane, so that any strides will
+//          do).  Step t + S - 1 is issued into the stage of step t - 1 behind the
+//          one barrier of step t.
 //   k      a lane of group g = lane / 16 takes chunks g and g + 4 of its row,
 //          for A and B alike: any assignment of k to bytes that both share is
 //          the product.
@@ -23,8 +23,15 @@
 //          row lane % 16 of C, so one multiplication gives the scale of a row
 //          and a block of columns, and 8 or 16 consecutive bytes are stored.
 //
-// K past the last whole block is filled through registers with zeros on both
-// sides; rows past M or N read the last valid row and are never stored.
+// A partial block at the end is a step like the others, its bytes behind K
+// cleared in the registers on both sides; rows past M or N read the last valid
+// row and are never stored.
+//
+// float32 results (WIDE): the FP8 matrix instructions add products in groups of
+// 8, aligned to the group's largest and cut 2^-13 below it (measured; the older
+// and the newer ones alike), which leaves sums of 1 to 3 in 10^5 of their
+// size: far below a 16-bit result's last place, but not a float32 one's.  Those go
+// through binary16, which holds every 8-bit value, at half the rate.
 #pragma once
 
 #include "f8_kernel.hpp"
@@ -48,9 +55,6 @@ struct F8sArgs {
   int64_t M, N, K;
   int64_t GM, GN;
   int32_t panel, out, shift;
-  int32_t splits;           // parts of K; > 1: float32 sums to W[part][M][N]
-  int64_t part_steps;       // steps of a part
-  float* W;
 };
 
 template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
@@ -65,7 +69,9 @@ struct F8sCfg {
   static constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES, LDS = STAGES * STAGE;
   static constexpr int DMA_A = A_BYTES / 1024, DMA_B = B_BYTES / 1024;   // instructions of the workgroup
   static constexpr int DI = (DMA_A + DMA_B) / NW;                        // per wave
+  static constexpr int BATCH = DI % 4 == 0 ? 4 : 2, BATCHES = DI / BATCH;
   static constexpr int PER_STEP = DI + SI;
+  static_assert(DI % 2 == 0 && DMA_A % BATCH == 0, "batches of one operand");
   static_assert((DMA_A + DMA_B) % NW == 0 && TM % 16 == 0 && TN % 16 == 0 && 128 % TN == 0, "shape");
   static_assert(LDS <= 160 * 1024, "LDS budget");
 };
@@ -84,16 +90,55 @@ __device__ __forceinline__ void dma16_any(const void* p, uint32_t lds) {
                : "memory", "m0");
 }
 
+// An operand's 32 bytes of a lane: as they are, or widened to binary16.
+template <bool WIDE>
+struct F8sFrag {
+  i32x8 v;
+};
+template <>
+struct F8sFrag<true> {
+  f16x8 v[4];
+};
+// Two 8-bit elements of w (its low or high half) as binary16, exactly.
+template <int F, bool HI>
+__device__ __forceinline__ uint32_t widen2(uint32_t w) {
+  if constexpr (F == F8_E4M3)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
+  else   // binary16's upper byte
+    return __builtin_amdgcn_perm(w, 0u, HI ? 0x07000600u : 0x05000400u);
+}
+template <bool WIDE, int F>
+__device__ __forceinline__ F8sFrag<WIDE> f8s_frag(const i32x8& b) {
+  F8sFrag<WIDE> f;
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = (uint32_t)b[2 * i], hi = (uint32_t)b[2 * i + 1];
+      f.v[i] = __builtin_bit_cast(f16x8, u32x4{widen2<F, false>(lo), widen2<F, true>(lo), widen2<F, false>(hi),
+                                               widen2<F, true>(hi)});
+    }
+  } else {
+    f.v = b;
+  }
+  return f;
+}
+
+// Sum over a block's 128 k, from zero; first operand the B block.
+template <int FA, int FB>
+__device__ __forceinline__ f32x4 f8s_block(const F8sFrag<true>& b, const F8sFrag<true>& a) {
+  f32x4 d{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[i], a.v[i], d, 0, 0, 0);
+  return d;
+}
 template <int FA, int FB>
 __device__ __forceinline__ f32x4 mfma_f8_block(const i32x8& b, const i32x8& a) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, FB, FA, 0, 0, 0, 0);
 }
 
-// Chunks g and g + 4 of row r of an operand's stage.
-__device__ __forceinline__ i32x8 read_f8_row(const char* st, int r, int g) {
-  const char* row = st + r * 128;
-  return join8(*reinterpret_cast<const u32x4*>(row + ((g ^ f8(r)) * 16)),
-               *reinterpret_cast<const u32x4*>(row + (((g + 4) ^ f8(r)) * 16)));
+template <int FA, int FB>
+__device__ __forceinline__ f32x4 f8s_block(const F8sFrag<false>& b, const F8sFrag<false>& a) {
+  return mfma_f8_block<FA, FB>(b.v, a.v);
 }
 
 // 4 consecutive outputs of a row, the first nv of them.
@@ -124,7 +169,27 @@ __device__ __forceinline__ void store_out4(void* C, int out, int64_t at, f32x4 v
     store4_part(p, h, (int)nv);
 }
 
-template <class CF, int FA, int FB, bool ROWB>
+// Bytes of a lane's 32 that lie behind rem, zeroed (those at k >= rem of the block:
+// chunk g is k 16 g .., chunk g + 4 k 64 + 16 g ..).
+__device__ __forceinline__ i32x8 mask_block(i32x8 v, int g, int rem) {
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const int n = rem - (16 * g + 4 * (w & 3) + (w < 4 ? 0 : 64));
+    v[w] = n >= 4 ? v[w] : (n <= 0 ? 0 : (v[w] & ((1 << (8 * n)) - 1)));
+  }
+  return v;
+}
+
+// Offset of a DMA lane's chunk c in a block of which rem bytes are left: chunks
+// wholly behind K read the block's first one (mask_block clears them; a chunk
+// that K ends in is read whole, 16 aligned bytes of which one at least is K's).
+__device__ __forceinline__ int tail_chunk(int c, int rem) { return 16 * c < rem ? 16 * c : 0; }
+
+// 16-byte chunk c of row r lies in slot c ^ f16r(r): the same for every block of
+// 16 rows, 16 rows reading one chunk fall on distinct banks.
+__device__ __forceinline__ int f16r(int r) { return (r ^ (r >> 3 & 1)) & 7; }
+
+template <class CF, int FA, int FB, bool ROWB, bool WIDE>
 __global__ __launch_bounds__(CF::NT) void f8s_tile_kernel(F8sArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[CF::LDS];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -132,43 +197,76 @@ __global__ __launch_bounds__(CF::NT) void f8s_tile_kernel(F8sArgs a) {
   const int wm = wave / CF::WN, wn = wave % CF::WN;
   const int lr = lane & 15, g = lane >> 4;
 
-  int64_t pm, pn, w = blockIdx.x;
-  int64_t part = 0;
-  if (a.splits > 1) {
-    part = w / (a.GM * a.GN);
-    w -= part * (a.GM * a.GN);
-  }
-  raster_tile(w, a.GM, a.GN, a.panel, pm, pn);
+  int64_t pm, pn;
+  raster_tile(blockIdx.x, a.GM, a.GN, a.panel, pm, pn);
   const int64_t m0 = pm * CF::BM, n0 = pn * CF::BN;
-  const int64_t k0 = part * a.part_steps * 128;
-  const int64_t ke = a.splits > 1 && k0 + a.part_steps * 128 < a.K ? k0 + a.part_steps * 128 : a.K;
+  const int nf = (int)(a.K / 128);                // whole blocks
+  const int rem = (int)(a.K - (int64_t)nf * 128);
+  const int nb = nf + (rem > 0);
 
-  // This wave's DMA instructions of a step: DI of 8 rows, A's first, then SI of
-  // 64 scales, A's first (the last may be one too many: it repeats B's rows).
-  const char* src[CF::DI];
+  // This wave's DMA instructions of a step: DI of 8 rows, A's first, in batches of
+  // one operand, then SI of 64 scales, A's first (the last may be one too many: it
+  // repeats B's rows).  Uniform bases, and 32-bit offsets of the lanes.
+  const char* src[CF::BATCHES];
+  uint32_t off[CF::DI];
   const char* ssrc[CF::SI];
+  uint32_t soff[CF::SI];
   int64_t sstep[CF::SI];
+  auto chunk = [&](int i) { return (lane % 8) ^ f16r((wave * CF::DI + i) * 8 + lane / 8); };
 #pragma unroll
   for (int i = 0; i < CF::DI; ++i) {
     const int q = wave * CF::DI + i;
     const bool is_a = q < CF::DMA_A;
-    const int r = (is_a ? q : q - CF::DMA_A) * 8 + lane / 8, c = (lane % 8) ^ f8(r);
-    int64_t row = (is_a ? m0 : n0) + r;
-    const int64_t last = (is_a ? a.M : a.N) - 1;
-    if (row > last) row = last;
-    src[i] = (is_a ? a.A + row * a.lda : a.B + row * a.ldb) + k0 + 16 * c;
+    const int64_t r = (is_a ? q : q - CF::DMA_A) * 8 + lane / 8, left = (is_a ? a.M - m0 : a.N - n0) - 1;
+    if (i % CF::BATCH == 0) src[i / CF::BATCH] = uniform_ptr((is_a ? a.A + m0 * a.lda : a.B + n0 * a.ldb) - kSBias);
+    off[i] = (uint32_t)((r < left ? r : left) * (is_a ? a.lda : a.ldb) + (nf > 0 ? 16 * chunk(i) : tail_chunk(chunk(i), rem)) +
+                        kSBias - 1024 * (i % CF::BATCH));
   }
 #pragma unroll
   for (int i = 0; i < CF::SI; ++i) {
     const int q = wave * CF::SI + i;
     const bool is_a = q < (CF::BM + 63) / 64;
-    int64_t row = (is_a ? m0 + q * 64 : n0 + (q - (CF::BM + 63) / 64) * 64) + lane;
-    const int64_t last = (is_a ? a.M : a.N) - 1;
-    if (row > last) row = last;
-    const int64_t b0 = k0 / 128;
-    ssrc[i] = (const char*)(is_a ? a.SA + row * a.sa_m + b0 * a.sa_k : a.SB + (row >> a.shift) * a.sb_n + b0 * a.sb_k);
+    const int64_t last = (is_a ? a.M : a.N) - 1, row = is_a ? m0 + q * 64 : n0 + (q - (CF::BM + 63) / 64) * 64;
+    const int64_t r0 = row < last ? row : last, r1 = row + lane < last ? row + lane : last;
+    ssrc[i] = uniform_ptr((const char*)(is_a ? a.SA + r0 * a.sa_m : a.SB + (r0 >> a.shift) * a.sb_n));
+    soff[i] = (uint32_t)(4 * (is_a ? (r1 - r0) * a.sa_m : ((r1 >> a.shift) - (r0 >> a.shift)) * a.sb_n));
     sstep[i] = 4 * (is_a ? a.sa_k : a.sb_k);
   }
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+  // Step t into `slot`, from bases that advance with each call but the last
+  // block's (which is loaded again past the end, so that every step issues the
+  // same number); ahead of a partial block the lanes' chunks are set for it.
+  int at = 0;
+  auto issue = [&](int slot) {
+    const uint32_t st = lds0 + slot * CF::STAGE;
+#pragma unroll
+    for (int i = 0; i < CF::BATCHES; ++i)
+      dma16s_batch<CF::BATCH>(&off[i * CF::BATCH], src[i], st + (wave * CF::DI + i * CF::BATCH) * 1024);
+#pragma unroll
+    for (int i = 0; i < CF::SI; ++i)
+      dma4s(soff[i], ssrc[i], st + CF::A_BYTES + CF::B_BYTES + (wave * CF::SI + i) * 256);
+    if (++at < nb) {
+#pragma unroll
+      for (int i = 0; i < CF::BATCHES; ++i) src[i] += 128;
+#pragma unroll
+      for (int i = 0; i < CF::SI; ++i) ssrc[i] += sstep[i];
+      if (rem > 0 && at == nf) {
+#pragma unroll
+        for (int i = 0; i < CF::DI; ++i) off[i] += tail_chunk(chunk(i), rem) - 16 * chunk(i);
+      }
+    }
+  };
+
+  // LDS addresses of stage 0: chunks g and g + 4 of row lr of a block of rows.
+  const int c0 = (g ^ f16r(lr)) * 16, c1 = c0 ^ 64;
+  const char* const la = smem + (wm * CF::TM + lr) * 128;
+  const char* const lb = smem + CF::A_BYTES + (wn * CF::TN + lr) * 128;
+  const char* const lsa = smem + CF::A_BYTES + CF::B_BYTES + (wm * CF::TM + lr) * 4;
+  const char* const lsb = smem + CF::A_BYTES + CF::B_BYTES + CF::SB_AT + wn * CF::TN * 4;
+  auto read = [&](const char* rows, int i) {
+    const char* p = rows + i * 2048;
+    return join8(*reinterpret_cast<const u32x4*>(p + c0), *reinterpret_cast<const u32x4*>(p + c1));
+  };
 
   f32x4 acc[CF::FN][CF::FM];
 #pragma unroll
@@ -176,96 +274,74 @@ __global__ __launch_bounds__(CF::NT) void f8s_tile_kernel(F8sArgs a) {
 #pragma unroll
     for (int j = 0; j < CF::FM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
-  auto issue = [&](int64_t t, int slot) {
-    const uint32_t st = lds0 + slot * CF::STAGE;
-#pragma unroll
-    for (int i = 0; i < CF::DI; ++i) dma16_any(src[i] + t * 128, st + (wave * CF::DI + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < CF::SI; ++i)
-      dma4_any(ssrc[i] + t * sstep[i], st + CF::A_BYTES + CF::B_BYTES + (wave * CF::SI + i) * 256);
-  };
-  auto compute = [&](int slot) {
-    const char* st = smem + slot * CF::STAGE;
-    const char* sc = st + CF::A_BYTES + CF::B_BYTES;
-    i32x8 fm[CF::FM];
+  // One block of K: unit u multiplies block i = u / FM of B by block j = u % FM of
+  // A, then the sums of the unit LAG before are taken to their scales.  A block
+  // of B is read while the one before it is multiplied.
+  constexpr int UNITS = CF::FN * CF::FM, LAG = UNITS > 3 ? 3 : UNITS - 1;
+  auto compute = [&](auto tail_tag, int slot) {
+    constexpr bool TAIL = decltype(tail_tag)::value;
+    const char* const ra = la + slot * CF::STAGE;
+    const char* const rb = lb + slot * CF::STAGE;
+    const char* const rsa = lsa + slot * CF::STAGE;
+    const char* const rsb = lsb + slot * CF::STAGE;
+    auto part = [&](const i32x8& v) { return TAIL ? mask_block(v, g, rem) : v; };
+    i32x8 next = part(read(rb, 0));
+    F8sFrag<WIDE> fm[CF::FM], fb;
     float s[CF::FM];
-    const float sb = ROWB ? 1.0f : *(const float*)(sc + CF::SB_AT + wn * CF::TN * 4);
+    const float sb = ROWB ? 1.0f : *reinterpret_cast<const float*>(rsb);
 #pragma unroll
     for (int j = 0; j < CF::FM; ++j) {
-      fm[j] = read_f8_row(st, wm * CF::TM + j * 16 + lr, g);
-      s[j] = *(const float*)(sc + (wm * CF::TM + j * 16 + lr) * 4) * sb;
+      fm[j] = f8s_frag<WIDE, FA>(part(read(ra, j)));
+      s[j] = *reinterpret_cast<const float*>(rsa + j * 64) * sb;
     }
+    f32x4 d[LAG + 1], sn[2];
+    if constexpr (ROWB) sn[0] = *reinterpret_cast<const f32x4*>(rsb + 16 * g);
 #pragma unroll
-    for (int i = 0; i < CF::FN; ++i) {
-      const i32x8 fb = read_f8_row(st + CF::A_BYTES, wn * CF::TN + i * 16 + lr, g);
-      f32x4 sn{1.0f, 1.0f, 1.0f, 1.0f};
-      if constexpr (ROWB) sn = *(const f32x4*)(sc + CF::SB_AT + (wn * CF::TN + i * 16 + 4 * g) * 4);
-      f32x4 d[CF::FM];
-#pragma unroll
-      for (int j = 0; j < CF::FM; ++j) d[j] = mfma_f8_block<FA, FB>(fb, fm[j]);
-#pragma unroll
-      for (int j = 0; j < CF::FM; ++j)
+    for (int u = 0; u < UNITS + LAG; ++u) {
+      if (u < UNITS) {
+        const int i = u / CF::FM, j = u % CF::FM;
+        if (j == 0) {
+          fb = f8s_frag<WIDE, FB>(next);
+          if (i + 1 < CF::FN) next = part(read(rb, i + 1));
+        }
+        d[u % (LAG + 1)] = f8s_block<FA, FB>(fb, fm[j]);
+      }
+      if (u >= LAG) {
+        const int v = u - LAG, i = v / CF::FM, j = v % CF::FM;
+        if constexpr (ROWB)
+          if (j == 0 && i + 1 < CF::FN) sn[(i + 1) & 1] = *reinterpret_cast<const f32x4*>(rsb + (i + 1) * 64 + 16 * g);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          acc[i][j][e] = __builtin_fmaf(ROWB ? d[j][e] * sn[e] : d[j][e], s[j], acc[i][j][e]);
+          acc[i][j][e] = __builtin_fmaf(ROWB ? d[v % (LAG + 1)][e] * sn[i & 1][e] : d[v % (LAG + 1)][e], s[j], acc[i][j][e]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  const int64_t nf = (ke - k0) / 128;
-  const int rem = (int)((ke - k0) - nf * 128);
-  auto at = [&](int64_t t) { return t < nf ? t : nf - 1; };
-  if (nf > 0) {
 #pragma unroll
-    for (int t = 0; t < CF::STAGES - 1; ++t) issue(at(t), t);
-    int slot = 0;
-    for (int64_t t = 0; t < nf; ++t) {
-      wait_vmcnt<(CF::STAGES - 2) * CF::PER_STEP>();    // this wave's part of step t landed,
-      wait_lgkmcnt0();                                  // and its reads of step t - 1 returned
-      wg_barrier();                                     // both of every wave's
-      issue(at(t + CF::STAGES - 1), slot == 0 ? CF::STAGES - 1 : slot - 1);
-      compute(slot);
-      slot = slot == CF::STAGES - 1 ? 0 : slot + 1;
-    }
-    wait_vmcnt<0>();
+  for (int t = 0; t < CF::STAGES - 1; ++t) issue(t);
+  int slot = 0;
+  for (int t = 0; t < nb; ++t) {
+    wait_vmcnt<(CF::STAGES - 2) * CF::PER_STEP>();    // this wave's part of step t landed,
+    wait_lgkmcnt0();                                  // and its reads of step t - 1 returned
+    wg_barrier();                                     // both of every wave's
+    issue(slot == 0 ? CF::STAGES - 1 : slot - 1);
+    __builtin_amdgcn_sched_barrier(0);
+    if (rem > 0 && t == nf)
+      compute(std::true_type{}, slot);
+    else
+      compute(std::false_type{}, slot);
+    slot = slot == CF::STAGES - 1 ? 0 : slot + 1;
   }
-  wait_lgkmcnt0();
-  wg_barrier();
-  if (rem > 0) {
-    // The last, partial block, into stage 0 (free after the barrier).
-    for (int cell = tid; cell < (CF::BM + CF::BN) * 8; cell += CF::NT) {
-      const bool is_a = cell < CF::BM * 8;
-      const int r = (is_a ? cell : cell - CF::BM * 8) / 8, c = cell % 8;
-      int64_t row = (is_a ? m0 : n0) + r;
-      const int64_t last = (is_a ? a.M : a.N) - 1;
-      if (row > last) row = last;
-      const char* p = (is_a ? a.A + row * a.lda : a.B + row * a.ldb) + k0 + nf * 128 + 16 * c;
-      *reinterpret_cast<u32x4*>(smem + (is_a ? 0 : CF::A_BYTES) + r * 128 + ((c ^ f8(r)) * 16)) =
-          load_bytes(p, rem - 16 * c);
-    }
-    for (int r = tid; r < CF::BM + CF::BN; r += CF::NT) {
-      const bool is_a = r < CF::BM;
-      int64_t row = is_a ? m0 + r : n0 + r - CF::BM;
-      const int64_t last = (is_a ? a.M : a.N) - 1;
-      if (row > last) row = last;
-      const int64_t b = k0 / 128 + nf;
-      const float v = is_a ? a.SA[row * a.sa_m + b * a.sa_k] : a.SB[(row >> a.shift) * a.sb_n + b * a.sb_k];
-      *reinterpret_cast<float*>(smem + CF::A_BYTES + CF::B_BYTES + (is_a ? 4 * r : CF::SB_AT + 4 * (r - CF::BM))) = v;
-    }
-    __syncthreads();
-    compute(0);
-  }
+  wait_vmcnt<0>();       // no LDS transfer may outlive the workgroup
 
-  void* const C = a.splits > 1 ? (void*)(a.W + part * a.M * a.N) : a.C;
-  const int out = a.splits > 1 ? (int)F8S_F32 : a.out;
-  const int64_t ldc = a.splits > 1 ? a.N : a.ldc;
 #pragma unroll
   for (int j = 0; j < CF::FM; ++j) {
     const int64_t m = m0 + wm * CF::TM + j * 16 + lr;
 #pragma unroll
     for (int i = 0; i < CF::FN; ++i) {
       const int64_t n = n0 + wn * CF::TN + i * 16 + 4 * g;
-      if (m < a.M && n < a.N) store_out4(C, out, m * ldc + n, acc[i][j], a.N - n);
+      if (m < a.M && n < a.N) store_out4(a.C, a.out, m * a.ldc + n, acc[i][j], a.N - n);
     }
   }
 }

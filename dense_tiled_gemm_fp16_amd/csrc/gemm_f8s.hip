@@ -48,6 +48,62 @@ const void* quant_fn(int32_t fmt, bool tiles, bool square, bool along_k, bool fe
   return fmt == GEMM_FMT_F16 ? rows_fn<MX_F16, F8>(few) : fmt == GEMM_FMT_BF16 ? rows_fn<MX_BF16, F8>(few) : rows_fn<MX_F32, F8>(few);
 }
 
+const void* product_fn(int32_t fmt_a, int32_t fmt_b, int variant, bool rowb, bool wide, int out) {
+  if (fmt_a == 0)
+    return fmt_b == 0 ? f8s_fn<F8_E4M3, F8_E4M3>(variant, rowb, wide, out)
+                      : f8s_fn<F8_E4M3, F8_E5M2>(variant, rowb, wide, out);
+  return fmt_b == 0 ? f8s_fn<F8_E5M2, F8_E4M3>(variant, rowb, wide, out)
+                    : f8s_fn<F8_E5M2, F8_E5M2>(variant, rowb, wide, out);
+}
+
+// Lanes reach a workgroup's rows by 32-bit offsets of bytes, scales too.
+constexpr int64_t kMaxPitch = INT64_C(1) << 23, kMaxScalePitch = INT64_C(1) << 21;
+
+// Whether a variant takes the call.
+bool takes(const F8sArgs& a, int variant, bool wide) {
+  if (variant == GEMM_F8S_TILE_256X256 && (a.shift == 0 || wide)) return false;
+  const F8sShape& s = kF8sShapes[variant];
+  const int64_t gm = cdiv(a.M, s.rows), gn = cdiv(a.N, s.cols);
+  if (s.parts > 1) return gm <= 65535 && fits_x(gn, s.threads);
+  int64_t grid;
+  return !__builtin_mul_overflow(gm, gn, &grid) && fits_x(grid, s.threads);
+}
+
+// The variant that takes least by the times of f8s_tiles.hpp; 0 if none takes the
+// call.  Measured in graphs (us; M x N x K, square blocks, bfloat16; strips of
+// rows x columns, whose 8 waves share K, then tiles):
+//   1 x 2048 x 7168      16x16 5.6, 16x32 5.7
+//   32 x 7168 x 2048     16x32 6.4, 32x16 6.6, 32x32 4.6, 64x32 5.2
+//   64 x 7168 x 2048     32x32 8.1, 64x32 5.5, 64x64 6.9, tile 64x128 12.9
+//   128 x 2048 x 7168    16x32 12.4, 32x32 8.4, 64x32 10.2, 64x64 12.8
+//   512 x 2048 x 7168    64x32 23, 64x64 17, tiles 64x128 36, 128x128 47
+//   1024 x 2048 x 2048   64x64 12.4, tiles 64x128 13.3, 128x128 16.2
+//   2048 x 2048 x 7168   64x64 60, tiles 64x128 50, 128x128 49, 256x128 75
+//   2048 x 4096 x 4096   tiles 64x128 58, 128x128 58, 256x128 49, 256x256 47
+//   8192 x 2048 x 7168   189, 188, 158, 101
+//   32768 x 2048 x 7168  785, 777, 639, 414
+// Row blocks and float32, 2048 x 7168 x 8192: strips 64x64 436, tiles 64x128 331,
+// 128x128 347, 256x128 280; to bfloat16: 273, 246, 250, 187.  Over 60 random
+// sizes the choice took 3% longer than the best one in the mean, 26% at most.
+int plan(const F8sArgs& a, bool wide, int cus) {
+  int best = 0;
+  float least = 0.0f;
+  for (int v = 1; v < kF8sVariants; ++v) {
+    if (!takes(a, v, wide)) continue;
+    const F8sShape& s = kF8sShapes[v];
+    const double wgs = (double)cdiv(a.M, s.rows) * (double)cdiv(a.N, s.cols);
+    const double slots = (double)cus * s.per_cu;
+    const float rounds = (float)(int64_t)((wgs + slots - 1) / slots);
+    const float step = (wgs > slots / 2 ? s.step_full : s.step) * (wide ? s.wide : 1.0f);
+    const float t = rounds * (s.start + step * (float)cdiv(cdiv(a.K, kF8Block), s.parts));
+    if (best == 0 || t < least) {
+      best = v;
+      least = t;
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 extern "C" {
@@ -90,19 +146,14 @@ int gemm_f8s_quantize(const void* X, int32_t fmt, int64_t ldx_r, int64_t ldx_k, 
   return run(fn, wide_grid(grid), 256, &a, (hipStream_t)stream);
 }
 
-size_t gemm_f8s_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (M <= 0 || N <= 0 || K <= 0) return 0;
-  return 0;
-}
-
-int gemm_f8s(const gemm_f8s_args* p, void* stream, void* workspace, size_t workspace_bytes) {
+int gemm_f8s(const gemm_f8s_args* p, void* stream) {
   if (!p) return GEMM_ERR_NULL;
   const gemm_f8s_args& q = *p;
   const int64_t M = q.M, N = q.N, K = q.K;
   if (!q.A || !q.SA || !q.B || !q.SB || !q.C) return GEMM_ERR_NULL;
   if (M <= 0 || N <= 0 || K <= 0 || K > kMaxK) return GEMM_ERR_SHAPE;
   if (q.fmt_a < 0 || q.fmt_a > 1 || q.fmt_b < 0 || q.fmt_b > 1 || (q.b_block_rows != 1 && q.b_block_rows != 128) ||
-      q.fmt_c < GEMM_FMT_F16 || q.fmt_c > GEMM_FMT_F32)
+      q.fmt_c < GEMM_FMT_F16 || q.fmt_c > GEMM_FMT_F32 || q.variant < 0 || q.variant >= kF8sVariants)
     return GEMM_ERR_OPTS;
   if (q.lda <= 0 || q.ldb <= 0 || q.lsa_m <= 0 || q.lsa_k <= 0 || q.lsb_n <= 0 || q.lsb_k <= 0) return GEMM_ERR_STRIDE;
   if ((M > 1 && q.lda < K) || (N > 1 && q.ldb < K)) return GEMM_ERR_STRIDE;
@@ -114,6 +165,7 @@ int gemm_f8s(const gemm_f8s_args* p, void* stream, void* workspace, size_t works
       !byte_view(q.C, M, N, q.ldc, 1, elem_size(q.fmt_c), &rc))
     return GEMM_ERR_SHAPE;
   if (((uintptr_t)q.A & 15u) || (M > 1 && q.lda % 16 != 0) || ((uintptr_t)q.B & 15u) || (N > 1 && q.ldb % 16 != 0) ||
+      (M > 1 && (q.lda > kMaxPitch || q.lsa_m > kMaxScalePitch)) || (N > 1 && q.ldb > kMaxPitch) || (nb > 1 && q.lsb_n > kMaxScalePitch) ||
       ((uintptr_t)q.SA & 3u) || ((uintptr_t)q.SB & 3u) || ((uintptr_t)q.C % elem_size(q.fmt_c)))
     return GEMM_ERR_LAYOUT;
   if (overlap(rc, ra) || overlap(rc, rsa) || overlap(rc, rb) || overlap(rc, rsb)) return GEMM_ERR_ALIAS;
@@ -121,12 +173,12 @@ int gemm_f8s(const gemm_f8s_args* p, void* stream, void* workspace, size_t works
   a.A = (const char*)q.A;
   a.lda = M > 1 ? q.lda : 0;
   a.SA = q.SA;
-  a.sa_m = q.lsa_m;
+  a.sa_m = M > 1 ? q.lsa_m : 0;
   a.sa_k = q.lsa_k;
   a.B = (const char*)q.B;
   a.ldb = N > 1 ? q.ldb : 0;
   a.SB = q.SB;
-  a.sb_n = q.lsb_n;
+  a.sb_n = nb > 1 ? q.lsb_n : 0;
   a.sb_k = q.lsb_k;
   a.C = q.C;
   a.ldc = q.ldc;
@@ -135,15 +187,23 @@ int gemm_f8s(const gemm_f8s_args* p, void* stream, void* workspace, size_t works
   a.K = K;
   a.out = q.fmt_c;
   a.shift = q.b_block_rows == 128 ? 7 : 0;
-  a.panel = 8;
-  a.splits = 1;
-  a.GM = cdiv(M, 128);
-  a.GN = cdiv(N, 128);
-  int64_t grid;
-  if (__builtin_mul_overflow(a.GM, a.GN, &grid) || !fits_x(grid, 256)) return GEMM_ERR_SHAPE;
-  (void)workspace;
-  (void)workspace_bytes;
-  return run(f8s_tile_fn(F8S_TILE_128, q.fmt_a, q.fmt_b, a.shift == 0), dim3((unsigned)grid), 256, &a, (hipStream_t)stream);
+  a.panel = 8;   // 32768 x 2048 x 7168 by 256x256: 410 us, 443 with 4, 439 with 16
+  const bool wide = q.fmt_c == GEMM_FMT_F32;
+  int variant = q.variant;
+  if (variant == GEMM_F8S_AUTO) {
+    int cus = 0;
+    const int rc = device_cus(&cus);
+    if (rc) return rc;
+    variant = plan(a, wide, cus);
+    if (variant == GEMM_F8S_AUTO) return GEMM_ERR_SHAPE;
+  } else if (!takes(a, variant, wide)) {
+    return GEMM_ERR_OPTS;
+  }
+  const F8sShape& s = kF8sShapes[variant];
+  a.GM = cdiv(M, s.rows);
+  a.GN = cdiv(N, s.cols);
+  const dim3 grid = s.parts > 1 ? dim3((unsigned)a.GN, (unsigned)a.GM) : dim3((unsigned)(a.GM * a.GN));
+  return run(product_fn(q.fmt_a, q.fmt_b, variant, a.shift == 0, wide, q.fmt_c), grid, s.threads, &a, (hipStream_t)stream);
 }
 
 }  // extern "C"

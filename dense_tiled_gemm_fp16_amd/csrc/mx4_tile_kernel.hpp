@@ -104,14 +104,6 @@ __global__ __launch_bounds__(256) void mx4_scales_kernel(Mx4ScaleArgs a) {
   }
 }
 
-// One 256-byte DMA: lane l's dword at base + 4 l lands at LDS lds + 4 l.
-__device__ __forceinline__ void dma4s(uint32_t off, const char* base, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-               :
-               : "s"(lds), "v"(off), "s"(base)
-               : "memory", "m0");
-}
-
 struct Mx4Frag {
   u32x4 c[2];       // blocks 2 g and 2 g + 1 of a row
   uint32_t s;       // their scales in bytes 0 and 1

@@ -44,10 +44,33 @@ int gemm_f8s_quantize(const void* X, int32_t fmt, int64_t ldx_r, int64_t ldx_k, 
  * A [M, K] of 8-bit format fmt_a in row blocks, scale of block b of row m at
  * SA + m*lsa_m + b*lsa_k; B [N, K] of fmt_b in row blocks (b_block_rows 1) or
  * square blocks (128), scale at SB + (n / b_block_rows)*lsb_n + b*lsb_k.
- * lda, ldb: row strides in bytes; rows start 16-byte aligned (GEMM_ERR_LAYOUT).
- * Needs gemm_f8s_workspace_bytes(M, N, K) bytes of workspace (may be 0), 256-byte
- * aligned; with workspace == NULL they are allocated in stream order.
+ * lda, ldb: row strides in bytes, at most 2^23; rows start 16-byte aligned; lsa_m,
+ * lsb_n at most 2^21 (else GEMM_ERR_LAYOUT).  Up to the next multiple of 16 bytes
+ * behind a row's K may be read, and is ignored.
+ *
+ * Sums: for 16-bit C the FP8 matrix instructions add each 8 consecutive products
+ * aligned to their largest and cut 2^-13 below it, then in float32: 1 to 3 in 10^5
+ * of a sum of random products, far below C's own rounding.  For float32 C the
+ * products are exact and all sums float32, at about half the rate.
+ *
+ * variant: GEMM_F8S_AUTO, or a kernel by its tile (all compute the same; one that
+ * does not take the call is GEMM_ERR_OPTS).  GEMM_ERR_SHAPE: more tiles than a
+ * launch of any of them takes.
  */
+enum gemm_f8s_variant {
+  GEMM_F8S_AUTO = 0,
+  GEMM_F8S_STRIP_16X16 = 1,
+  GEMM_F8S_STRIP_16X32 = 2,
+  GEMM_F8S_STRIP_32X16 = 3,
+  GEMM_F8S_STRIP_32X32 = 4,
+  GEMM_F8S_STRIP_64X32 = 5,
+  GEMM_F8S_STRIP_64X64 = 6,
+  GEMM_F8S_TILE_64X128 = 7,
+  GEMM_F8S_TILE_128X128 = 8,
+  GEMM_F8S_TILE_256X128 = 9,
+  GEMM_F8S_TILE_256X256 = 10
+};
+
 typedef struct gemm_f8s_args {
   const void* A;
   int64_t lda;
@@ -60,11 +83,10 @@ typedef struct gemm_f8s_args {
   void* C;
   int64_t ldc;
   int64_t M, N, K;
-  int32_t fmt_a, fmt_b, b_block_rows, fmt_c;
+  int32_t fmt_a, fmt_b, b_block_rows, fmt_c, variant;
 } gemm_f8s_args;
 
-int gemm_f8s(const gemm_f8s_args* args, void* stream, void* workspace, size_t workspace_bytes);
-size_t gemm_f8s_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int gemm_f8s(const gemm_f8s_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -58,11 +58,19 @@ def values(data, scales):
 
 def product(a, sa, b, sb, dtype):
     """(C, tolerance) of gemm_f8_scaled: fp32 sums over K products and the
-    blocks' scaled sums (two roundings of the scale, one of the sum), the
-    output's half step."""
+    blocks' scaled sums (two roundings of the scale, one of the sum); for a 16-bit
+    C each 8 consecutive products cut at 2^-13 of their largest, so that seven of
+    them are off by that much at most; the output's half step."""
     x, y = values(a, sa), values(b, sb)
     c, mag = x @ y.T, np.abs(x) @ np.abs(y).T
     tol = (a.shape[1] + 4 * blocks(a.shape[1]) + 8) * U * mag
+    if dtype != torch.float32:
+        for k in range(0, a.shape[1], 8):
+            xs, ys = np.abs(x[:, k:k + 8]), np.abs(y[:, k:k + 8])
+            top = np.zeros_like(c)
+            for i in range(xs.shape[1]):
+                np.maximum(top, np.outer(xs[:, i], ys[:, i]), out=top)
+            tol += 7 * 2.0 ** -13 * top
     return c, tol + half_step(np.abs(c) + tol, dtype)
 
 

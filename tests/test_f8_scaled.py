@@ -166,22 +166,95 @@ def test_product(M, N, K, fa, fb, brows, dtype):
     check_product(a, sa, b, sb, dtype, f"f8 scaled {M}x{N}x{K} {fa} {fb} {brows} {dtype}")
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 100, 700), (31, 70, 300), (200, 300, 900), (513, 700, 1281)])
+VARIANTS = list(g.f8_scaled.VARIANTS)
+
+
+def taken(variant, brows, dtype):
+    return variant != "tile256x256" or (brows == 128 and dtype != F32)
+
+
+def whole(R, K, dtype, seed):
+    """Whole numbers of up to 4 in 8 bits, with NaN codes behind K."""
+    data = rows8(R, K, dtype, seed)
+    data.copy_(torch.from_numpy(np.random.default_rng(seed).integers(-4, 5, (R, K))).float())
+    return data
+
+
+def rounded(c, dtype):
+    """Whole numbers below 2^24 to dtype, once."""
+    return f64(torch.from_numpy(c).float().to(dtype))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 100, 700), (31, 70, 128), (70, 130, 300), (200, 300, 900), (513, 700, 1281)])
 @pytest.mark.parametrize("brows", [1, 128])
-def test_exact_on_whole_numbers(M, N, K, brows):
+@pytest.mark.parametrize("variant", VARIANTS)
+def test_exact_on_whole_numbers(M, N, K, brows, variant):
     """Whole numbers of up to 4 and scales of 1, 2 and 4: every sum is exact, so
-    every bit of a float32 result is."""
-    say(f"f8 scaled exact {M}x{N}x{K} {brows}")
+    every bit of a result is."""
+    a, b = whole(M, K, E4M3, 1), whole(N, K, E5M2, 2)
     rng = np.random.default_rng(M + N)
-    A, B = rng.integers(-4, 5, (M, K)), rng.integers(-4, 5, (N, K))
-    a, b = rows8(M, K, E4M3, 1), rows8(N, K, E5M2, 2)
-    a.copy_(torch.from_numpy(A).float())
-    b.copy_(torch.from_numpy(B).float())
     sa = torch.from_numpy(2.0 ** rng.integers(0, 3, (M, ref.blocks(K)))).float().to(DEV)
     sb = torch.from_numpy(2.0 ** rng.integers(0, 3, (-(-N // brows), ref.blocks(K)))).float().to(DEV)
-    c = g.gemm_f8_scaled(a, sa, b, sb, dtype=F32)
     want, _ = ref.product(a, sa, b, sb, F32)
-    assert np.array_equal(f64(c), want)
+    for dtype in (F32, F16, BF16):
+        if taken(variant, brows, dtype):
+            say(f"f8 scaled exact {M}x{N}x{K} {brows} {variant} {dtype}")
+            c = g.gemm_f8_scaled(a, sa, b, sb, dtype=dtype, variant=variant)
+            assert np.array_equal(f64(c), rounded(want, dtype))
+
+
+@pytest.mark.parametrize("K", [1, 16, 17, 127, 128, 129, 255, 256, 384, 500, 512, 640, 641, 1025, 1153, 2049, 2176])
+@pytest.mark.parametrize("variant", VARIANTS)
+def test_every_number_of_blocks(K, variant):
+    """Rings that are longer than K, and K's end at every place of them."""
+    say(f"f8 scaled blocks {K} {variant}")
+    M, N = 90, 150
+    a, b = whole(M, K, E5M2, 3), whole(N, K, E4M3, 4)
+    rng = np.random.default_rng(K)
+    sa = torch.from_numpy(2.0 ** rng.integers(0, 3, (M, ref.blocks(K)))).float().to(DEV)
+    sb = torch.from_numpy(2.0 ** rng.integers(0, 3, (2, ref.blocks(K)))).float().to(DEV)
+    want, _ = ref.product(a, sa, b, sb, F32)
+    assert np.array_equal(f64(g.gemm_f8_scaled(a, sa, b, sb, dtype=BF16, variant=variant)), rounded(want, BF16))
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("fa,fb", [(E4M3, E4M3), (E4M3, E5M2), (E5M2, E4M3), (E5M2, E5M2)])
+def test_every_code_times_every_code(fa, fb, variant):
+    """Row m has code m at one place, so C is the table of products, each exact in
+    float32: subnormal and non-finite codes included."""
+    say(f"f8 scaled codes {fa} {fb} {variant}")
+    K, at = 200, 150
+    a, b = torch.zeros(256, 208, dtype=torch.uint8), torch.zeros(256, 208, dtype=torch.uint8)
+    a[:, at] = b[:, at] = torch.arange(256).to(torch.uint8)
+    a, b = a.to(DEV).view(fa)[:, :K], b.to(DEV).view(fb)[:, :K]
+    one = torch.ones(256, 2, device=DEV)
+    with np.errstate(invalid="ignore"):
+        table = np.outer(f64(a)[:, at], f64(b)[:, at])
+    for dtype, sb in ((F32, one), (BF16, one[:2])):
+        if taken(variant, sb.shape[0] // 256 or 128, dtype):
+            c = g.gemm_f8_scaled(a, one, b, sb, dtype=dtype, variant=variant)
+            want = f64(torch.from_numpy(table).float().to(dtype))
+            assert np.array_equal(f64(c), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("variant", VARIANTS[1:])
+@pytest.mark.parametrize("M,N,K", [(300, 400, 1100), (70, 260, 2000)])
+def test_variants_within_tolerance(M, N, K, variant):
+    a, b = rows8(M, K, E4M3, 1), rows8(N, K, E4M3, 2)
+    for brows in (1, 128):
+        sa, sb = scales_of(M, K, 3), scales_of(-(-N // brows), K, 4)
+        for dtype in (F32, F16, BF16):
+            if taken(variant, brows, dtype):
+                check_product(a, sa, b, sb, dtype, f"f8 scaled {M}x{N}x{K} {brows} {variant} {dtype}", variant=variant)
+
+
+def test_variants_that_do_not_take_the_call():
+    a, b, s = rows8(8, 128, E4M3, 1), rows8(8, 128, E4M3, 2), torch.ones(8, 1, device=DEV)
+    for sb, dtype in ((s, BF16), (s[:1], F32)):
+        with pytest.raises(g.GemmError):
+            g.gemm_f8_scaled(a, s, b, sb, dtype=dtype, variant="tile256x256")
+    with pytest.raises(KeyError):
+        g.gemm_f8_scaled(a, s, b, s, variant="tile1x1")
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 300, 700), (20, 300, 700), (200, 300, 700)])

@@ -54,11 +54,11 @@ def test_quantize_refusals(kw, code):
     assert quantize(**kw) == code
 
 
-def product(ws=0, nws=0, **kw):
+def product(**kw):
     d = dict(A=P[0], lda=304, SA=P[1], lsa_m=3, lsa_k=1, B=P[2], ldb=304, SB=P[3], lsb_n=3, lsb_k=1, C=P[4], ldc=200,
-             M=100, N=200, K=300, fmt_a=0, fmt_b=1, b_block_rows=128, fmt_c=1)
+             M=100, N=200, K=300, fmt_a=0, fmt_b=1, b_block_rows=128, fmt_c=1, variant=0)
     d.update(kw)
-    return g.lib.gemm_f8s(ctypes.byref(_lib.F8sArgs(**d)), None, ws, nws)
+    return g.lib.gemm_f8s(ctypes.byref(_lib.F8sArgs(**d)), None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -66,9 +66,12 @@ def product(ws=0, nws=0, **kw):
     (dict(M=0), -2), (dict(N=-1), -2), (dict(K=0), -2), (dict(K=2 ** 40, lda=2 ** 40, ldb=2 ** 40), -2),
     (dict(lda=2 ** 62), -2), (dict(ldc=2 ** 62), -2), (dict(lsa_m=2 ** 61), -2), (dict(lsb_k=2 ** 62), -2),
     (dict(fmt_a=2), -7), (dict(fmt_b=-1), -7), (dict(b_block_rows=2), -7), (dict(fmt_c=3), -7),
+    (dict(variant=-1), -7), (dict(variant=11), -7), (dict(variant=10, b_block_rows=1, lsb_n=3), -7),
+    (dict(variant=10, fmt_c=2, ldc=200), -7),
     (dict(lda=0), -3), (dict(lda=288), -3), (dict(ldb=288), -3), (dict(lsa_m=0), -3), (dict(lsa_k=0), -3),
     (dict(lsb_n=-3), -3), (dict(lsb_k=0), -3), (dict(ldc=199), -4),
-    (dict(lda=300), -9), (dict(ldb=312), -9), (dict(A=P[0] + 8), -9), (dict(B=P[2] + 4), -9), (dict(SA=P[1] + 2), -9),
+    (dict(lda=300), -9), (dict(lda=2 ** 23 + 16), -9), (dict(ldb=2 ** 24), -9), (dict(lsa_m=2 ** 22), -9),
+    (dict(lsb_n=2 ** 22), -9), (dict(ldb=312), -9), (dict(A=P[0] + 8), -9), (dict(B=P[2] + 4), -9), (dict(SA=P[1] + 2), -9),
     (dict(C=P[4] + 1), -9), (dict(C=P[0]), -5), (dict(C=P[1]), -5), (dict(C=P[2]), -5), (dict(C=P[3]), -5),
 ])
 def test_product_refusals(kw, code):
@@ -76,7 +79,7 @@ def test_product_refusals(kw, code):
 
 
 def test_product_refuses_no_arguments_at_all():
-    assert g.lib.gemm_f8s(None, None, 0, 0) == -1
+    assert g.lib.gemm_f8s(None, None) == -1
 
 
 def norm(X=P[0], ldx=300, res=P[1], ldr=300, fmt=1, W=P[2], fmt_w=2, eps=1e-6, H=P[3], ldh=300, data=P[4], fmt8=0,
@@ -192,7 +195,6 @@ def test_python_refusals_need_no_gpu():
 
 
 def test_workspaces_of_empty_shapes():
-    assert g.gemm_f8_scaled_workspace_bytes(0, 4, 4) == 0
     assert g.rms_norm_backward_workspace_bytes(0, 4) == 0 == g.rms_norm_backward_workspace_bytes(4, 70000)
     assert g.moe_sort_workspace_bytes(0, 2, 4) == 0 == g.moe_sort_workspace_bytes(64, 2, 4)
     assert g.moe_sort_workspace_bytes(100000, 2, 4) > 0
