@@ -6,10 +6,12 @@ library.  There is no fallback: if the library cannot be loaded, importing
 this module raises."""
 import ctypes
 import os
+import struct
 
 from . import build as _build
 
 i32, i64, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+f32 = ctypes.c_float
 
 GEMM_OK = 0
 STATUS = {0: "GEMM_OK", -1: "GEMM_ERR_NULL", -2: "GEMM_ERR_SHAPE", -3: "GEMM_ERR_STRIDE",
@@ -69,6 +71,50 @@ class F8sArgs(ctypes.Structure):   # gemm_f8s_args
                 ("B", vp), ("ldb", i64), ("SB", vp), ("lsb_n", i64), ("lsb_k", i64),
                 ("C", vp), ("ldc", i64), ("M", i64), ("N", i64), ("K", i64),
                 ("fmt_a", i32), ("fmt_b", i32), ("b_block_rows", i32), ("fmt_c", i32), ("variant", i32)]
+
+
+class F8sQuantizeArgs(ctypes.Structure):   # gemm_f8s_quantize_args
+    _fields_ = [("X", vp), ("ldx_r", i64), ("ldx_k", i64), ("R", i64), ("K", i64), ("data", vp), ("ldd", i64),
+                ("scales", vp), ("lds_r", i64), ("lds_k", i64), ("fmt", i32), ("fmt8", i32), ("block_rows", i32)]
+
+
+class NormArgs(ctypes.Structure):   # gemm_rms_norm_f8_args
+    _fields_ = [("X", vp), ("ldx", i64), ("residual", vp), ("ldr", i64), ("W", vp), ("H", vp), ("ldh", i64),
+                ("data", vp), ("ldd", i64), ("scales", vp), ("lds_r", i64), ("lds_k", i64), ("R", i64), ("K", i64),
+                ("eps", f32), ("fmt", i32), ("fmt_w", i32), ("fmt8", i32)]
+
+
+class NormBackwardArgs(ctypes.Structure):   # gemm_rms_norm_backward_args
+    _fields_ = [("DY", vp), ("ldy", i64), ("H", vp), ("ldh", i64), ("W", vp), ("DH", vp), ("lddh", i64), ("DX", vp),
+                ("lddx", i64), ("DW", vp), ("R", i64), ("K", i64), ("eps", f32), ("fmt", i32), ("fmt_w", i32)]
+
+
+class SortArgs(ctypes.Structure):   # gemm_moe_sort_args
+    _fields_ = [("experts", vp), ("ld", i64), ("T", i64), ("offsets", vp), ("rows", vp), ("slots", vp),
+                ("id_bytes", i32), ("top_k", i32), ("E", i32)]
+
+
+class GatherArgs(ctypes.Structure):   # gemm_moe_gather_args
+    _fields_ = [("X", vp), ("ldx", i64), ("offsets", vp), ("slots", vp), ("Y", vp), ("ldy", i64), ("T", i64),
+                ("H", i64), ("elem_bytes", i32), ("E", i32), ("top_k", i32)]
+
+
+class CombineArgs(ctypes.Structure):   # gemm_moe_combine_args
+    _fields_ = [("X", vp), ("ldx", i64), ("slots", vp), ("weights", vp), ("ldw", i64), ("Y", vp), ("ldy", i64),
+                ("T", i64), ("H", i64), ("fmt", i32), ("fmt_w", i32), ("top_k", i32)]
+
+
+class CombineBackwardArgs(ctypes.Structure):   # gemm_moe_combine_backward_args
+    _fields_ = [("DY", vp), ("lddy", i64), ("X", vp), ("ldx", i64), ("offsets", vp), ("slots", vp), ("weights", vp),
+                ("ldw", i64), ("DX", vp), ("lddx", i64), ("DW", vp), ("lddw", i64), ("T", i64), ("H", i64),
+                ("fmt", i32), ("fmt_w", i32), ("E", i32), ("top_k", i32)]
+
+
+def packer(cls):
+    """cls's fields in order -> its bytes, which a c_void_p argument takes: a third
+    of the time of making the Structure (padded to its end)."""
+    code = {vp: "q", i64: "q", i32: "i", f32: "f"}
+    return struct.Struct("@" + "".join(code[t] for _, t in cls._fields_) + "0q").pack
 
 
 def _load():
@@ -142,30 +188,17 @@ def _load():
     lib.gemm_moe.restype = ctypes.c_int
     lib.gemm_moe_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
     lib.gemm_moe_workspace_bytes.restype = sz
-    lib.gemm_f8s_quantize.argtypes = [vp, i32, i64, i64, i64, i64, i32, vp, i32, i64, vp, i64, i64, vp]
-    lib.gemm_f8s_quantize.restype = ctypes.c_int
-    lib.gemm_f8s.argtypes = [ctypes.POINTER(F8sArgs), vp]
-    lib.gemm_f8s.restype = ctypes.c_int
-    f32 = ctypes.c_float
-    lib.gemm_rms_norm_f8.argtypes = [vp, i64, vp, i64, i32, vp, i32, f32, vp, i64, vp, i32, i64, vp, i64, i64,
-                                     i64, i64, vp]
-    lib.gemm_rms_norm_f8.restype = ctypes.c_int
-    lib.gemm_rms_norm_backward.argtypes = [vp, i64, vp, i64, i32, vp, i32, f32, vp, i64, vp, i64, vp, i64, i64,
-                                           vp, vp, sz]
-    lib.gemm_rms_norm_backward.restype = ctypes.c_int
+    for name in ("gemm_f8s_quantize", "gemm_f8s", "gemm_rms_norm_f8", "gemm_moe_gather", "gemm_moe_combine",
+                 "gemm_moe_combine_backward"):
+        getattr(lib, name).argtypes = [vp, vp]
+        getattr(lib, name).restype = ctypes.c_int
+    for name in ("gemm_rms_norm_backward", "gemm_moe_sort"):
+        getattr(lib, name).argtypes = [vp, vp, vp, sz]
+        getattr(lib, name).restype = ctypes.c_int
     lib.gemm_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
     lib.gemm_rms_norm_backward_workspace_bytes.restype = sz
-    lib.gemm_moe_sort.argtypes = [vp, i32, i64, i64, i32, i32, vp, vp, vp, vp, vp, sz]
-    lib.gemm_moe_sort.restype = ctypes.c_int
     lib.gemm_moe_sort_workspace_bytes.argtypes = [i64, i32, i32]
     lib.gemm_moe_sort_workspace_bytes.restype = sz
-    lib.gemm_moe_gather.argtypes = [vp, i64, i32, vp, vp, i32, vp, i64, i64, i32, i64, vp]
-    lib.gemm_moe_gather.restype = ctypes.c_int
-    lib.gemm_moe_combine.argtypes = [vp, i64, i32, vp, vp, i32, i64, vp, i64, i64, i32, i64, vp]
-    lib.gemm_moe_combine.restype = ctypes.c_int
-    lib.gemm_moe_combine_backward.argtypes = [vp, i64, vp, i64, i32, vp, vp, i32, vp, i32, i64, vp, i64, vp, i64,
-                                              i64, i32, i64, vp]
-    lib.gemm_moe_combine_backward.restype = ctypes.c_int
     lib.gemm_f16_status_string.argtypes = [ctypes.c_int]
     lib.gemm_f16_status_string.restype = ctypes.c_char_p
     lib.gemm_f16_version.argtypes = []

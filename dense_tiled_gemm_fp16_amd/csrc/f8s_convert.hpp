@@ -50,25 +50,31 @@ __device__ __forceinline__ F8Scale f8_scale(uint32_t m) {
   s.bad = m >= 0x7F800000u;
   const uint32_t least = lb - (126u << 23);                // L 2^-126
   if (m < least) m = least;
-  s.scale = s.bad ? __builtin_nanf("") : __builtin_bit_cast(float, m) / L;
+  // m / L: the quotient by L's reciprocal, with its residual's correction.
+  const float v = __builtin_bit_cast(float, m), rl = 1.0f / L;               // rl: a constant
+  const float q = v * rl;
+  s.scale = s.bad ? __builtin_nanf("") : __builtin_fmaf(__builtin_fmaf(-q, L, v), rl, q);
   s.f = __builtin_bit_cast(float, (m & 0x007FFFFFu) | 0x3F800000u);
   s.up = __builtin_bit_cast(float, lb - (m & 0x7F800000u) + (127u << 23));   // L 2^-e
-  s.rf = 1.0f / s.f;
+  const float r = __builtin_amdgcn_rcpf(s.f);                                // one Newton step
+  s.rf = __builtin_fmaf(__builtin_fmaf(-s.f, r, 1.0f), r, r);
   return s;
 }
 
+// EXACT: rounded once for a 16-bit x; else twice.
+template <bool EXACT>
 __device__ __forceinline__ float f8_quotient(float x, const F8Scale& s) {
   const float X = x * s.up;
   const float t = X * s.rf;
-  return __builtin_fmaf(__builtin_fmaf(-t, s.f, X), s.rf, t);
+  return EXACT ? __builtin_fmaf(__builtin_fmaf(-t, s.f, X), s.rf, t) : t;
 }
 
 // 8 floats -> 8 codes, the first in the lowest byte; zeros for a bad block.
-template <int F8>
+template <int F8, bool EXACT = true>
 __device__ __forceinline__ u32x2 f8_codes(const float (&x)[8], const F8Scale& s) {
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = f8_quotient(x[i], s);
+  for (int i = 0; i < 8; ++i) q[i] = f8_quotient<EXACT>(x[i], s);
   int d[2] = {0, 0};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -96,9 +102,10 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
 __device__ __forceinline__ uint32_t magnitude(float f) { return __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu; }
 
 // The first n (<= 8) of 8 codes.
+template <bool ONCE = false>
 __device__ __forceinline__ void store_codes(uint8_t* p, u32x2 v, int64_t n) {
   if (n >= 8) {
-    gstore<u32x2>(p, v);
+    gstore_once<ONCE>(p, v);
     return;
   }
 #pragma unroll
@@ -120,7 +127,7 @@ struct F8QuantArgs {
 
 // Rows with unit k stride; wave items as in quantize_rows_kernel, with 16 octets
 // a block.
-template <int FMT, int F8, bool SHORT>
+template <int FMT, int F8, bool SHORT, bool ONCE>
 __global__ __launch_bounds__(256) void f8_rows_kernel(F8QuantArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t w = wave_item();
@@ -129,7 +136,7 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(F8QuantArgs a) {
 #pragma unroll
   for (int u = 0; u < kQuantU; ++u) {
     const Place p = place<SHORT>(w, u, lane, a.R, octs, a.segs, a.few);
-    v[u].load((const char*)a.x + p.row * a.s_r * Oct<FMT>::ES, 8 * p.o, p.ok ? a.K - 8 * p.o : 0);
+    v[u].template load<ONCE>((const char*)a.x + p.row * a.s_r * Oct<FMT>::ES, 8 * p.o, p.ok ? a.K - 8 * p.o : 0);
   }
 #pragma unroll
   for (int u = 0; u < kQuantU; ++u) {
@@ -144,7 +151,7 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(F8QuantArgs a) {
     }
     const F8Scale s = f8_scale<F8>(max16(m));
     if (p.ok) {
-      store_codes(a.data + p.row * a.ldd + 8 * p.o, f8_codes<F8>(f, s), a.K - 8 * p.o);
+      store_codes<ONCE>(a.data + p.row * a.ldd + 8 * p.o, f8_codes<F8>(f, s), a.K - 8 * p.o);
       if ((p.o & 15) == 0) gstore<float>(a.scales + p.row * a.ss_r + (p.o >> 4) * a.ss_k, s.scale);
     }
   }

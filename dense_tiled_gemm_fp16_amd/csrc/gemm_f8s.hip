@@ -30,8 +30,9 @@ int64_t wave_items(int64_t rows, int64_t octs, int64_t* segs, Short* few) {
 }
 
 template <int FMT, int F8>
-const void* rows_fn(bool few) {
-  return few ? (const void*)f8_rows_kernel<FMT, F8, true> : (const void*)f8_rows_kernel<FMT, F8, false>;
+const void* rows_fn(bool few, bool once) {
+  if (once) return few ? (const void*)f8_rows_kernel<FMT, F8, true, true> : (const void*)f8_rows_kernel<FMT, F8, false, true>;
+  return few ? (const void*)f8_rows_kernel<FMT, F8, true, false> : (const void*)f8_rows_kernel<FMT, F8, false, false>;
 }
 template <int FMT, int F8>
 const void* tiles_fn(bool square, bool along_k) {
@@ -40,12 +41,14 @@ const void* tiles_fn(bool square, bool along_k) {
                    : (const void*)f8_tiles_kernel<FMT, F8, true, false>;
 }
 template <int F8>
-const void* quant_fn(int32_t fmt, bool tiles, bool square, bool along_k, bool few) {
+const void* quant_fn(int32_t fmt, bool tiles, bool square, bool along_k, bool few, bool once) {
   if (tiles)
     return fmt == GEMM_FMT_F16    ? tiles_fn<MX_F16, F8>(square, along_k)
            : fmt == GEMM_FMT_BF16 ? tiles_fn<MX_BF16, F8>(square, along_k)
                                   : tiles_fn<MX_F32, F8>(square, along_k);
-  return fmt == GEMM_FMT_F16 ? rows_fn<MX_F16, F8>(few) : fmt == GEMM_FMT_BF16 ? rows_fn<MX_BF16, F8>(few) : rows_fn<MX_F32, F8>(few);
+  return fmt == GEMM_FMT_F16    ? rows_fn<MX_F16, F8>(few, once)
+         : fmt == GEMM_FMT_BF16 ? rows_fn<MX_BF16, F8>(few, once)
+                                : rows_fn<MX_F32, F8>(few, once);
 }
 
 const void* product_fn(int32_t fmt_a, int32_t fmt_b, int variant, bool rowb, bool wide, int out) {
@@ -84,7 +87,7 @@ bool takes(const F8sArgs& a, int variant, bool wide) {
 //   32768 x 2048 x 7168  785, 777, 639, 414
 // Row blocks and float32, 2048 x 7168 x 8192: strips 64x64 436, tiles 64x128 331,
 // 128x128 347, 256x128 280; to bfloat16: 273, 246, 250, 187.  Over 60 random
-// sizes the choice took 3% longer than the best one in the mean, 26% at most.
+// sizes the choice took 3% longer than the best one in the mean, 15% at most.
 int plan(const F8sArgs& a, bool wide, int cus) {
   int best = 0;
   float least = 0.0f;
@@ -108,9 +111,9 @@ int plan(const F8sArgs& a, bool wide, int cus) {
 
 extern "C" {
 
-int gemm_f8s_quantize(const void* X, int32_t fmt, int64_t ldx_r, int64_t ldx_k, int64_t R, int64_t K,
-                      int32_t block_rows, void* data, int32_t fmt8, int64_t ldd, float* scales, int64_t lds_r,
-                      int64_t lds_k, void* stream) {
+int gemm_f8s_quantize(const gemm_f8s_quantize_args* args, void* stream) {
+  if (!args) return GEMM_ERR_NULL;
+  const auto [X, ldx_r, ldx_k, R, K, data, ldd, scales, lds_r, lds_k, fmt, fmt8, block_rows] = *args;
   if (!X || !data || !scales) return GEMM_ERR_NULL;
   if (R <= 0 || K <= 0 || K > kMaxK) return GEMM_ERR_SHAPE;
   if (fmt < GEMM_FMT_F16 || fmt > GEMM_FMT_F32 || fmt8 < 0 || fmt8 > 1 || (block_rows != 1 && block_rows != 128))
@@ -141,8 +144,10 @@ int gemm_f8s_quantize(const void* X, int32_t fmt, int64_t ldx_r, int64_t ldx_k, 
   }
   if (grid > kMaxWide) return GEMM_ERR_SHAPE;
   const bool along_k = ldx_k == 1 || K == 1;
-  const void* fn = fmt8 == 0 ? quant_fn<F8_E4M3>(fmt, tiles, block_rows == 128, along_k, a.few.rows > 0)
-                             : quant_fn<F8_E5M2>(fmt, tiles, block_rows == 128, along_k, a.few.rows > 0);
+  // Past the caches: 32768 x 7168 bfloat16 112 us instead of 120.
+  const bool once = (double)R * (double)K * (double)(elem_size(fmt) + 1) > kOnceBytes;
+  const void* fn = fmt8 == 0 ? quant_fn<F8_E4M3>(fmt, tiles, block_rows == 128, along_k, a.few.rows > 0, once)
+                             : quant_fn<F8_E5M2>(fmt, tiles, block_rows == 128, along_k, a.few.rows > 0, once);
   return run(fn, wide_grid(grid), 256, &a, (hipStream_t)stream);
 }
 

@@ -44,6 +44,10 @@ inline int run(const void* fn, dim3 grid, int threads, void* args, hipStream_t s
   return hipLaunchKernel(fn, grid, dim3((unsigned)threads), p, 0, s) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 
+// The last cache holds 256 MiB: what a call moves beyond half as much again need
+// not stay in it for the next one.
+constexpr double kOnceBytes = 384.0 * (1 << 20);
+
 // A call's workspace: the caller's (checked), or allocated in stream order and
 // given back in that order by done().
 class Workspace {

@@ -179,7 +179,7 @@ struct RowsArgs {
   void* dweights;
   int64_t lddw;
   int64_t T, P, H;         // H: gather: bytes of a row; else elements
-  int32_t top_k, w32;
+  int32_t top_k, w32, parts;
 };
 
 __device__ __forceinline__ int64_t slot_of(const RowsArgs& a, int64_t t, int j) {
@@ -188,9 +188,10 @@ __device__ __forceinline__ int64_t slot_of(const RowsArgs& a, int64_t t, int j) 
 }
 
 // n (<= 16) bytes.
+template <bool ONCE>
 __device__ __forceinline__ void store_bytes(char* p, u32x4 v, int64_t n) {
   if (n >= 16) {
-    store16(p, v);
+    gstore_once<ONCE>(p, v);
     return;
   }
 #pragma unroll
@@ -208,32 +209,26 @@ __device__ __forceinline__ void clear_rest(const RowsArgs& a, int64_t t, int64_t
     const int64_t r = n + t * a.top_k + j;
     if (r >= a.P) return;
     for (int64_t c = c0 + threadIdx.x; c < c1; c += NT)
-      store_bytes((char*)a.out + r * a.ldo + 16 * c, zero4(), bytes - 16 * c);
+      store_bytes<false>((char*)a.out + r * a.ldo + 16 * c, zero4(), bytes - 16 * c);
   }
 }
 
-// Workgroup (part of the row, token): U chunks of 16 bytes per lane.
-template <int U>
-__global__ __launch_bounds__(256) void moe_gather_kernel(RowsArgs a) {
-  const int64_t t = blockIdx.x, chunks = (a.H + 15) / 16;
-  const int64_t c0 = (int64_t)blockIdx.y * (256 * U);
-  const int64_t c1 = c0 + 256 * U < chunks ? c0 + 256 * U : chunks;
-  u32x4 v[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t c = c0 + 256 * u + threadIdx.x;
-    v[u] = c < c1 ? load_bytes((const char*)a.in + t * a.ldi + 16 * c, a.H - 16 * c) : zero4();
-  }
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t s = slot_of(a, t, j);
-    if (s < 0) continue;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = c0 + 256 * u + threadIdx.x;
-      if (c < c1) store_bytes((char*)a.out + s * a.ldo + 16 * c, v[u], a.H - 16 * c);
+// Workgroups of 128 threads: parts of a token's row, its parts one after another,
+// 16 bytes a lane.
+constexpr int kRowThreads = 128;
+
+template <bool ONCE>
+__global__ __launch_bounds__(kRowThreads) void moe_gather_kernel(RowsArgs a) {
+  const int64_t t = blockIdx.x / a.parts, chunks = (a.H + 15) / 16;
+  const int64_t c0 = (int64_t)(blockIdx.x % a.parts) * kRowThreads, c = c0 + threadIdx.x;
+  if (c < chunks) {
+    const u32x4 v = load_bytes((const char*)a.in + t * a.ldi, 16 * c, a.H - 16 * c);
+    for (int j = 0; j < a.top_k; ++j) {
+      const int64_t s = slot_of(a, t, j);
+      if (s >= 0) store_bytes<ONCE>((char*)a.out + s * a.ldo + 16 * c, v, a.H - 16 * c);
     }
   }
-  clear_rest<256>(a, t, a.H, c0, c1);
+  clear_rest<kRowThreads>(a, t, a.H, c0, c0 + kRowThreads < chunks ? c0 + kRowThreads : chunks);
 }
 
 // Weight of choice j of token t, 1 without weights.
@@ -245,53 +240,53 @@ __device__ __forceinline__ float weight_of(const RowsArgs& a, int64_t t, int j) 
   return mx_in<FMT>(((const typename MxElem<FMT>::type*)a.weights)[at]);
 }
 
-template <int FMT>
+template <int FMT, bool ONCE>
 __device__ __forceinline__ void store_oct(char* row, int64_t k, const float (&f)[8], int64_t n) {
   if constexpr (FMT == MX_F32) {
     float* p = (float*)row + k;
     if (n >= 8) {
-      gstore<f32x4>(p, f32x4{f[0], f[1], f[2], f[3]});
-      gstore<f32x4>(p + 4, f32x4{f[4], f[5], f[6], f[7]});
+      gstore_once<ONCE>(p, f32x4{f[0], f[1], f[2], f[3]});
+      gstore_once<ONCE>(p + 4, f32x4{f[4], f[5], f[6], f[7]});
     } else {
 #pragma unroll
       for (int i = 0; i < 7; ++i)
         if (i < n) gstore<float>(p + i, f[i]);
     }
   } else {
-    store8_part((uint16_t*)row + k, pack8<FMT>(f), n);
+    store8_part<ONCE>((uint16_t*)row + k, pack8<FMT>(f), n);
   }
 }
 
 constexpr int kRowsAhead = 8;   // rows in flight
 
-// Workgroup (part of the row, token), an octet per lane.
-template <int FMT>
-__global__ __launch_bounds__(256) void moe_combine_kernel(RowsArgs a) {
-  const int64_t t = blockIdx.x, k = 8 * ((int64_t)blockIdx.y * 256 + threadIdx.x);
+// An octet per lane, workgroups as above.
+template <int FMT, bool ONCE>
+__global__ __launch_bounds__(kRowThreads) void moe_combine_kernel(RowsArgs a) {
+  const int64_t t = blockIdx.x / a.parts, k = 8 * ((int64_t)(blockIdx.x % a.parts) * kRowThreads + threadIdx.x);
   if (k >= a.H) return;
   float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   for (int j0 = 0; j0 < a.top_k; j0 += kRowsAhead) {
     Oct<FMT> v[kRowsAhead];
+    int64_t s[kRowsAhead];
 #pragma unroll
     for (int i = 0; i < kRowsAhead; ++i) {
-      const int64_t s = j0 + i < a.top_k ? slot_of(a, t, j0 + i) : -1;
-      v[i].load((const char*)a.in + (s < 0 ? 0 : s) * a.ldi, k, s < 0 ? 0 : a.H - k);
+      s[i] = j0 + i < a.top_k ? slot_of(a, t, j0 + i) : -1;
+      v[i].template load<ONCE>((const char*)a.in + (s[i] < 0 ? 0 : s[i]) * a.ldi, k, s[i] < 0 ? 0 : a.H - k);
     }
 #pragma unroll
     for (int i = 0; i < kRowsAhead; ++i) {
       // an absent row takes no part, whatever its weight
-      const bool some = j0 + i < a.top_k && slot_of(a, t, j0 + i) >= 0;
-      const float w = some ? weight_of<FMT>(a, t, j0 + i) : 0.0f;
+      const float w = s[i] >= 0 ? weight_of<FMT>(a, t, j0 + i) : 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(w, v[i].get(e), sum[e]);
     }
   }
-  store_oct<FMT>((char*)a.out + t * a.ldo, k, sum, a.H - k);
+  store_oct<FMT, false>((char*)a.out + t * a.ldo, k, sum, a.H - k);
 }
 
 // Workgroup: a token.  Choices eight at a time; the token's gradient is read
 // again for each further eight.
-template <int FMT>
+template <int FMT, bool ONCE>
 __global__ __launch_bounds__(256) void moe_combine_back_kernel(RowsArgs a) {
   __shared__ float part[4][kRowsAhead];
   const int64_t t = blockIdx.x;
@@ -310,7 +305,7 @@ __global__ __launch_bounds__(256) void moe_combine_back_kernel(RowsArgs a) {
       g.load((const char*)a.dy + t * a.ldy, k, a.H - k);
 #pragma unroll
       for (int i = 0; i < kRowsAhead; ++i)
-        v[i].load((const char*)a.in + (s[i] < 0 ? 0 : s[i]) * a.ldi, k, s[i] < 0 ? 0 : a.H - k);
+        v[i].template load<ONCE>((const char*)a.in + (s[i] < 0 ? 0 : s[i]) * a.ldi, k, s[i] < 0 ? 0 : a.H - k);
 #pragma unroll
       for (int i = 0; i < kRowsAhead; ++i) {
         if (s[i] < 0) continue;
@@ -320,7 +315,7 @@ __global__ __launch_bounds__(256) void moe_combine_back_kernel(RowsArgs a) {
           f[e] = w[i] * g.get(e);
           dot[i] = __builtin_fmaf(g.get(e), v[i].get(e), dot[i]);
         }
-        store_oct<FMT>((char*)a.out + s[i] * a.ldo, k, f, a.H - k);
+        store_oct<FMT, ONCE>((char*)a.out + s[i] * a.ldo, k, f, a.H - k);
       }
     }
 #pragma unroll

@@ -41,13 +41,49 @@ __device__ __forceinline__ void gstore(void* p, T v) {
 __device__ __forceinline__ u32x4 load16(const void* p) { return gload<u32x4>(p); }
 __device__ __forceinline__ void store16(void* p, u32x4 v) { gstore<u32x4>(p, v); }
 
-// n bytes (0 .. 16) at p, zeros behind them; nothing past them is read.
-__device__ __forceinline__ u32x4 load_bytes(const char* p, int64_t n) {
-  if (n >= 16) return load16(p);
+// The same for what is read or written once and too much for the last cache to
+// keep (kOnceBytes): past the caches.
+template <bool ONCE>
+__device__ __forceinline__ u32x4 load16_once(const void* p) {
+  typedef u32x4 Any __attribute__((aligned(1)));
+  if constexpr (ONCE) return __builtin_nontemporal_load((const GEMM_GLOBAL Any*)p);
+  return load16(p);
+}
+template <bool ONCE, class T>
+__device__ __forceinline__ void gstore_once(void* p, T v) {
+  typedef T Any __attribute__((aligned(1)));
+  if constexpr (ONCE)
+    __builtin_nontemporal_store(v, (GEMM_GLOBAL Any*)p);
+  else
+    gstore<T>(p, v);
+}
+
+// v without its lowest `bytes` (1 .. 15), zeros from above.
+__device__ __forceinline__ u32x4 drop_bytes(u32x4 v, int bytes) {
+  uint64_t lo = (uint64_t)v[0] | (uint64_t)v[1] << 32, hi = (uint64_t)v[2] | (uint64_t)v[3] << 32;
+  if (bytes >= 8) {
+    lo = hi;
+    hi = 0;
+    bytes -= 8;
+  }
+  if (bytes > 0) {
+    lo = lo >> (8 * bytes) | hi << (64 - 8 * bytes);
+    hi >>= 8 * bytes;
+  }
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+// Bytes at .. at + 15 of a row, the first n of them, zeros behind (n is the rest
+// of the row where it is below 16).  The rest comes by one load of the row's
+// last 16 bytes: byte by byte, each load's latency is waited for.
+__device__ __forceinline__ u32x4 load_bytes(const char* row, int64_t at, int64_t n) {
+  if (n >= 16) return load16(row + at);
+  if (n <= 0) return zero4();
+  if (at + n >= 16) return drop_bytes(load16(row + at + n - 16), 16 - (int)n);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int e = 0; e < 15; ++e)
-    if (e < n) w[e / 4] |= (uint32_t)gload<uint8_t>(p + e) << (8 * (e % 4));
+    if (e < n) w[e / 4] |= (uint32_t)gload<uint8_t>(row + at + e) << (8 * (e % 4));
   return u32x4{w[0], w[1], w[2], w[3]};
 }
 

@@ -77,11 +77,12 @@ struct Oct {
   static constexpr int ES = FMT == MX_F32 ? 4 : 2;
   u32x4 v[ES / 2];
 
+  template <bool ONCE = false>
   __device__ __forceinline__ void load(const void* base, int64_t k, int64_t n) {
     const char* p = (const char*)base + k * ES;
     if (n >= 8) {
-      v[0] = load16(p);
-      if constexpr (FMT == MX_F32) v[1] = load16(p + 16);
+      v[0] = load16_once<ONCE>(p);
+      if constexpr (FMT == MX_F32) v[1] = load16_once<ONCE>(p + 16);
       return;
     }
     uint32_t h[8];

@@ -34,14 +34,42 @@ struct NormArgs {
   int64_t ss_r, ss_k;
   int64_t R, K;
   float eps;
-  int32_t waves;           // of a row
+  int32_t waves, lanes;    // of a row; lanes: log2 of 64, or of 16 or 32 where rows share a wave
 };
+
+// Sum over 16 neighbouring lanes, in all of them: lane exchanges that are part of
+// the addition (an exchange through LDS takes some 100 cycles, and each of a
+// sum's would be waited for).
+__device__ __forceinline__ float sum16(float v) {
+  auto other = [&](auto ctrl) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xF,
+                                                                 0xF, true));
+  };
+  v += other(std::integral_constant<int, 0xB1>{});    // lane ^ 1
+  v += other(std::integral_constant<int, 0x4E>{});    // lane ^ 2
+  v += other(std::integral_constant<int, 0x141>{});   // mirrored in 8
+  v += other(std::integral_constant<int, 0x140>{});   // mirrored in 16
+  return v;
+}
 
 // Sum over the wave, in all lanes.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+  const int s = __builtin_bit_cast(int, sum16(v));
+  auto lane = [&](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(s, l)); };
+  return (lane(0) + lane(16)) + (lane(32) + lane(48));
+}
+
+// Sum over the 2^lanes (16, 32 or 64) lanes of a row (or a row's part), in all of them.
+__device__ __forceinline__ float row_sum(float v, int lanes) {
+  if (lanes == 6) return wave_sum(v);
+  v = sum16(v);
+  return lanes == 5 ? v + __shfl_xor(v, 16) : v;
+}
+
+// Sum of the first n (<= 16) of 16 floats in LDS, in all lanes.
+__device__ __forceinline__ float sum_parts(const float* part, int n, int lane) {
+  const float v = part[lane & 15];
+  return sum16((lane & 15) < n ? v : 0.0f);
 }
 
 // 8 floats -> 8 16-bit elements.
@@ -53,9 +81,10 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
 }
 
 // The first n (<= 8) of 8 16-bit elements.
+template <bool ONCE = false>
 __device__ __forceinline__ void store8_part(uint16_t* p, u32x4 v, int64_t n) {
   if (n >= 8) {
-    store16(p, v);
+    gstore_once<ONCE>(p, v);
     return;
   }
 #pragma unroll
@@ -63,49 +92,51 @@ __device__ __forceinline__ void store8_part(uint16_t* p, u32x4 v, int64_t n) {
     if (i < n) gstore<uint16_t>(p + i, (uint16_t)(v[i / 2] >> (16 * (i % 2))));
 }
 
-// U octets of a row per lane; W32: the weight is float32, else of x's format.
-template <int FMT, int F8, int U, bool RES, bool W32>
+// U octets of a row per lane; W32: the weight is float32, else of x's format;
+// ONCE: the rows go past the caches (see kOnceBytes).
+template <int FMT, int F8, int U, bool RES, bool W32, bool ONCE>
 __global__ __launch_bounds__(1024) void rms_norm_f8_kernel(NormArgs a) {
   __shared__ float part[16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int sub = wave / a.waves, rw = wave - sub * a.waves;    // row of the workgroup, wave of the row
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / 64 / a.waves) + sub;
-  if (row >= a.R) return;                                       // several rows: each in a wave of its own
+  // Row of the workgroup, wave of the row.  A workgroup of several rows has each in
+  // a wave of its own, or a part of one.
+  const int share = 64 >> a.lanes, sub = wave / a.waves * share + (lane >> a.lanes), rw = wave % a.waves;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / 64 / a.waves * share) + sub;
+  if (row >= a.R) return;
   const int step = 64 * a.waves;
-  const int64_t o0 = 64 * rw + lane;
+  const int64_t o0 = 64 * rw + (lane & ((1 << a.lanes) - 1));
   constexpr int ES = 2;
   Oct<FMT> vx[U], vr[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t k = 8 * (o0 + u * step);
-    vx[u].load((const char*)a.x + row * a.ldx * ES, k, a.K - k);
-    if constexpr (RES) vr[u].load((const char*)a.residual + row * a.ldr * ES, k, a.K - k);
+    vx[u].template load<ONCE>((const char*)a.x + row * a.ldx * ES, k, a.K - k);
+    if constexpr (RES) vr[u].template load<ONCE>((const char*)a.residual + row * a.ldr * ES, k, a.K - k);
   }
   float v[U][8];
   float sum = 0.0f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
+    const int64_t k = 8 * (o0 + u * step);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[u][i] = vx[u].get(i);
     if constexpr (RES) {
-      const int64_t k = 8 * (o0 + u * step);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[u][i] += vr[u].get(i);
       Oct<FMT> o;
       o.v[0] = pack8<FMT>(v[u]);
-      if (k < a.K) store8_part((uint16_t*)a.h + row * a.ldh + k, o.v[0], a.K - k);
+      if (k < a.K) store8_part<ONCE>((uint16_t*)a.h + row * a.ldh + k, o.v[0], a.K - k);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[u][i] = o.get(i);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(v[u][i], v[u][i], sum);
   }
-  sum = wave_sum(sum);
+  sum = row_sum(sum, a.lanes);
   if (a.waves > 1) {                                            // then the workgroup's only row
     if (lane == 0) part[wave] = sum;
     __syncthreads();
-    sum = 0.0f;
-    for (int i = 0; i < a.waves; ++i) sum += part[i];
+    sum = sum_parts(part, a.waves, lane);
   }
   const float r = 1.0f / sqrtf(sum / (float)a.K + a.eps);
 #pragma unroll
@@ -122,7 +153,7 @@ __global__ __launch_bounds__(1024) void rms_norm_f8_kernel(NormArgs a) {
     }
     const F8Scale s = f8_scale<F8>(max16(m));
     if (k < a.K) {
-      store_codes(a.data + row * a.ldd + k, f8_codes<F8>(v[u], s), a.K - k);
+      store_codes<ONCE>(a.data + row * a.ldd + k, f8_codes<F8, false>(v[u], s), a.K - k);
       if ((lane & 15) == 0) gstore<float>(a.scales + row * a.ss_r + (k >> 7) * a.ss_k, s.scale);
     }
   }
@@ -141,18 +172,21 @@ struct NormBackArgs {
   float* part;             // [workgroups x rows of each][K]
   int64_t R, K;
   float eps;
-  int32_t waves;
+  int32_t waves, lanes;
 };
 
-template <int FMT, int U, bool DH, bool W32>
-__global__ __launch_bounds__(1024) void rms_norm_back_kernel(NormBackArgs a) {
+// NT: threads of the widest row.  With two or four octets a lane there are
+// registers for the next row, which is loaded under this one's sums.
+template <int FMT, int U, int NT, bool DH, bool W32, bool ONCE>
+__global__ __launch_bounds__(NT) void rms_norm_back_kernel(NormBackArgs a) {
+  constexpr bool AHEAD = U <= 4;
   __shared__ float part[2][2][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int sub = wave / a.waves, rw = wave - sub * a.waves;
-  const int64_t per = blockDim.x / 64 / a.waves;
+  const int share = 64 >> a.lanes, sub = wave / a.waves * share + (lane >> a.lanes), rw = wave % a.waves;
+  const int64_t per = blockDim.x / 64 / a.waves * share;
   const int64_t first = (int64_t)blockIdx.x * per + sub, stride = (int64_t)gridDim.x * per;
   const int step = 64 * a.waves;
-  const int64_t o0 = 64 * rw + lane;
+  const int64_t o0 = 64 * rw + (lane & ((1 << a.lanes) - 1));
   constexpr int ES = 2;
   float w[U][8], dw[U][8];
 #pragma unroll
@@ -166,27 +200,36 @@ __global__ __launch_bounds__(1024) void rms_norm_back_kernel(NormBackArgs a) {
       dw[u][i] = 0.0f;
     }
   }
-  int turn = 0;
-  for (int64_t row = first; row < a.R; row += stride, turn ^= 1) {
-    Oct<FMT> vy[U], vh[U], vd[U];
+  struct Row {
+    Oct<FMT> y[U], h[U], d[DH ? U : 1];
+  };
+  auto load = [&](Row& r, int64_t row) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t k = 8 * (o0 + u * step);
-      vy[u].load((const char*)a.dy + row * a.ldy * ES, k, a.K - k);
-      vh[u].load((const char*)a.h + row * a.ldh * ES, k, a.K - k);
-      if constexpr (DH) vd[u].load((const char*)a.dh + row * a.lddh * ES, k, a.K - k);
+      r.y[u].template load<ONCE>((const char*)a.dy + row * a.ldy * ES, k, a.K - k);
+      r.h[u].template load<ONCE>((const char*)a.h + row * a.ldh * ES, k, a.K - k);
+      if constexpr (DH) r.d[u].template load<ONCE>((const char*)a.dh + row * a.lddh * ES, k, a.K - k);
     }
+  };
+  int turn = 0;
+  Row next;
+  if (AHEAD && first < a.R) load(next, first);
+  for (int64_t row = first; row < a.R; row += stride, turn ^= 1) {
+    if constexpr (!AHEAD) load(next, row);
+    const Row now = next;
+    if (AHEAD && row + stride < a.R) load(next, row + stride);
     float ss = 0.0f, sg = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float h = vh[u].get(i);
+        const float h = now.h[u].get(i);
         ss = __builtin_fmaf(h, h, ss);
-        sg = __builtin_fmaf(vy[u].get(i) * w[u][i], h, sg);
+        sg = __builtin_fmaf(now.y[u].get(i) * w[u][i], h, sg);
       }
-    ss = wave_sum(ss);
-    sg = wave_sum(sg);
+    ss = row_sum(ss, a.lanes);
+    sg = row_sum(sg, a.lanes);
     if (a.waves > 1) {
       // the other half of `part` is still being read by slower waves; this one was
       // before the last barrier
@@ -195,11 +238,8 @@ __global__ __launch_bounds__(1024) void rms_norm_back_kernel(NormBackArgs a) {
         part[turn][1][wave] = sg;
       }
       __syncthreads();
-      ss = sg = 0.0f;
-      for (int i = 0; i < a.waves; ++i) {
-        ss += part[turn][0][i];
-        sg += part[turn][1][i];
-      }
+      ss = sum_parts(part[turn][0], a.waves, lane);
+      sg = sum_parts(part[turn][1], a.waves, lane);
     }
     const float r = 1.0f / sqrtf(ss / (float)a.K + a.eps);
     const float c = sg / (float)a.K * r * r;
@@ -209,12 +249,12 @@ __global__ __launch_bounds__(1024) void rms_norm_back_kernel(NormBackArgs a) {
       float d[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float h = vh[u].get(i), y = vy[u].get(i);
+        const float h = now.h[u].get(i), y = now.y[u].get(i);
         d[i] = r * (y * w[u][i] - h * c);
-        if constexpr (DH) d[i] += vd[u].get(i);
+        if constexpr (DH) d[i] += now.d[u].get(i);
         dw[u][i] = __builtin_fmaf(y * r, h, dw[u][i]);
       }
-      if (k < a.K) store8_part((uint16_t*)a.dx + row * a.lddx + k, pack8<FMT>(d), a.K - k);
+      if (k < a.K) store8_part<ONCE>((uint16_t*)a.dx + row * a.lddx + k, pack8<FMT>(d), a.K - k);
     }
   }
   float* p = a.part + first * a.K;
@@ -232,21 +272,30 @@ __global__ __launch_bounds__(1024) void rms_norm_back_kernel(NormBackArgs a) {
   }
 }
 
-// dw[k] = sum over p of part[p][k]: 64 columns a workgroup, its 16 waves every
-// 16th row each, then their sums in ascending order.
-template <int FMT>
+// dw[k] = sum over p of part[p][k]: COLS columns a workgroup, its G = 1024 / COLS
+// groups of lanes every G-th row each, eight at a time, then their sums in
+// ascending order.  Few columns leave more workgroups for short rows.
+template <int FMT, int COLS>
 __global__ __launch_bounds__(1024) void rms_norm_dw_kernel(const float* part, int64_t parts, int64_t K, void* dw) {
-  __shared__ float sums[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t k = (int64_t)blockIdx.x * 64 + lane;
+  constexpr int G = 1024 / COLS;
+  __shared__ float sums[G][COLS];
+  const int col = threadIdx.x % COLS, group = threadIdx.x / COLS;
+  const int64_t k = (int64_t)blockIdx.x * COLS + col;
   float s = 0.0f;
-  if (k < K)
-    for (int64_t p = wave; p < parts; p += 16) s += part[p * K + k];
-  sums[wave][lane] = s;
-  __syncthreads();
-  if (wave > 0 || k >= K) return;
+  if (k < K) {
+    for (int64_t p = group; p < parts; p += G * 8) {
+      float v[8];
 #pragma unroll
-  for (int i = 1; i < 16; ++i) s += sums[i][lane];
+      for (int i = 0; i < 8; ++i) v[i] = p + G * i < parts ? gload<float>(part + (p + G * i) * K + k) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+  }
+  sums[group][col] = s;
+  __syncthreads();
+  if (group > 0 || k >= K) return;
+#pragma unroll
+  for (int i = 1; i < G; ++i) s += sums[i][col];
   if constexpr (FMT == MX_F32)
     ((float*)dw)[k] = s;
   else

@@ -18,12 +18,10 @@ quantize_f8(x.t()).
 
 A stream by argument: as the package says.
 """
-import ctypes
-
 import torch
 
-from ._lib import F8sArgs, lib
-from .mx4 import FORMATS, _call, _check_stream, _keep, _new
+from ._lib import F8sArgs, F8sQuantizeArgs, lib, packer
+from .mx4 import FORMATS, _call, _check_stream, _keep, _new2
 
 BLOCK = 128
 FORMATS8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
@@ -33,13 +31,14 @@ VARIANTS = {name: i for i, name in enumerate(("auto", "strip16x16", "strip16x32"
                                               "strip64x64", "tile64x128", "tile128x128", "tile256x128", "tile256x256"))}
 
 _c_quantize, _c_product = lib.gemm_f8s_quantize, lib.gemm_f8s
+_quantize_args, _product_args = packer(F8sQuantizeArgs), packer(F8sArgs)
 
 
 def _new_f8(R, K, dtype, device, stream):
     """[R, K] in 8 bits whose rows start 16-byte aligned, as the products want
     them."""
     pitch = -(-K // 16) * 16
-    data = _new((R, pitch), dtype, device, stream)
+    data = _new2(R, pitch, dtype, device, stream)
     return data if pitch == K else data[:, :K]
 
 
@@ -68,9 +67,9 @@ def quantize_f8(x, rows=1, dtype=torch.float8_e4m3fn, out=None, stream=None):
         raise TypeError("expected float16, bfloat16 or float32")
     if fmt8 is None:
         raise TypeError("dtype must be float8_e4m3fn or float8_e5m2")
-    if x.ndim != 2 or not x.is_cuda:
+    if x.ndim != 2 or device.type != "cuda":
         raise ValueError("expected an [R, K] matrix on a GPU")
-    if rows not in (1, BLOCK):
+    if rows != 1 and rows != BLOCK:
         raise ValueError("blocks have 1 or 128 rows")
     R, K = x.shape
     sr, sk = x.stride()
@@ -81,26 +80,19 @@ def quantize_f8(x, rows=1, dtype=torch.float8_e4m3fn, out=None, stream=None):
     if stream is not None:
         _check_stream(stream, device)
     if out is None:
+        blocks = -(-K // BLOCK)
         data = _new_f8(R, K, dtype, device, stream)
-        scales = _new((R if rows == 1 else -(-R // BLOCK), -(-K // BLOCK)), torch.float32, device, stream)
+        scales = _new2(R if rows == 1 else -(-R // BLOCK), blocks, torch.float32, device, stream)
+        pitch, ss_r, ss_k = -(-K // 16) * 16, blocks, 1
     else:
         data, scales = out
         _check_f8_out(data, scales, dtype, device, R, K, rows)
-    _call(device, stream, _c_quantize, x.data_ptr(), fmt, sr, sk, R, K, rows, data.data_ptr(), fmt8,
-          data.stride(0) if R > 1 else K, scales.data_ptr(), *scales.stride())
+        pitch, (ss_r, ss_k) = data.stride(0) if R > 1 else K, scales.stride()
+    _call(device, stream, _c_quantize, _quantize_args(x.data_ptr(), sr, sk, R, K, data.data_ptr(), pitch,
+                                                      scales.data_ptr(), ss_r, ss_k, fmt, fmt8, rows))
     if stream is not None:
         _keep(stream, x, data, scales)
     return data, scales
-
-
-def _rows8(t, scales, name):
-    """Checks of an operand's rows; its format."""
-    fmt = FORMATS8.get(t.dtype)
-    if fmt is None or scales.dtype != torch.float32:
-        raise TypeError(f"{name} must be float8_e4m3fn or float8_e5m2 with float32 scales")
-    if t.ndim != 2 or scales.ndim != 2:
-        raise ValueError(f"expected matrices {name} and {name}_scales")
-    return fmt
 
 
 def gemm_f8_scaled(a, a_scales, b, b_scales, out=None, dtype=None, variant="auto", stream=None):
@@ -119,8 +111,11 @@ def gemm_f8_scaled(a, a_scales, b, b_scales, out=None, dtype=None, variant="auto
 
     variant: a kernel by its tile (VARIANTS), for measurements; all compute the
     same."""
-    fmt_a, fmt_b = _rows8(a, a_scales, "a"), _rows8(b, b_scales, "b")
-    device = a.device
+    fmt_a, fmt_b, device = FORMATS8.get(a.dtype), FORMATS8.get(b.dtype), a.device
+    if fmt_a is None or fmt_b is None or a_scales.dtype != torch.float32 or b_scales.dtype != torch.float32:
+        raise TypeError("a and b must be float8_e4m3fn or float8_e5m2, with float32 scales")
+    if a.ndim != 2 or b.ndim != 2 or a_scales.ndim != 2 or b_scales.ndim != 2:
+        raise ValueError("expected matrices a, a_scales, b and b_scales")
     if device.type != "cuda" or b.device != device or a_scales.device != device or b_scales.device != device:
         raise ValueError("inputs must share one GPU device")
     if stream is not None:
@@ -141,7 +136,7 @@ def gemm_f8_scaled(a, a_scales, b, b_scales, out=None, dtype=None, variant="auto
         dtype = dtype or torch.bfloat16
         if dtype not in FORMATS:
             raise TypeError("dtype must be float16, bfloat16 or float32")
-        out, ldc = _new((M, N), dtype, device, stream), N
+        out, ldc = _new2(M, N, dtype, device, stream), N
     else:
         if out.dtype not in FORMATS or (dtype is not None and out.dtype != dtype):
             raise TypeError("out must be float16, bfloat16 or float32, and of dtype where that is given")
@@ -149,10 +144,10 @@ def gemm_f8_scaled(a, a_scales, b, b_scales, out=None, dtype=None, variant="auto
                 (out.stride(0) < N and M > 1):
             raise ValueError("out must be a row-major [M, N] tensor on the inputs' device")
         ldc = out.stride(0) if M > 1 else N
-    args = F8sArgs(a.data_ptr(), lda, a_scales.data_ptr(), *sa, b.data_ptr(), ldb, b_scales.data_ptr(), *sb,
-                   out.data_ptr(), ldc, M, N, K, fmt_a, fmt_b, 1 if brows == N else BLOCK, FORMATS[out.dtype],
-                   VARIANTS[variant])
-    _call(device, stream, _c_product, ctypes.byref(args))
+    _call(device, stream, _c_product,
+          _product_args(a.data_ptr(), lda, a_scales.data_ptr(), *sa, b.data_ptr(), ldb, b_scales.data_ptr(), *sb,
+                        out.data_ptr(), ldc, M, N, K, fmt_a, fmt_b, 1 if brows == N else BLOCK, FORMATS[out.dtype],
+                        VARIANTS[variant]))
     if stream is not None:
         _keep(stream, a, a_scales, b, b_scales, out)
     return out

@@ -69,6 +69,16 @@ def _new(shape, dtype, device, stream):
     return t
 
 
+_empty = torch.empty
+
+
+def _new2(rows, cols, dtype, device, stream):
+    """_new of a matrix (its sizes by position: 0.4 us less than as a tuple)."""
+    if stream is None:
+        return _empty(rows, cols, dtype=dtype, device=device)
+    return _new((rows, cols), dtype, device, stream)
+
+
 def _workspace(nbytes, device, stream):
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)

@@ -34,9 +34,18 @@ extern "C" {
  * A block that holds an infinity or a NaN gets a NaN scale and zero elements.
  * Nothing past a row's K bytes is written.
  */
-int gemm_f8s_quantize(const void* X, int32_t fmt, int64_t ldx_r, int64_t ldx_k, int64_t R, int64_t K,
-                      int32_t block_rows, void* data, int32_t fmt8, int64_t ldd, float* scales, int64_t lds_r,
-                      int64_t lds_k, void* stream);
+typedef struct gemm_f8s_quantize_args {
+  const void* X;
+  int64_t ldx_r, ldx_k;
+  int64_t R, K;
+  void* data;
+  int64_t ldd;
+  float* scales;
+  int64_t lds_r, lds_k;
+  int32_t fmt, fmt8, block_rows;
+} gemm_f8s_quantize_args;
+
+int gemm_f8s_quantize(const gemm_f8s_quantize_args* args, void* stream);
 
 /*
  * C[m,n] := sum_k A[m,k] B[n,k] (values with their scales), float32 sums, C of

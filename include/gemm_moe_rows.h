@@ -33,9 +33,16 @@ extern "C" {
  * Needs gemm_moe_sort_workspace_bytes(T, top_k, E) bytes of workspace (may be 0),
  * 256-byte aligned; with workspace == NULL they are allocated in stream order.
  */
-int gemm_moe_sort(const void* experts, int32_t id_bytes, int64_t ld, int64_t T, int32_t top_k, int32_t E,
-                  int64_t* offsets, int64_t* rows, int64_t* slots, void* stream, void* workspace,
-                  size_t workspace_bytes);
+typedef struct gemm_moe_sort_args {
+  const void* experts;
+  int64_t ld, T;
+  int64_t* offsets;
+  int64_t* rows;
+  int64_t* slots;
+  int32_t id_bytes, top_k, E;
+} gemm_moe_sort_args;
+
+int gemm_moe_sort(const gemm_moe_sort_args* args, void* stream, void* workspace, size_t workspace_bytes);
 size_t gemm_moe_sort_workspace_bytes(int64_t T, int32_t top_k, int32_t E);
 
 /*
@@ -43,27 +50,58 @@ size_t gemm_moe_sort_workspace_bytes(int64_t T, int32_t top_k, int32_t E);
  * are zeros.  X [T, H], Y [P, H] of elements of elem_bytes (1, 2 or 4), unit
  * stride along H, row strides in elements.
  */
-int gemm_moe_gather(const void* X, int64_t ldx, int32_t elem_bytes, const int64_t* offsets, const int64_t* slots,
-                    int32_t E, void* Y, int64_t ldy, int64_t T, int32_t top_k, int64_t H, void* stream);
+typedef struct gemm_moe_gather_args {
+  const void* X;
+  int64_t ldx;
+  const int64_t* offsets;
+  const int64_t* slots;
+  void* Y;
+  int64_t ldy, T, H;
+  int32_t elem_bytes, E, top_k;
+} gemm_moe_gather_args;
+
+int gemm_moe_gather(const gemm_moe_gather_args* args, void* stream);
 
 /*
  * Y[t] := sum over j with a slot of weights[t*ldw + j] X[slots[t,j]], X [P, H] and
  * Y [T, H] of format fmt, weights of fmt_w (GEMM_FMT_F32 or fmt), or 1 with
  * weights == NULL (which is gather's gradient).
  */
-int gemm_moe_combine(const void* X, int64_t ldx, int32_t fmt, const int64_t* slots, const void* weights,
-                     int32_t fmt_w, int64_t ldw, void* Y, int64_t ldy, int64_t T, int32_t top_k, int64_t H,
-                     void* stream);
+typedef struct gemm_moe_combine_args {
+  const void* X;
+  int64_t ldx;
+  const int64_t* slots;
+  const void* weights;
+  int64_t ldw;
+  void* Y;
+  int64_t ldy, T, H;
+  int32_t fmt, fmt_w, top_k;
+} gemm_moe_combine_args;
+
+int gemm_moe_combine(const gemm_moe_combine_args* args, void* stream);
 
 /*
  * Gradients of gemm_moe_combine's X and weights, given those of its Y (DY [T, H]):
  *     DX[slots[t,j]] := weights[t,j] DY[t]; its rows from offsets[E] on are zeros
  *     DW[t*lddw + j] := sum_h DY[t,h] X[slots[t,j],h], 0 without a slot (of fmt_w)
  */
-int gemm_moe_combine_backward(const void* DY, int64_t lddy, const void* X, int64_t ldx, int32_t fmt,
-                              const int64_t* offsets, const int64_t* slots, int32_t E, const void* weights,
-                              int32_t fmt_w, int64_t ldw, void* DX, int64_t lddx, void* DW, int64_t lddw, int64_t T,
-                              int32_t top_k, int64_t H, void* stream);
+typedef struct gemm_moe_combine_backward_args {
+  const void* DY;
+  int64_t lddy;
+  const void* X;
+  int64_t ldx;
+  const int64_t* offsets;
+  const int64_t* slots;
+  const void* weights;
+  int64_t ldw;
+  void* DX;
+  int64_t lddx;
+  void* DW;
+  int64_t lddw, T, H;
+  int32_t fmt, fmt_w, E, top_k;
+} gemm_moe_combine_backward_args;
+
+int gemm_moe_combine_backward(const gemm_moe_combine_backward_args* args, void* stream);
 
 #ifdef __cplusplus
 }

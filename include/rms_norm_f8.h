@@ -25,9 +25,24 @@ extern "C" {
  * w: K elements of fmt_w, GEMM_FMT_F32 or fmt.  H may be X or the residual
  * itself, at the same row stride; nothing else overlaps.
  */
-int gemm_rms_norm_f8(const void* X, int64_t ldx, const void* residual, int64_t ldr, int32_t fmt, const void* W,
-                     int32_t fmt_w, float eps, void* H, int64_t ldh, void* data, int32_t fmt8, int64_t ldd,
-                     float* scales, int64_t lds_r, int64_t lds_k, int64_t R, int64_t K, void* stream);
+typedef struct gemm_rms_norm_f8_args {
+  const void* X;
+  int64_t ldx;
+  const void* residual;
+  int64_t ldr;
+  const void* W;
+  void* H;
+  int64_t ldh;
+  void* data;
+  int64_t ldd;
+  float* scales;
+  int64_t lds_r, lds_k;
+  int64_t R, K;
+  float eps;
+  int32_t fmt, fmt_w, fmt8;
+} gemm_rms_norm_f8_args;
+
+int gemm_rms_norm_f8(const gemm_rms_norm_f8_args* args, void* stream);
 
 /*
  * Gradients of h and w, given those of y (DY) and, from the residual stream, of
@@ -38,9 +53,24 @@ int gemm_rms_norm_f8(const void* X, int64_t ldx, const void* residual, int64_t l
  * Needs gemm_rms_norm_backward_workspace_bytes(R, K) bytes of workspace, 256-byte
  * aligned; with workspace == NULL they are allocated in stream order.
  */
-int gemm_rms_norm_backward(const void* DY, int64_t ldy, const void* H, int64_t ldh, int32_t fmt, const void* W,
-                           int32_t fmt_w, float eps, const void* DH, int64_t lddh, void* DX, int64_t lddx, void* DW,
-                           int64_t R, int64_t K, void* stream, void* workspace, size_t workspace_bytes);
+typedef struct gemm_rms_norm_backward_args {
+  const void* DY;
+  int64_t ldy;
+  const void* H;
+  int64_t ldh;
+  const void* W;
+  const void* DH;
+  int64_t lddh;
+  void* DX;
+  int64_t lddx;
+  void* DW;
+  int64_t R, K;
+  float eps;
+  int32_t fmt, fmt_w;
+} gemm_rms_norm_backward_args;
+
+int gemm_rms_norm_backward(const gemm_rms_norm_backward_args* args, void* stream, void* workspace,
+                           size_t workspace_bytes);
 size_t gemm_rms_norm_backward_workspace_bytes(int64_t R, int64_t K);
 
 #ifdef __cplusplus

@@ -39,7 +39,8 @@ def test_headers_compile_as_c(tmp_path):
 
 
 def quantize(X=P[0], fmt=1, sr=300, sk=1, R=4, K=300, rows=1, data=P[1], fmt8=0, ldd=304, scales=P[2], ss_r=3, ss_k=1):
-    return g.lib.gemm_f8s_quantize(X, fmt, sr, sk, R, K, rows, data, fmt8, ldd, scales, ss_r, ss_k, None)
+    return g.lib.gemm_f8s_quantize(ctypes.byref(_lib.F8sQuantizeArgs(X, sr, sk, R, K, data, ldd, scales, ss_r, ss_k, fmt,
+                                                                    fmt8, rows)), None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -78,14 +79,49 @@ def test_product_refusals(kw, code):
     assert product(**kw) == code
 
 
-def test_product_refuses_no_arguments_at_all():
-    assert g.lib.gemm_f8s(None, None) == -1
+@pytest.mark.parametrize("name", ["gemm_f8s", "gemm_f8s_quantize", "gemm_rms_norm_f8", "gemm_moe_gather",
+                                  "gemm_moe_combine", "gemm_moe_combine_backward"])
+def test_no_arguments_at_all(name):
+    assert getattr(g.lib, name)(None, None) == -1
+
+
+@pytest.mark.parametrize("name", ["gemm_rms_norm_backward", "gemm_moe_sort"])
+def test_no_arguments_at_all_with_workspace(name):
+    assert getattr(g.lib, name)(None, None, 0, 0) == -1
+
+
+@pytest.mark.parametrize("cls", [_lib.F8sArgs, _lib.F8sQuantizeArgs, _lib.NormArgs, _lib.NormBackwardArgs, _lib.SortArgs,
+                                 _lib.GatherArgs, _lib.CombineArgs, _lib.CombineBackwardArgs])
+def test_packed_arguments_are_the_structure(cls):
+    values = [float(i) if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(cls._fields_)]
+    packed = _lib.packer(cls)(*values)
+    assert packed == bytes(cls(*values))
+
+
+def test_structures_have_the_headers_sizes(tmp_path):
+    names = {"gemm_f8s_args": _lib.F8sArgs, "gemm_f8s_quantize_args": _lib.F8sQuantizeArgs,
+             "gemm_rms_norm_f8_args": _lib.NormArgs, "gemm_rms_norm_backward_args": _lib.NormBackwardArgs,
+             "gemm_moe_sort_args": _lib.SortArgs, "gemm_moe_gather_args": _lib.GatherArgs,
+             "gemm_moe_combine_args": _lib.CombineArgs, "gemm_moe_combine_backward_args": _lib.CombineBackwardArgs}
+    lines = ["#include <stddef.h>", "#include <stdio.h>", '#include "rms_norm_f8.h"', '#include "gemm_moe_rows.h"',
+             "int main(void) {"]
+    for name, cls in names.items():
+        lines.append(f'printf("%zu\\n", sizeof({name}));')
+        lines += [f'printf("%zu\\n", offsetof({name}, {f}));' for f, _ in cls._fields_]
+    src = tmp_path / "sizes.c"
+    src.write_text("\n".join(lines + ["return 0; }"]))
+    subprocess.run(["gcc", "-std=c99", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(tmp_path / "sizes")], check=True)
+    out = subprocess.run([str(tmp_path / "sizes")], capture_output=True, text=True, check=True).stdout.split()
+    want = []
+    for cls in names.values():
+        want += [ctypes.sizeof(cls)] + [getattr(cls, f).offset for f, _ in cls._fields_]
+    assert [int(v) for v in out] == want
 
 
 def norm(X=P[0], ldx=300, res=P[1], ldr=300, fmt=1, W=P[2], fmt_w=2, eps=1e-6, H=P[3], ldh=300, data=P[4], fmt8=0,
          ldd=304, scales=P[5], ss_r=3, ss_k=1, R=4, K=300):
-    return g.lib.gemm_rms_norm_f8(X, ldx, res, ldr, fmt, W, fmt_w, eps, H, ldh, data, fmt8, ldd, scales, ss_r, ss_k, R,
-                                  K, None)
+    return g.lib.gemm_rms_norm_f8(ctypes.byref(_lib.NormArgs(X, ldx, res, ldr, W, H, ldh, data, ldd, scales, ss_r, ss_k,
+                                                             R, K, eps, fmt, fmt_w, fmt8)), None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -104,7 +140,8 @@ def test_norm_refusals(kw, code):
 
 def norm_back(DY=P[0], ldy=300, H=P[1], ldh=300, fmt=1, W=P[2], fmt_w=1, eps=1e-6, DH=P[3], lddh=300, DX=P[4], lddx=300,
               DW=P[5], R=4, K=300, ws=0, nws=0):
-    return g.lib.gemm_rms_norm_backward(DY, ldy, H, ldh, fmt, W, fmt_w, eps, DH, lddh, DX, lddx, DW, R, K, None, ws, nws)
+    return g.lib.gemm_rms_norm_backward(ctypes.byref(_lib.NormBackwardArgs(DY, ldy, H, ldh, W, DH, lddh, DX, lddx, DW, R,
+                                                                           K, eps, fmt, fmt_w)), None, ws, nws)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -122,7 +159,7 @@ def test_norm_backward_refusals(kw, code):
 
 
 def sort(ids=P[0], size=8, ld=2, T=4, k=2, E=4, off=P[1], rows=P[2], slots=P[3], ws=0, nws=0):
-    return g.lib.gemm_moe_sort(ids, size, ld, T, k, E, off, rows, slots, None, ws, nws)
+    return g.lib.gemm_moe_sort(ctypes.byref(_lib.SortArgs(ids, ld, T, off, rows, slots, size, k, E)), None, ws, nws)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -139,7 +176,7 @@ def test_sort_refusals(kw, code):
 
 
 def gather(X=P[0], ldx=8, size=2, off=P[1], slots=P[2], E=4, Y=P[3], ldy=8, T=4, k=2, H=8):
-    return g.lib.gemm_moe_gather(X, ldx, size, off, slots, E, Y, ldy, T, k, H, None)
+    return g.lib.gemm_moe_gather(ctypes.byref(_lib.GatherArgs(X, ldx, off, slots, Y, ldy, T, H, size, E, k)), None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -152,7 +189,7 @@ def test_gather_refusals(kw, code):
 
 
 def combine(X=P[0], ldx=8, fmt=1, slots=P[1], w=P[2], fmt_w=2, ldw=2, Y=P[3], ldy=8, T=4, k=2, H=8):
-    return g.lib.gemm_moe_combine(X, ldx, fmt, slots, w, fmt_w, ldw, Y, ldy, T, k, H, None)
+    return g.lib.gemm_moe_combine(ctypes.byref(_lib.CombineArgs(X, ldx, slots, w, ldw, Y, ldy, T, H, fmt, fmt_w, k)), None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -166,8 +203,8 @@ def test_combine_refusals(kw, code):
 
 def combine_back(DY=P[0], lddy=8, X=P[1], ldx=8, fmt=1, off=P[2], slots=P[3], E=4, w=P[4], fmt_w=2, ldw=2, DX=P[5],
                  lddx=8, DW=P[6], lddw=2, T=4, k=2, H=8):
-    return g.lib.gemm_moe_combine_backward(DY, lddy, X, ldx, fmt, off, slots, E, w, fmt_w, ldw, DX, lddx, DW, lddw, T, k,
-                                           H, None)
+    return g.lib.gemm_moe_combine_backward(ctypes.byref(_lib.CombineBackwardArgs(
+        DY, lddy, X, ldx, off, slots, w, ldw, DX, lddx, DW, lddw, T, H, fmt, fmt_w, E, k)), None)
 
 
 @pytest.mark.parametrize("kw,code", [
