@@ -23,6 +23,12 @@
 //          row lane % 16 of C, so one multiplication gives the scale of a row
 //          and a block of columns, and 8 or 16 consecutive bytes are stored.
 //
+// What this is bound by is the wait for LDS behind each barrier, so where the LDS
+// holds two workgroups a compute unit takes two, whose barriers do not coincide:
+// the 128 x 128 tile is four waves of 64 x 64 and two stages, 2048 x 7168 x 8192
+// in 151 us (square blocks) and 176 (row blocks); eight waves of 32 x 64 with four
+// stages took 206 and 250, a 256 x 128 tile alone on its unit 167 and 187.
+//
 // A partial block at the end is a step like the others, its bytes behind K
 // cleared in the registers on both sides; rows past M or N read the last valid
 // row and are never stored.
@@ -31,7 +37,8 @@
 // 8, aligned to the group's largest and cut 2^-13 below it (measured; the older
 // and the newer ones alike), which leaves sums of 1 to 3 in 10^5 of their
 // size: far below a 16-bit result's last place, but not a float32 one's.  Those go
-// through binary16, which holds every 8-bit value, at half the rate.
+// through binary16, which holds every 8-bit value, at half the rate: 264 us
+// (910 TFLOP/s; 216 on zeros, so the power it takes counts too).
 #pragma once
 
 #include "f8_kernel.hpp"
@@ -67,6 +74,7 @@ struct F8sCfg {
   static constexpr int S_BYTES = SI * NW * 256;
   static constexpr int SB_AT = (BM + 63) / 64 * 256;         // B's scales behind A's
   static constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES, LDS = STAGES * STAGE;
+  static constexpr int PER_CU = LDS <= 80 * 1024 ? 2 : 1, WAVES = PER_CU * NW / 4;   // workgroups a CU, waves a SIMD
   static constexpr int DMA_A = A_BYTES / 1024, DMA_B = B_BYTES / 1024;   // instructions of the workgroup
   static constexpr int DI = (DMA_A + DMA_B) / NW;                        // per wave
   static constexpr int BATCH = DI % 4 == 0 ? 4 : 2, BATCHES = DI / BATCH;
@@ -189,55 +197,49 @@ __device__ __forceinline__ int tail_chunk(int c, int rem) { return 16 * c < rem 
 // 16 rows, 16 rows reading one chunk fall on distinct banks.
 __device__ __forceinline__ int f16r(int r) { return (r ^ (r >> 3 & 1)) & 7; }
 
-template <class CF, int FA, int FB, bool ROWB, bool WIDE>
-__global__ __launch_bounds__(CF::NT) void f8s_tile_kernel(F8sArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[CF::LDS];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / CF::WN, wn = wave % CF::WN;
-  const int lr = lane & 15, g = lane >> 4;
-
-  int64_t pm, pn;
-  raster_tile(blockIdx.x, a.GM, a.GN, a.panel, pm, pn);
-  const int64_t m0 = pm * CF::BM, n0 = pn * CF::BN;
-  const int nf = (int)(a.K / 128);                // whole blocks
-  const int rem = (int)(a.K - (int64_t)nf * 128);
-  const int nb = nf + (rem > 0);
-
-  // This wave's DMA instructions of a step: DI of 8 rows, A's first, in batches of
-  // one operand, then SI of 64 scales, A's first (the last may be one too many: it
-  // repeats B's rows).  Uniform bases, and 32-bit offsets of the lanes.
+// A wave's LDS-DMA of a step: DI instructions of 8 rows, A's first, in batches of
+// one operand, then SI of 64 scales, A's first (the last may be one too many: it
+// repeats B's rows).  Uniform bases, and 32-bit offsets of the lanes.
+template <class CF>
+struct F8sFeed {
   const char* src[CF::BATCHES];
   uint32_t off[CF::DI];
   const char* ssrc[CF::SI];
   uint32_t soff[CF::SI];
   int64_t sstep[CF::SI];
-  auto chunk = [&](int i) { return (lane % 8) ^ f16r((wave * CF::DI + i) * 8 + lane / 8); };
+  int wave, lane, nf, rem, nb, at;      // whole blocks, k behind them, blocks, blocks issued
+  uint32_t lds0;
+
+  __device__ __forceinline__ int chunk(int i) const { return (lane % 8) ^ f16r((wave * CF::DI + i) * 8 + lane / 8); }
+
+  __device__ __forceinline__ F8sFeed(const F8sArgs& a, int64_t m0, int64_t n0, const char* smem, int wave_, int lane_)
+      : wave(wave_), lane(lane_), nf((int)(a.K / 128)), rem((int)(a.K % 128)), nb(nf + (rem > 0)), at(0),
+        lds0(__builtin_amdgcn_readfirstlane(lds_addr(smem))) {
 #pragma unroll
-  for (int i = 0; i < CF::DI; ++i) {
-    const int q = wave * CF::DI + i;
-    const bool is_a = q < CF::DMA_A;
-    const int64_t r = (is_a ? q : q - CF::DMA_A) * 8 + lane / 8, left = (is_a ? a.M - m0 : a.N - n0) - 1;
-    if (i % CF::BATCH == 0) src[i / CF::BATCH] = uniform_ptr((is_a ? a.A + m0 * a.lda : a.B + n0 * a.ldb) - kSBias);
-    off[i] = (uint32_t)((r < left ? r : left) * (is_a ? a.lda : a.ldb) + (nf > 0 ? 16 * chunk(i) : tail_chunk(chunk(i), rem)) +
-                        kSBias - 1024 * (i % CF::BATCH));
-  }
+    for (int i = 0; i < CF::DI; ++i) {
+      const int q = wave * CF::DI + i;
+      const bool is_a = q < CF::DMA_A;
+      const int64_t r = (is_a ? q : q - CF::DMA_A) * 8 + lane / 8, left = (is_a ? a.M - m0 : a.N - n0) - 1;
+      if (i % CF::BATCH == 0) src[i / CF::BATCH] = uniform_ptr((is_a ? a.A + m0 * a.lda : a.B + n0 * a.ldb) - kSBias);
+      off[i] = (uint32_t)((r < left ? r : left) * (is_a ? a.lda : a.ldb) +
+                          (nf > 0 ? 16 * chunk(i) : tail_chunk(chunk(i), rem)) + kSBias - 1024 * (i % CF::BATCH));
+    }
 #pragma unroll
-  for (int i = 0; i < CF::SI; ++i) {
-    const int q = wave * CF::SI + i;
-    const bool is_a = q < (CF::BM + 63) / 64;
-    const int64_t last = (is_a ? a.M : a.N) - 1, row = is_a ? m0 + q * 64 : n0 + (q - (CF::BM + 63) / 64) * 64;
-    const int64_t r0 = row < last ? row : last, r1 = row + lane < last ? row + lane : last;
-    ssrc[i] = uniform_ptr((const char*)(is_a ? a.SA + r0 * a.sa_m : a.SB + (r0 >> a.shift) * a.sb_n));
-    soff[i] = (uint32_t)(4 * (is_a ? (r1 - r0) * a.sa_m : ((r1 >> a.shift) - (r0 >> a.shift)) * a.sb_n));
-    sstep[i] = 4 * (is_a ? a.sa_k : a.sb_k);
+    for (int i = 0; i < CF::SI; ++i) {
+      const int q = wave * CF::SI + i;
+      const bool is_a = q < (CF::BM + 63) / 64;
+      const int64_t last = (is_a ? a.M : a.N) - 1, row = is_a ? m0 + q * 64 : n0 + (q - (CF::BM + 63) / 64) * 64;
+      const int64_t r0 = row < last ? row : last, r1 = row + lane < last ? row + lane : last;
+      ssrc[i] = uniform_ptr((const char*)(is_a ? a.SA + r0 * a.sa_m : a.SB + (r0 >> a.shift) * a.sb_n));
+      soff[i] = (uint32_t)(4 * (is_a ? (r1 - r0) * a.sa_m : ((r1 >> a.shift) - (r0 >> a.shift)) * a.sb_n));
+      sstep[i] = 4 * (is_a ? a.sa_k : a.sb_k);
+    }
   }
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
-  // Step t into `slot`, from bases that advance with each call but the last
+
+  // The next step into `slot`, from bases that advance with each call but the last
   // block's (which is loaded again past the end, so that every step issues the
   // same number); ahead of a partial block the lanes' chunks are set for it.
-  int at = 0;
-  auto issue = [&](int slot) {
+  __device__ __forceinline__ void issue(int slot) {
     const uint32_t st = lds0 + slot * CF::STAGE;
 #pragma unroll
     for (int i = 0; i < CF::BATCHES; ++i)
@@ -255,7 +257,22 @@ __global__ __launch_bounds__(CF::NT) void f8s_tile_kernel(F8sArgs a) {
         for (int i = 0; i < CF::DI; ++i) off[i] += tail_chunk(chunk(i), rem) - 16 * chunk(i);
       }
     }
-  };
+  }
+};
+
+template <class CF, int FA, int FB, bool ROWB, bool WIDE>
+__global__ __launch_bounds__(CF::NT, CF::WAVES) void f8s_tile_kernel(F8sArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[CF::LDS];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / CF::WN, wn = wave % CF::WN;
+  const int lr = lane & 15, g = lane >> 4;
+
+  int64_t pm, pn;
+  raster_tile(blockIdx.x, a.GM, a.GN, a.panel, pm, pn);
+  const int64_t m0 = pm * CF::BM, n0 = pn * CF::BN;
+  F8sFeed<CF> feed(a, m0, n0, smem, wave, lane);
+  const int nf = feed.nf, rem = feed.rem, nb = feed.nb;
 
   // LDS addresses of stage 0: chunks g and g + 4 of row lr of a block of rows.
   const int c0 = (g ^ f16r(lr)) * 16, c1 = c0 ^ 64;
@@ -294,6 +311,35 @@ __global__ __launch_bounds__(CF::NT) void f8s_tile_kernel(F8sArgs a) {
       fm[j] = f8s_frag<WIDE, FA>(part(read(ra, j)));
       s[j] = *reinterpret_cast<const float*>(rsa + j * 64) * sb;
     }
+    if constexpr (WIDE) {
+      // Four instructions to a sum: those of a block of B's units in turn, so that
+      // none waits for the one before it.
+      f32x4 d[2][CF::FM], sn[2];
+      auto add = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < CF::FM; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i][j][e] = __builtin_fmaf(ROWB ? d[i & 1][j][e] * sn[i & 1][e] : d[i & 1][j][e], s[j], acc[i][j][e]);
+      };
+      fb = f8s_frag<WIDE, FB>(next);
+#pragma unroll
+      for (int i = 0; i < CF::FN; ++i) {
+        if (i + 1 < CF::FN) next = part(read(rb, i + 1));
+        if constexpr (ROWB) sn[i & 1] = *reinterpret_cast<const f32x4*>(rsb + i * 64 + 16 * g);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int j = 0; j < CF::FM; ++j)
+            d[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                fb.v[q], fm[j].v[q], q == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : d[i & 1][j], 0, 0, 0);
+        if (i > 0) add(i - 1);
+        if (i + 1 < CF::FN) fb = f8s_frag<WIDE, FB>(next);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      add(CF::FN - 1);
+      return;
+    }
     f32x4 d[LAG + 1], sn[2];
     if constexpr (ROWB) sn[0] = *reinterpret_cast<const f32x4*>(rsb + 16 * g);
 #pragma unroll
@@ -319,13 +365,13 @@ __global__ __launch_bounds__(CF::NT) void f8s_tile_kernel(F8sArgs a) {
   };
 
 #pragma unroll
-  for (int t = 0; t < CF::STAGES - 1; ++t) issue(t);
+  for (int t = 0; t < CF::STAGES - 1; ++t) feed.issue(t);
   int slot = 0;
   for (int t = 0; t < nb; ++t) {
     wait_vmcnt<(CF::STAGES - 2) * CF::PER_STEP>();    // this wave's part of step t landed,
     wait_lgkmcnt0();                                  // and its reads of step t - 1 returned
     wg_barrier();                                     // both of every wave's
-    issue(slot == 0 ? CF::STAGES - 1 : slot - 1);
+    feed.issue(slot == 0 ? CF::STAGES - 1 : slot - 1);
     __builtin_amdgcn_sched_barrier(0);
     if (rem > 0 && t == nf)
       compute(std::true_type{}, slot);

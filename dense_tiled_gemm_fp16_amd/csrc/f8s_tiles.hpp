@@ -23,13 +23,12 @@ using F8sS32x32 = F8sStrip<2, 2, 2, 8>;
 using F8sS64x32 = F8sStrip<4, 2, 1, 8>;
 using F8sS64x64 = F8sStrip<4, 4, 1, 8>;
 using F8sT64x128 = F8sCfg<64, 128, 2, 2, 3>;
-using F8sT128x128 = F8sCfg<128, 128, 4, 2, 4>;
-using F8sT256x128 = F8sCfg<256, 128, 4, 2, 3>;
+using F8sT128x128 = F8sCfg<128, 128, 2, 2, 2>;
 
 // A workgroup's share of C and of K (parts: its waves' blocks of K at a time), its
 // threads, how many fit a compute unit, and what it takes: per round of workgroups
-// `start` and `step` for each `parts` blocks of K, step_full where more than half
-// the compute units work at once, either `wide` times as long through binary16
+// `start` and `step_full` for each `parts` blocks of K, `step` in a round that at
+// most half of them fit into, either `wide` times as long through binary16
 // (us; fitted to times of calls in graphs, some of which stand at plan()).
 struct F8sShape {
   int rows, cols, parts, threads, per_cu;
@@ -41,7 +40,7 @@ constexpr F8sShape f8s_strip_shape(float start, float step, float step_full, flo
 }
 template <class CF>
 constexpr F8sShape f8s_tile_shape(float start, float step, float step_full, float wide) {
-  return F8sShape{CF::BM, CF::BN, 1, CF::NT, CF::LDS <= 80 * 1024 ? 2 : 1, start, step, step_full, wide};
+  return F8sShape{CF::BM, CF::BN, 1, CF::NT, CF::PER_CU, start, step, step_full, wide};
 }
 constexpr F8sShape kF8sShapes[] = {
     {},
@@ -50,10 +49,9 @@ constexpr F8sShape kF8sShapes[] = {
     f8s_strip_shape<F8sS32x16>(1.2f, 0.52f, 0.7f, 1.7f),
     f8s_strip_shape<F8sS32x32>(1.3f, 0.75f, 0.85f, 1.7f),
     f8s_strip_shape<F8sS64x32>(1.9f, 0.85f, 1.2f, 1.7f),
-    f8s_strip_shape<F8sS64x64>(3.2f, 1.1f, 1.6f, 2.4f),
-    f8s_tile_shape<F8sT64x128>(2.3f, 0.57f, 0.84f, 1.5f),
-    f8s_tile_shape<F8sT128x128>(2.3f, 0.72f, 0.81f, 1.6f),
-    f8s_tile_shape<F8sT256x128>(3.4f, 1.1f, 1.4f, 1.5f),
+    f8s_strip_shape<F8sS64x64>(3.2f, 1.1f, 1.6f, 1.75f),
+    f8s_tile_shape<F8sT64x128>(4.8f, 0.57f, 0.7f, 1.85f),
+    f8s_tile_shape<F8sT128x128>(5.0f, 0.88f, 1.13f, 1.8f),
     {F8sBig::BM, F8sBig::BN, 1, F8sBig::NT, 1, 5.3f, 1.2f, 1.7f, 1.0f},
 };
 constexpr int kF8sVariants = sizeof(kF8sShapes) / sizeof(kF8sShapes[0]);
@@ -87,7 +85,6 @@ const void* f8s_strip_fn(bool rowb, bool wide) {
       case GEMM_F8S_STRIP_64X64: return f8s_strip_fn<F8sS64x64, FA, FB>(rowb, wide);         \
       case GEMM_F8S_TILE_64X128: return f8s_tile_fn<F8sT64x128, FA, FB>(rowb, wide);         \
       case GEMM_F8S_TILE_128X128: return f8s_tile_fn<F8sT128x128, FA, FB>(rowb, wide);       \
-      case GEMM_F8S_TILE_256X128: return f8s_tile_fn<F8sT256x128, FA, FB>(rowb, wide);       \
       case GEMM_F8S_TILE_256X256:                                                            \
         if (rowb || wide) return nullptr;                                                    \
         return out == F8S_F16 ? (const void*)f8s_big_kernel<FA, FB, DT_F16>                  \

@@ -78,16 +78,16 @@ bool takes(const F8sArgs& a, int variant, bool wide) {
 //   1 x 2048 x 7168      16x16 5.6, 16x32 5.7
 //   32 x 7168 x 2048     16x32 6.4, 32x16 6.6, 32x32 4.6, 64x32 5.2
 //   64 x 7168 x 2048     32x32 8.1, 64x32 5.5, 64x64 6.9, tile 64x128 12.9
-//   128 x 2048 x 7168    16x32 12.4, 32x32 8.4, 64x32 10.2, 64x64 12.8
-//   512 x 2048 x 7168    64x32 23, 64x64 17, tiles 64x128 36, 128x128 47
-//   1024 x 2048 x 2048   64x64 12.4, tiles 64x128 13.3, 128x128 16.2
-//   2048 x 2048 x 7168   64x64 60, tiles 64x128 50, 128x128 49, 256x128 75
-//   2048 x 4096 x 4096   tiles 64x128 58, 128x128 58, 256x128 49, 256x256 47
-//   8192 x 2048 x 7168   189, 188, 158, 101
-//   32768 x 2048 x 7168  785, 777, 639, 414
-// Row blocks and float32, 2048 x 7168 x 8192: strips 64x64 436, tiles 64x128 331,
-// 128x128 347, 256x128 280; to bfloat16: 273, 246, 250, 187.  Over 60 random
-// sizes the choice took 3% longer than the best one in the mean, 15% at most.
+//   128 x 2048 x 7168    32x32 9.2, 64x32 10.5, 64x64 12.9, tile 64x128 36
+//   512 x 2048 x 7168    64x32 23, 64x64 17, tiles 64x128 35, 128x128 51
+//   1024 x 2048 x 2048   64x64 12.6, tiles 64x128 13.3, 128x128 18.2
+//   2048 x 2048 x 7168   64x64 59, tiles 64x128 47, 128x128 52, 256x256 76
+//   2048 x 4096 x 4096   64x64 72, tiles 64x128 55, 128x128 45, 256x256 46
+//   8192 x 2048 x 7168   64x64 226, tiles 64x128 176, 128x128 143, 256x256 98
+//   32768 x 2048 x 7168  256x256 410
+// Row blocks and float32: 2048 x 7168 x 8192 strips 64x64 322, tiles 64x128 309,
+// 128x128 264; 512 x 2048 x 7168 23, 50, 74.  Over 74 sizes, most of them random,
+// the choice took 3% longer than the best one in the mean, 18% at most.
 int plan(const F8sArgs& a, bool wide, int cus) {
   int best = 0;
   float least = 0.0f;
@@ -96,9 +96,10 @@ int plan(const F8sArgs& a, bool wide, int cus) {
     const F8sShape& s = kF8sShapes[v];
     const double wgs = (double)cdiv(a.M, s.rows) * (double)cdiv(a.N, s.cols);
     const double slots = (double)cus * s.per_cu;
-    const float rounds = (float)(int64_t)((wgs + slots - 1) / slots);
-    const float step = (wgs > slots / 2 ? s.step_full : s.step) * (wide ? s.wide : 1.0f);
-    const float t = rounds * (s.start + step * (float)cdiv(cdiv(a.K, kF8Block), s.parts));
+    const double full = (double)(int64_t)(wgs / slots), rest = wgs - full * slots;
+    const float n = (float)cdiv(cdiv(a.K, kF8Block), s.parts) * (wide ? s.wide : 1.0f);
+    const float t = (float)full * (s.start + s.step_full * n) +
+                    (rest > 0 ? s.start + (rest > slots / 2 ? s.step_full : s.step) * n : 0.0f);
     if (best == 0 || t < least) {
       best = v;
       least = t;

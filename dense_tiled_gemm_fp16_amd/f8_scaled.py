@@ -28,7 +28,7 @@ FORMATS8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 
 # Kernels that a call may be given to (enum gemm_f8s_variant).
 VARIANTS = {name: i for i, name in enumerate(("auto", "strip16x16", "strip16x32", "strip32x16", "strip32x32", "strip64x32",
-                                              "strip64x64", "tile64x128", "tile128x128", "tile256x128", "tile256x256"))}
+                                              "strip64x64", "tile64x128", "tile128x128", "tile256x256"))}
 
 _c_quantize, _c_product = lib.gemm_f8s_quantize, lib.gemm_f8s
 _quantize_args, _product_args = packer(F8sQuantizeArgs), packer(F8sArgs)

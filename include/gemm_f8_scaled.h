@@ -76,8 +76,7 @@ enum gemm_f8s_variant {
   GEMM_F8S_STRIP_64X64 = 6,
   GEMM_F8S_TILE_64X128 = 7,
   GEMM_F8S_TILE_128X128 = 8,
-  GEMM_F8S_TILE_256X128 = 9,
-  GEMM_F8S_TILE_256X256 = 10
+  GEMM_F8S_TILE_256X256 = 9
 };
 
 typedef struct gemm_f8s_args {

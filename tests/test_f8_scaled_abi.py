@@ -67,8 +67,8 @@ def product(**kw):
     (dict(M=0), -2), (dict(N=-1), -2), (dict(K=0), -2), (dict(K=2 ** 40, lda=2 ** 40, ldb=2 ** 40), -2),
     (dict(lda=2 ** 62), -2), (dict(ldc=2 ** 62), -2), (dict(lsa_m=2 ** 61), -2), (dict(lsb_k=2 ** 62), -2),
     (dict(fmt_a=2), -7), (dict(fmt_b=-1), -7), (dict(b_block_rows=2), -7), (dict(fmt_c=3), -7),
-    (dict(variant=-1), -7), (dict(variant=11), -7), (dict(variant=10, b_block_rows=1, lsb_n=3), -7),
-    (dict(variant=10, fmt_c=2, ldc=200), -7),
+    (dict(variant=-1), -7), (dict(variant=10), -7), (dict(variant=9, b_block_rows=1, lsb_n=3), -7),
+    (dict(variant=9, fmt_c=2, ldc=200), -7),
     (dict(lda=0), -3), (dict(lda=288), -3), (dict(ldb=288), -3), (dict(lsa_m=0), -3), (dict(lsa_k=0), -3),
     (dict(lsb_n=-3), -3), (dict(lsb_k=0), -3), (dict(ldc=199), -4),
     (dict(lda=300), -9), (dict(lda=2 ** 23 + 16), -9), (dict(ldb=2 ** 24), -9), (dict(lsa_m=2 ** 22), -9),
