@@ -204,7 +204,7 @@ __device__ __forceinline__ void store_bytes(char* p, u32x4 v, int64_t n) {
 template <int NT>
 __device__ __forceinline__ void clear_rest(const RowsArgs& a, int64_t t, int64_t bytes, int64_t c0, int64_t c1) {
   int64_t n = *a.placed;
-  if (n < 0) n = 0;
+  n = n < 0 ? 0 : n < a.P ? n : a.P;     // a caller's offsets may hold anything
   for (int j = 0; j < a.top_k; ++j) {
     const int64_t r = n + t * a.top_k + j;
     if (r >= a.P) return;
