@@ -272,7 +272,7 @@ __global__ __launch_bounds__(CF::NT, CF::WAVES) void f8s_tile_kernel(F8sArgs a) 
   raster_tile(blockIdx.x, a.GM, a.GN, a.panel, pm, pn);
   const int64_t m0 = pm * CF::BM, n0 = pn * CF::BN;
   F8sFeed<CF> feed(a, m0, n0, smem, wave, lane);
-  const int nf = feed.nf, rem = feed.rem, nb = feed.nb;
+  const int nf = feed.nf, rem = feed.rem;
 
   // LDS addresses of stage 0: chunks g and g + 4 of row lr of a block of rows.
   const int c0 = (g ^ f16r(lr)) * 16, c1 = c0 ^ 64;
@@ -367,17 +367,20 @@ __global__ __launch_bounds__(CF::NT, CF::WAVES) void f8s_tile_kernel(F8sArgs a) 
 #pragma unroll
   for (int t = 0; t < CF::STAGES - 1; ++t) feed.issue(t);
   int slot = 0;
-  for (int t = 0; t < nb; ++t) {
+  for (int t = 0; t < nf; ++t) {
     wait_vmcnt<(CF::STAGES - 2) * CF::PER_STEP>();    // this wave's part of step t landed,
     wait_lgkmcnt0();                                  // and its reads of step t - 1 returned
     wg_barrier();                                     // both of every wave's
     feed.issue(slot == 0 ? CF::STAGES - 1 : slot - 1);
     __builtin_amdgcn_sched_barrier(0);
-    if (rem > 0 && t == nf)
-      compute(std::true_type{}, slot);
-    else
-      compute(std::false_type{}, slot);
+    compute(std::false_type{}, slot);
     slot = slot == CF::STAGES - 1 ? 0 : slot + 1;
+  }
+  if (rem > 0) {     // behind the loop: within it the running sums would change registers
+    wait_vmcnt<(CF::STAGES - 2) * CF::PER_STEP>();
+    wait_lgkmcnt0();
+    wg_barrier();
+    compute(std::true_type{}, slot);
   }
   wait_vmcnt<0>();       // no LDS transfer may outlive the workgroup
 
