@@ -118,7 +118,7 @@ __global__ __launch_bounds__(CF::NT) void f8s_strip_kernel(F8sArgs a) {
   for (int q = 1; q < CF::D; ++q)
     if (q < nq) issue(block(q), q);
   int slot = 0;
-  for (int64_t q = 0; q < nq; ++q) {
+  auto step = [&](auto tail_tag, int64_t q) {
     // Blocks behind this one that are in flight: D - 1, fewer at the end.
     const int64_t left = nq - 1 - q;
     if (CF::D >= 4 && left >= 3)
@@ -129,14 +129,14 @@ __global__ __launch_bounds__(CF::NT) void f8s_strip_kernel(F8sArgs a) {
       wait_vmcnt<CF::PER_STEP>();
     else
       wait_vmcnt<0>();
-    if (q < (int64_t)tail)
-      compute(std::true_type{}, slot);
-    else
-      compute(std::false_type{}, slot);
+    compute(tail_tag, slot);
     wait_lgkmcnt0();               // read, so that the stage may be loaded again
     if (q + CF::D < nq) issue(block(q + CF::D), slot);
     slot = slot == CF::D - 1 ? 0 : slot + 1;
-  }
+  };
+  // The partial block ahead of the loop: within it the running sums would change registers.
+  if (tail) step(std::true_type{}, 0);
+  for (int64_t q = tail; q < nq; ++q) step(std::false_type{}, q);
 
   // The waves' sums: [wave][i][j][lane], then each 16 x 16 block's by one wave.
   __syncthreads();

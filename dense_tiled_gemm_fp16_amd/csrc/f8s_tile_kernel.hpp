@@ -23,11 +23,13 @@
 //          row lane % 16 of C, so one multiplication gives the scale of a row
 //          and a block of columns, and 8 or 16 consecutive bytes are stored.
 //
-// What this is bound by is the wait for LDS behind each barrier, so where the LDS
-// holds two workgroups a compute unit takes two, whose barriers do not coincide:
-// the 128 x 128 tile is four waves of 64 x 64 and two stages, 2048 x 7168 x 8192
-// in 151 us (square blocks) and 176 (row blocks); eight waves of 32 x 64 with four
-// stages took 206 and 250, a 256 x 128 tile alone on its unit 167 and 187.
+// What bounds it: a step's data, which two stages give one step's time to arrive,
+// and for float32 results the vector unit's instructions (256 beside 64 matrix
+// instructions of 16 cycles).  Where the LDS holds two workgroups a compute unit
+// takes two, whose barriers do not coincide: the 128 x 128 tile is four waves of
+// 64 x 64 and two stages, 2048 x 7168 x 8192 in 138 us (1740 TFLOP/s; square
+// blocks) and 165 (row blocks).  Eight waves of 32 x 64 with four stages took 206
+// and 250, a 256 x 128 tile alone on its unit 167 and 187.
 //
 // A partial block at the end is a step like the others, its bytes behind K
 // cleared in the registers on both sides; rows past M or N read the last valid
@@ -37,8 +39,9 @@
 // 8, aligned to the group's largest and cut 2^-13 below it (measured; the older
 // and the newer ones alike), which leaves sums of 1 to 3 in 10^5 of their
 // size: far below a 16-bit result's last place, but not a float32 one's.  Those go
-// through binary16, which holds every 8-bit value, at half the rate: 264 us
-// (910 TFLOP/s; 216 on zeros, so the power it takes counts too).
+// through binary16, which holds every 8-bit value, at half the rate: 248 us
+// (970 TFLOP/s; 200 on zeros, so the power it takes counts too).  Matrix
+// instructions of 32 x 32 with their longer sums did not fit the registers.
 #pragma once
 
 #include "f8_kernel.hpp"
