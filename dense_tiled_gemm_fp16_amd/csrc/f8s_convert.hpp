@@ -17,11 +17,14 @@
 //   rows   blocks of one row, k contiguous: a lane takes 8 consecutive elements
 //          (one 16-byte load of a 16-bit type), 16 neighbouring lanes a block,
 //          whose maximum goes round them by four lane exchanges in registers.
-//          A wave has four such loads in flight; short rows share them.
+//          A wave has four such loads in flight; short rows share them.  32768 x
+//          7168 bfloat16 110 us (6.4 TB/s), 8192 x 7168 35.
 //   tiles  blocks of 128 rows x 128 elements, or of one row where k is strided: a
 //          workgroup takes 128 x 128 elements, a thread 8 x 8 of them, loaded
 //          along the contiguous axis.  Rows of k-strided input leave through LDS
-//          so that stores are whole lines.
+//          so that stores are whole lines.  8192 x 7168 bfloat16 along the columns
+//          44 us, in square blocks 37; as wide floats from the load on, with twice
+//          the registers and lane exchanges, 54 and 41.
 #pragma once
 
 #include "f8_kernel.hpp"
@@ -125,6 +128,45 @@ struct F8QuantArgs {
   Short few;
 };
 
+// The larger of two magnitudes, of both halves in 16-bit formats (whose bits order
+// them as float32's do).
+template <int FMT>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  if constexpr (FMT == MX_F32) return a > b ? a : b;
+  using half2 = uint16_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(half2, a), __builtin_bit_cast(half2, b)));
+}
+// Largest magnitudes of N lines of 8 elements, of each element on its own.
+template <int FMT, int N>
+__device__ __forceinline__ Oct<FMT> largest_of(const Oct<FMT> (&v)[N]) {
+  Oct<FMT> m;
+#pragma unroll
+  for (int h = 0; h < Oct<FMT>::ES / 2; ++h)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t x = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) x = larger<FMT>(x, v[i].v[h][w] & (FMT == MX_F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu));
+      m.v[h][w] = x;
+    }
+  return m;
+}
+
+// Bits of the largest of 8 magnitudes, as a float32's.
+template <int FMT>
+__device__ __forceinline__ uint32_t largest_bits(const Oct<FMT>& m) {
+  Oct<FMT> one = m;
+  uint32_t x = 0;
+#pragma unroll
+  for (int h = 0; h < Oct<FMT>::ES / 2; ++h)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) x = larger<FMT>(x, m.v[h][w]);
+  one.v[0][0] = x;
+  if constexpr (FMT == MX_F32) return x;
+  const uint32_t a = magnitude(one.get(0)), b = magnitude(one.get(1));
+  return a > b ? a : b;
+}
+
 // Rows with unit k stride; wave items as in quantize_rows_kernel, with 16 octets
 // a block.
 template <int FMT, int F8, bool SHORT, bool ONCE>
@@ -141,47 +183,47 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(F8QuantArgs a) {
 #pragma unroll
   for (int u = 0; u < kQuantU; ++u) {
     const Place p = place<SHORT>(w, u, lane, a.R, octs, a.segs, a.few);
-    float f[8];
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f[i] = v[u].get(i);
-      const uint32_t b = magnitude(f[i]);
-      m = b > m ? b : m;
-    }
-    const F8Scale s = f8_scale<F8>(max16(m));
+    const Oct<FMT> line[1] = {v[u]};
+    const F8Scale s = f8_scale<F8>(max16(largest_bits(largest_of(line))));
     if (p.ok) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = v[u].get(i);
       store_codes<ONCE>(a.data + p.row * a.ldd + 8 * p.o, f8_codes<F8>(f, s), a.K - 8 * p.o);
       if ((p.o & 15) == 0) gstore<float>(a.scales + p.row * a.ss_r + (p.o >> 4) * a.ss_k, s.scale);
     }
   }
 }
 
-// 8 elements n apart in memory, `valid` of them.
-template <int FMT>
-__device__ __forceinline__ void load8_strided(float (&f)[8], const void* x, int64_t at, int64_t step, int64_t valid) {
+// 8 elements `step` apart in memory, `valid` of them.
+template <int FMT, bool ONCE>
+__device__ __forceinline__ void load8_strided(Oct<FMT>& v, const void* x, int64_t at, int64_t step, int64_t valid) {
   if (step == 1) {
-    Oct<FMT> v;
-    v.load(x, at, valid);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = v.get(i);
+    v.template load<ONCE>(x, at, valid);
     return;
   }
   const char* p = (const char*)x + at * Oct<FMT>::ES;
+  uint32_t h[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     typename MxElem<FMT>::type e = 0;
     if (i < valid) e = gload<typename MxElem<FMT>::type>(p + i * step * Oct<FMT>::ES);
-    f[i] = mx_in<FMT>(e);
+    h[i] = e;
+  }
+  if constexpr (FMT == MX_F32) {
+    v.v[0] = u32x4{h[0], h[1], h[2], h[3]};
+    v.v[1] = u32x4{h[4], h[5], h[6], h[7]};
+  } else {
+    v.v[0] = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
   }
 }
 
 // One 128 x 128 tile.  ALONG_K: a thread's 8 loads are 8 rows of 8 consecutive k
 // (threads of a row: 16 neighbouring lanes); else 8 k of 8 consecutive rows.
-template <int FMT, int F8, bool SQUARE, bool ALONG_K>
+template <int FMT, int F8, bool SQUARE, bool ALONG_K, bool ONCE>
 __global__ __launch_bounds__(256) void f8_tiles_kernel(F8QuantArgs a) {
   static_assert(SQUARE || !ALONG_K, "rows with unit k stride have their own kernel");
-  __shared__ uint32_t part[4][kF8Block];
+  __shared__ __attribute__((aligned(16))) uint32_t part[4 * kF8Block];
   __shared__ __attribute__((aligned(16))) char turn[SQUARE && ALONG_K ? 16 : kF8Block * 128];
   const int tid = threadIdx.x, hi = tid >> 4, lo = tid & 15, lane = tid & 63, wave = tid >> 6;
   const int64_t tile = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
@@ -191,56 +233,53 @@ __global__ __launch_bounds__(256) void f8_tiles_kernel(F8QuantArgs a) {
   const int rl = 8 * (ALONG_K ? hi : lo), kl = 8 * (ALONG_K ? lo : hi);
   const int64_t r0 = br * kF8Block + rl, q0 = bk * kF8Block + kl;
   const int64_t nr = a.R - r0, nk = a.K - q0;
-  float f[8][8];           // [line][element]: ALONG_K [row][k], else [k][row]
+  Oct<FMT> v[8];           // [line][element]: ALONG_K [row][k], else [k][row]
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t at = ALONG_K ? (r0 + i) * a.s_r + q0 * a.s_k : (q0 + i) * a.s_k + r0 * a.s_r;
     const bool ok = i < (ALONG_K ? nr : nk);
-    load8_strided<FMT>(f[i], a.x, at, ALONG_K ? a.s_k : a.s_r, ok ? (ALONG_K ? nk : nr) : 0);
+    load8_strided<FMT, ONCE>(v[i], a.x, at, ALONG_K ? a.s_k : a.s_r, ok ? (ALONG_K ? nk : nr) : 0);
   }
+  Oct<FMT> most = largest_of(v);
   F8Scale s[SQUARE ? 1 : 8];
   if constexpr (SQUARE) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t b = magnitude(f[i][e]);
-        m = b > m ? b : m;
-      }
-    m = max16(m);
-    if (lo == 0) part[0][hi] = m;
+    uint32_t m = max16(largest_bits(most));
+    if (lo == 0) part[hi] = m;
     __syncthreads();
     m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = part[0][i] > m ? part[0][i] : m;
+    for (int i = 0; i < 16; ++i) m = part[i] > m ? part[i] : m;
     s[0] = f8_scale<F8>(m);
     if (tid == 0) a.scales[br * a.ss_r + bk * a.ss_k] = s[0].scale;
   } else {
     // Row rl + e: over this thread's 8 k, the wave's four groups of 16 lanes,
     // the four waves.
+    constexpr int H = Oct<FMT>::ES / 2;
+    u32x4* const rows = reinterpret_cast<u32x4*>(part);       // [wave][lo][H]
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t m = 0;
+    for (int h = 0; h < H; ++h) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t b = magnitude(f[i][e]);
-        m = b > m ? b : m;
+      for (int w = 0; w < 4; ++w) {
+        uint32_t m = most.v[h][w];
+        m = larger<FMT>(m, (uint32_t)__shfl_xor((int)m, 16));
+        most.v[h][w] = larger<FMT>(m, (uint32_t)__shfl_xor((int)m, 32));
       }
-      uint32_t o = __shfl_xor(m, 16);
-      m = o > m ? o : m;
-      o = __shfl_xor(m, 32);
-      m = o > m ? o : m;
-      if (lane < 16) part[wave][rl + e] = m;
+      if (lane < 16) rows[(wave * 16 + lo) * H + h] = most.v[h];
     }
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t m = 0;
+    for (int h = 0; h < H; ++h) {
+      u32x4 m = rows[lo * H + h];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m = part[i][rl + e] > m ? part[i][rl + e] : m;
-      s[e] = f8_scale<F8>(m);
+      for (int i = 1; i < 4; ++i) {
+        const u32x4 o = rows[(i * 16 + lo) * H + h];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m[w] = larger<FMT>(m[w], o[w]);
+      }
+      most.v[h] = m;
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = f8_scale<F8>(magnitude(most.get(e)));
     // its scale by the first k's thread
     if (hi == 0)
 #pragma unroll
@@ -250,17 +289,22 @@ __global__ __launch_bounds__(256) void f8_tiles_kernel(F8QuantArgs a) {
   if constexpr (ALONG_K) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < nr) store_codes(a.data + (r0 + i) * a.ldd + q0, f8_codes<F8>(f[i], s[0]), nk);
+      if (i < nr) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
+        store_codes<ONCE>(a.data + (r0 + i) * a.ldd + q0, f8_codes<F8>(f, s[0]), nk);
+      }
   } else {
     // Row e's 8 k into LDS (rows of 128 bytes, 8-byte chunk c of row r in slot
     // c ^ (r / 8) % 16: the 16 rows 8 apart that neighbouring lanes write fall on
     // distinct banks), back as whole rows.
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float v[8];
+      float f[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = f[i][e];
-      *reinterpret_cast<u32x2*>(turn + (rl + e) * 128 + ((hi ^ lo) * 8)) = f8_codes<F8>(v, s[SQUARE ? 0 : e]);
+      for (int i = 0; i < 8; ++i) f[i] = v[i].get(e);
+      *reinterpret_cast<u32x2*>(turn + (rl + e) * 128 + ((hi ^ lo) * 8)) = f8_codes<F8>(f, s[SQUARE ? 0 : e]);
     }
     __syncthreads();
 #pragma unroll
@@ -268,7 +312,7 @@ __global__ __launch_bounds__(256) void f8_tiles_kernel(F8QuantArgs a) {
       const int r = 16 * i + hi;
       const int64_t row = br * kF8Block + r, k = bk * kF8Block + 8 * lo;
       const u32x2 v = *reinterpret_cast<const u32x2*>(turn + r * 128 + ((lo ^ (r >> 3)) * 8));
-      if (row < a.R) store_codes(a.data + row * a.ldd + k, v, a.K - k);
+      if (row < a.R) store_codes<ONCE>(a.data + row * a.ldd + k, v, a.K - k);
     }
   }
 }
