@@ -175,11 +175,11 @@ struct NormBackArgs {
   int32_t waves, lanes;
 };
 
-// NT: threads of the widest row.  With two or four octets a lane there are
-// registers for the next row, which is loaded under this one's sums.
-template <int FMT, int U, int NT, bool DH, bool W32, bool ONCE>
-__global__ __launch_bounds__(NT) void rms_norm_back_kernel(NormBackArgs a) {
-  constexpr bool AHEAD = U <= 4;
+// Rows of at most 8 waves of U octets a lane: the weight stays in registers, and
+// the next row is loaded under this one's sums.
+constexpr int kBackThreads = 512;
+template <int FMT, int U, bool DH, bool W32, bool ONCE>
+__global__ __launch_bounds__(kBackThreads) void rms_norm_back_kernel(NormBackArgs a) {
   __shared__ float part[2][2][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int share = 64 >> a.lanes, sub = wave / a.waves * share + (lane >> a.lanes), rw = wave % a.waves;
@@ -214,11 +214,10 @@ __global__ __launch_bounds__(NT) void rms_norm_back_kernel(NormBackArgs a) {
   };
   int turn = 0;
   Row next;
-  if (AHEAD && first < a.R) load(next, first);
+  if (first < a.R) load(next, first);
   for (int64_t row = first; row < a.R; row += stride, turn ^= 1) {
-    if constexpr (!AHEAD) load(next, row);
     const Row now = next;
-    if (AHEAD && row + stride < a.R) load(next, row + stride);
+    if (row + stride < a.R) load(next, row + stride);
     float ss = 0.0f, sg = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -269,6 +268,82 @@ __global__ __launch_bounds__(NT) void rms_norm_back_kernel(NormBackArgs a) {
       for (int i = 0; i < 7; ++i)
         if (k + i < a.K) gstore<float>(p + k + i, dw[u][i]);
     }
+  }
+}
+
+// Wider rows, up to 8 octets for each of 1024 lanes: only the weight gradient's
+// sums stay in registers; a row is read again after the sums over it, from the
+// caches.  (2048 x 20000 bfloat16 with dh 133 us; in registers, of which there are
+// 128 a lane, it spilled: 493.)
+constexpr int kWideThreads = 1024, kWideOcts = 8;
+template <int FMT, bool DH, bool W32>
+__global__ __launch_bounds__(kWideThreads) void rms_norm_back_wide_kernel(NormBackArgs a) {
+  __shared__ float part[2][2][16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, K = (int)a.K;
+  using W = Oct<W32 ? MX_F32 : FMT>;
+  float dw[kWideOcts][8];
+#pragma unroll
+  for (int u = 0; u < kWideOcts; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[u][i] = 0.0f;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x, turn ^= 1) {
+    const char* const py = (const char*)a.dy + row * a.ldy * 2;
+    const char* const ph = (const char*)a.h + row * a.ldh * 2;
+    float ss = 0.0f, sg = 0.0f;
+#pragma unroll 2
+    for (int k = 8 * tid; k < K; k += 8 * kWideThreads) {
+      Oct<FMT> y, h;
+      W w;
+      y.load(py, k, K - k);
+      h.load(ph, k, K - k);
+      w.load(a.w, k, K - k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        ss = __builtin_fmaf(h.get(i), h.get(i), ss);
+        sg = __builtin_fmaf(y.get(i) * w.get(i), h.get(i), sg);
+      }
+    }
+    ss = wave_sum(ss);
+    sg = wave_sum(sg);
+    if (lane == 0) {
+      part[turn][0][wave] = ss;
+      part[turn][1][wave] = sg;
+    }
+    __syncthreads();
+    ss = sum_parts(part[turn][0], kWideThreads / 64, lane);
+    sg = sum_parts(part[turn][1], kWideThreads / 64, lane);
+    const float r = 1.0f / sqrtf(ss / (float)K + a.eps);
+    const float c = sg / (float)K * r * r;
+#pragma unroll
+    for (int u = 0; u < kWideOcts; ++u) {
+      asm volatile("" ::: "memory");   // no octet's loads before the one ahead is done with
+      const int k = 8 * (tid + u * kWideThreads);
+      if (k < K) {
+        Oct<FMT> y, h, d;
+        W w;
+        y.load(py, k, K - k);
+        h.load(ph, k, K - k);
+        w.load(a.w, k, K - k);
+        if constexpr (DH) d.load((const char*)a.dh + row * a.lddh * 2, k, K - k);
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f[i] = r * (y.get(i) * w.get(i) - h.get(i) * c);
+          if constexpr (DH) f[i] += d.get(i);
+          dw[u][i] = __builtin_fmaf(y.get(i) * r, h.get(i), dw[u][i]);
+        }
+        store8_part((uint16_t*)a.dx + row * a.lddx + k, pack8<FMT>(f), K - k);
+      }
+    }
+  }
+  float* const p = a.part + (int64_t)blockIdx.x * a.K;
+#pragma unroll
+  for (int u = 0; u < kWideOcts; ++u) {
+    const int k = 8 * (tid + u * kWideThreads);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k + i < K) gstore<float>(p + k + i, dw[u][i]);
   }
 }
 

@@ -33,8 +33,12 @@ Shape shape(int64_t K, int most) {
   return Shape{U, (int)cdiv(octs, 64 * U), 6};
 }
 Shape norm_shape(int64_t K) { return shape(K, 16); }
-// The backward kernel holds more of a row: 8 waves, 16 of the widest.
-Shape back_shape(int64_t K) { return shape(K, 8); }
+// The backward kernel holds more of a row: 8 waves, and rows wider than they hold
+// have a kernel of their own (U 8, 16 waves).
+Shape back_shape(int64_t K) {
+  const Shape s = shape(K, kBackThreads / 64);
+  return s.U < kWideOcts ? s : Shape{kWideOcts, kWideThreads / 64, 6};
+}
 
 bool weight_format(int32_t fmt, int32_t fmt_w) { return fmt_w == fmt || fmt_w == GEMM_FMT_F32; }
 
@@ -65,10 +69,10 @@ const void* norm_fn(int32_t fmt, int32_t fmt8, int U, bool res, bool w32, bool o
 
 template <int FMT>
 const void* back_fn1(int U, bool dh, bool w32, bool o) {
-  return U == 1   ? GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 1, 512)
-         : U == 2 ? GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 2, 512)
-         : U == 4 ? GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 4, 512)
-                  : GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 8, 1024);
+  return U == 1   ? GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 1)
+         : U == 2 ? GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 2)
+         : U == 4 ? GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 4)
+                  : GEMM_BY_FLAGS2(rms_norm_back_wide_kernel, dh, w32, FMT);
 }
 const void* back_fn(int32_t fmt, int U, bool dh, bool w32, bool o) {
   return fmt == GEMM_FMT_F16 ? back_fn1<MX_F16>(U, dh, w32, o) : back_fn1<MX_BF16>(U, dh, w32, o);

@@ -244,6 +244,28 @@ def test_sort_without_a_workspace():
         same(o, want)
 
 
+@pytest.mark.parametrize("R,K", [(300, 16384), (300, 16392), (290, 20001), (260, 65536)])
+def test_norm_backward_of_wide_rows_in_place(R, K):
+    """More rows than workgroups, and dx where dy or dh was."""
+    say(f"wide norm backward {R}x{K}")
+    dy, h, dh, w = randn(R, K), randn(R, K, seed=1), randn(R, K, seed=3), randn(K, dtype=F32, seed=2)
+    dx, dw = g.rms_norm_backward(dy, h, w, dh=dh)
+    hd, y = h.double(), dy.double()
+    r = 1 / (hd.square().mean(dim=1, keepdim=True) + 1e-6).sqrt()
+    yw = y * w.double()
+    c = (yw * hd).mean(dim=1, keepdim=True) * r * r
+    want, mag = r * (yw - hd * c) + dh.double(), r * (yw.abs() + (hd * c).abs()) + dh.double().abs()
+    cmag = (yw * hd).abs().mean(dim=1, keepdim=True) * r * r * hd.abs() * r
+    # dx: half a step of bfloat16; r and c within 100 float32 roundings of their terms
+    assert ((dx.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -24 * (100 * cmag + 120 * mag)).all()
+    terms = y * hd * r
+    # dw: at most 2 rows of a workgroup and R workgroups added, 60 roundings in a term
+    assert ((dw.double() - terms.sum(dim=0)).abs() <= (R + 60) * 2.0 ** -24 * terms.abs().sum(dim=0)).all()
+    for i in range(2):
+        a, b = dy.clone(), dh.clone()
+        same(g.rms_norm_backward(a, h, w, dh=b, out=(a, b)[i]), (dx, dw))
+
+
 # ---- larger than the caches: the same rows in parts have the same bits
 
 def test_large_norm():
