@@ -21,6 +21,11 @@
 // Registers: 128 running sums, 4 sums of blocks in flight (16), A 32, B 5 blocks
 // (40).  The stages' halves lie so that all LDS addresses of both are one base
 // and an immediate; the loop takes two steps a turn.
+//
+// 32768 x 2048 x 7168 in 415 us (2320 TFLOP/s), 348 on zeros: the clock falls to
+// 1.8 GHz at the power of multiplying random bytes, with the matrix core busy 57%
+// of the cycles (the unscaled FP8 tile, without the multiply-adds: 373).  Touching
+// the lines of later steps ahead of their transfer made it slower (432).
 #pragma once
 
 #include "f8s_tile_kernel.hpp"

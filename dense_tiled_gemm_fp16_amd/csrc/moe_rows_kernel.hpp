@@ -18,7 +18,9 @@
 //            copy is written and the product with the expert's row summed up.
 // The last three move rows of up to some ten KB with a few operations per
 // element: memory bounds them.  Lanes take 16 bytes each, so that loads and
-// stores are whole lines.
+// stores are whole lines.  16384 tokens, top 8 of 64, 7168 bfloat16: sort 15 us,
+// gather 420 (5.0 TB/s, nearly all of it writes of rows in no order; in their order,
+// reading x in no order, 520), combine 360 (5.9 TB/s).  48 tokens: 4.0, 5.9, 5.3.
 #pragma once
 
 #include "norm_kernel.hpp"

@@ -72,7 +72,8 @@ def rms_norm_f8(x, weight, eps=1e-6, residual=None, dtype=torch.float8_e4m3fn, o
     (float8_e4m3fn or float8_e5m2) by row blocks, as quantize_f8 does it.
 
     x, residual [R, K] float16 or bfloat16, unit stride along K, K at most 65536;
-    weight [K] of their dtype or float32.  Sums are float32.
+    weight [K] of their dtype or float32.  Sums are float32: a row whose squares sum
+    past 3.4e38 becomes zeros.
     out: a pair (data, scales); h: where the sum goes, which may be x or residual
     themselves."""
     shape, R, K, ldx, fmt = _check_rows(x, weight, eps)
