@@ -129,6 +129,7 @@ int gemm_f8s_quantize(const gemm_f8s_quantize_args* args, void* stream) {
   if (!byte_view(X, R, K, ldx_r, ldx_k, elem_size(fmt), &rx) || !byte_rows(data, R, ldd, K, &rd) ||
       !byte_view(scales, sr, kb, lds_r, lds_k, 4, &rs))
     return GEMM_ERR_SHAPE;
+  if (!apart(sr, kb, lds_r, lds_k)) return GEMM_ERR_LDC;
   if ((uintptr_t)scales & 3u) return GEMM_ERR_LAYOUT;
   if (overlap(rx, rd) || overlap(rx, rs) || overlap(rd, rs)) return GEMM_ERR_ALIAS;
 

@@ -27,6 +27,12 @@ inline bool byte_view(const void* p, int64_t rows, int64_t cols, int64_t sr, int
   return view_span(rows, cols, sr, sc, &span) && span <= INT64_MAX / 16 && byte_rows(p, 1, 1, (span + 1) * elem, r);
 }
 
+// Whether the elements of a rows x cols view (whose range is known not to overflow)
+// are apart from each other, as an output's have to be.
+inline bool apart(int64_t rows, int64_t cols, int64_t sr, int64_t sc) {
+  return rows == 1 || cols == 1 || sr > (cols - 1) * sc || sc > (rows - 1) * sr;
+}
+
 inline bool overlap(const Range& a, const Range& b) { return ranges_overlap(a.lo, a.hi, b.lo, b.hi); }
 
 // A launch takes fewer than 2^32 work items along x.

@@ -118,6 +118,7 @@ int gemm_rms_norm_f8(const gemm_rms_norm_f8_args* args, void* stream) {
       !byte_rows(data, R, ldd, K, &rd) || !byte_view(scales, R, cdiv(K, kF8Block), lds_r, lds_k, 4, &rs))
     return GEMM_ERR_SHAPE;
   if (residual && (!byte_view(residual, R, K, ldr, 1, 2, &rr) || !byte_view(H, R, K, ldh, 1, 2, &rh))) return GEMM_ERR_SHAPE;
+  if (!apart(R, cdiv(K, kF8Block), lds_r, lds_k)) return GEMM_ERR_LDC;
   if ((uintptr_t)scales & 3u) return GEMM_ERR_LAYOUT;
   if (overlap(rd, rx) || overlap(rd, rw) || overlap(rd, rs) || overlap(rs, rx) || overlap(rs, rw)) return GEMM_ERR_ALIAS;
   if (residual && (overlap(rd, rr) || overlap(rs, rr) || overlap(rd, rh) || overlap(rs, rh) || overlap(rh, rw) ||

@@ -61,7 +61,7 @@ def quantize_f8(x, rows=1, dtype=torch.float8_e4m3fn, out=None, stream=None):
     elements are multiplied by L / m and rounded to nearest, ties to even.  A block
     with an infinity or a NaN gets a NaN scale and zero elements.
     data has rows that start 16-byte aligned.  out: a pair (data, scales), data
-    with any row stride, scales with any positive strides."""
+    with any row stride, scales with any positive strides that keep them apart."""
     fmt, fmt8, device = FORMATS.get(x.dtype), FORMATS8.get(dtype), x.device
     if fmt is None:
         raise TypeError("expected float16, bfloat16 or float32")

@@ -32,7 +32,8 @@ extern "C" {
  * element x becomes x L / m' rounded to nearest, ties to even (for a 16-bit x
  * that quotient is rounded once; for a float32 x it is first rounded to float32).
  * A block that holds an infinity or a NaN gets a NaN scale and zero elements.
- * Nothing past a row's K bytes is written.
+ * Nothing past a row's K bytes is written.  Scales of different blocks may not
+ * share an address (GEMM_ERR_LDC).
  */
 typedef struct gemm_f8s_quantize_args {
   const void* X;

@@ -49,6 +49,7 @@ def quantize(X=P[0], fmt=1, sr=300, sk=1, R=4, K=300, rows=1, data=P[1], fmt8=0,
     (dict(ldd=2 ** 62), -2), (dict(ss_r=2 ** 61), -2),
     (dict(fmt=3), -7), (dict(fmt=-1), -7), (dict(fmt8=2), -7), (dict(fmt8=-1), -7), (dict(rows=64), -7),
     (dict(sr=0), -3), (dict(sk=0), -3), (dict(ss_r=0), -3), (dict(ss_k=-1), -3), (dict(ldd=299), -4),
+    (dict(ss_r=1), -4), (dict(ss_r=2, ss_k=1), -4), (dict(ss_r=1, ss_k=3), -4),
     (dict(scales=P[2] + 2), -9), (dict(data=P[0] + 64), -5), (dict(scales=P[0] + 64), -5), (dict(scales=P[1] + 16), -5),
 ])
 def test_quantize_refusals(kw, code):
@@ -129,7 +130,7 @@ def norm(X=P[0], ldx=300, res=P[1], ldr=300, fmt=1, W=P[2], fmt_w=2, eps=1e-6, H
     (dict(R=0), -2), (dict(K=0), -2), (dict(K=65537, ldd=70000, ldh=70000), -2), (dict(ldx=2 ** 62), -2),
     (dict(fmt=2), -7), (dict(fmt=-1), -7), (dict(fmt_w=0), -7), (dict(fmt8=2), -7), (dict(eps=-1.0), -7),
     (dict(eps=float("nan")), -7), (dict(ldx=0), -3), (dict(ldr=0), -3), (dict(ss_r=0), -3), (dict(ss_k=0), -3),
-    (dict(ldd=299), -4), (dict(ldh=299), -4), (dict(scales=P[5] + 1), -9),
+    (dict(ldd=299), -4), (dict(ldh=299), -4), (dict(ss_r=2), -4), (dict(ss_r=1, ss_k=3), -4), (dict(scales=P[5] + 1), -9),
     (dict(data=P[0]), -5), (dict(data=P[1]), -5), (dict(data=P[2]), -5), (dict(data=P[3]), -5), (dict(scales=P[0]), -5),
     (dict(scales=P[4]), -5), (dict(H=P[0] + 2), -5), (dict(H=P[0], ldh=302), -5), (dict(H=P[1] + 600), -5),
     (dict(H=P[2]), -5),
