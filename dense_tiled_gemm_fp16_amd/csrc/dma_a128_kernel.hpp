@@ -366,40 +366,6 @@ __device__ __forceinline__ void store8_any(uint16_t* dst, u32x4 v) {
   }
 }
 
-// The wave's staged 64 x 128 block (chunk c of row r at position c ^ (r % 16)) to
-// C, row by row.
-template <class CF>
-__device__ __forceinline__ void store_staged_rows(uint16_t* C, int64_t ldc, int64_t M, int64_t N, const char* stage,
-                                                  int64_t m0, int64_t n0, int wm, int wn, int lane) {
-  uint16_t* const cw = C + (m0 + wm * CF::WTM) * ldc + n0 + wn * CF::WTN;
-  // Rows and columns of this wave's block that lie inside C (clamped).
-  const int64_t mr = M - (m0 + wm * CF::WTM), nc = N - (n0 + wn * CF::WTN);
-  const int rows = mr < 0 ? 0 : (mr > CF::WTM ? CF::WTM : (int)mr);
-  const int cols = nc < 0 ? 0 : (nc > CF::WTN ? CF::WTN : (int)nc);
-  if (((uintptr_t)C & 15u) == 0 && (ldc & 7) == 0 && (cols & 7) == 0) {
-#pragma unroll
-    for (int it = 0; it < CF::WTM / 4; ++it) {
-      const int r = 4 * it + lane / 16, c = lane % 16;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(stage + r * 256 + ((c ^ (r & 15)) << 4));
-      if (r < rows && 8 * c + 8 <= cols) *reinterpret_cast<u32x4*>(cw + (int64_t)r * ldc + c * 8) = v;
-    }
-  } else {
-    for (int it = 0; it < CF::WTM / 4; ++it) {
-      const int r = 4 * it + lane / 16, c = lane % 16;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(stage + r * 256 + ((c ^ (r & 15)) << 4));
-      const int nv = cols - 8 * c;
-      uint16_t* const dst = cw + (int64_t)r * ldc + c * 8;
-      if (r < rows && nv >= 8) {
-        store8_any(dst, v);
-      } else if (r < rows && nv > 0) {
-#pragma unroll
-        for (int e = 0; e < 7; ++e)
-          if (e < nv) dst[e] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
-      }
-    }
-  }
-}
-
 // Output of a tile staged through LDS, so that each store instruction
 // writes four whole rows of the wave's 64 x 128 block (256 bytes each) rather
 // than 8 bytes into each of 32 rows.  Stored straight from the accumulators,
@@ -443,7 +409,33 @@ __device__ __forceinline__ void store_tile_staged(const KArgs& a, const f32x16 (
         const int r = j * 32 + lr, c = 4 * i + 2 * p + h;
         *reinterpret_cast<u32x4*>(stage + r * 256 + ((c ^ (r & 15)) << 4)) = u32x4{x0, x1, y0, y1};
       }
-  store_staged_rows<CF>(a.C, a.ldc, a.M, a.N, stage, m0, n0, wm, wn, lane);
+  uint16_t* const cw = a.C + (m0 + wm * CF::WTM) * a.ldc + n0 + wn * CF::WTN;
+  // Rows and columns of this wave's block that lie inside C (clamped).
+  const int64_t mr = a.M - (m0 + wm * CF::WTM), nc = a.N - (n0 + wn * CF::WTN);
+  const int rows = mr < 0 ? 0 : (mr > CF::WTM ? CF::WTM : (int)mr);
+  const int cols = nc < 0 ? 0 : (nc > CF::WTN ? CF::WTN : (int)nc);
+  if (((uintptr_t)a.C & 15u) == 0 && (a.ldc & 7) == 0 && (cols & 7) == 0) {
+#pragma unroll
+    for (int it = 0; it < CF::WTM / 4; ++it) {
+      const int r = 4 * it + lane / 16, c = lane % 16;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(stage + r * 256 + ((c ^ (r & 15)) << 4));
+      if (r < rows && 8 * c + 8 <= cols) *reinterpret_cast<u32x4*>(cw + (int64_t)r * a.ldc + c * 8) = v;
+    }
+  } else {
+    for (int it = 0; it < CF::WTM / 4; ++it) {
+      const int r = 4 * it + lane / 16, c = lane % 16;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(stage + r * 256 + ((c ^ (r & 15)) << 4));
+      const int nv = cols - 8 * c;
+      uint16_t* const dst = cw + (int64_t)r * a.ldc + c * 8;
+      if (r < rows && nv >= 8) {
+        store8_any(dst, v);
+      } else if (r < rows && nv > 0) {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+          if (e < nv) dst[e] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
+      }
+    }
+  }
 }
 
 // fp32 partials of the wave's 64 x 128 block to base (its element (0, 0); row

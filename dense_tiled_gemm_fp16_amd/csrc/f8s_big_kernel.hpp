@@ -278,7 +278,7 @@ __global__ __launch_bounds__(F8sBig::NT) void f8s_big_kernel(F8sArgs a) {
     wg_barrier();
   }
   // Through LDS, so that each store instruction writes four whole rows of the
-  // wave's block (see store_tile_staged): a lane's 4 columns are half a chunk.
+  // wave's block (store_staged_block): a lane's 4 columns are half a chunk.
   char* const stage = smem + wave * (CF::WTM * CF::WTN * 2);
 #pragma unroll
   for (int i = 0; i < CF::FN; ++i)
@@ -288,7 +288,8 @@ __global__ __launch_bounds__(F8sBig::NT) void f8s_big_kernel(F8sArgs a) {
       *reinterpret_cast<u32x2*>(stage + r * 256 + ((c ^ (r & 15)) << 4) + 8 * (g & 1)) =
           u32x2{pack_out2<DT>(acc[i][j][0], acc[i][j][1]), pack_out2<DT>(acc[i][j][2], acc[i][j][3])};
     }
-  store_staged_rows<CF>((uint16_t*)a.C, a.ldc, a.M, a.N, stage, m0, n0, wm, wn, lane);
+  const int64_t mw = m0 + wm * CF::WTM, nw = n0 + wn * CF::WTN;
+  store_staged_block<CF::WTM, CF::WTN * 2>((char*)a.C + (mw * a.ldc + nw) * 2, a.ldc * 2, a.M - mw, (a.N - nw) * 2, stage, lane);
 }
 
 }  // namespace gemmf16

@@ -84,7 +84,7 @@ struct F8sCfg {
   static constexpr int PER_STEP = DI + SI;
   static_assert(DI % 2 == 0 && DMA_A % BATCH == 0, "batches of one operand");
   static_assert((DMA_A + DMA_B) % NW == 0 && TM % 16 == 0 && TN % 16 == 0 && 128 % TN == 0, "shape");
-  static_assert(LDS <= 160 * 1024, "LDS budget");
+  static_assert(LDS <= 160 * 1024 && BM * BN * 4 <= LDS, "LDS budget, staging space");
 };
 
 // One 256-byte DMA: lane l's dword at base + off lands at LDS lds + 4 l.
@@ -178,6 +178,40 @@ __device__ __forceinline__ void store_out4(void* C, int out, int64_t at, f32x4 v
     gstore<u32x2>(p, u32x2{(uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16)});
   else
     store4_part(p, h, (int)nv);
+}
+
+// A wave's block of TM rows x RB bytes, staged in LDS (16-byte chunk c of row r in
+// place c ^ r % (RB / 16)), to C by whole rows.  Stored from the sums, 8 or 16 bytes
+// into each of 16 rows, a tile's end costs a request per piece: 16384 x 4096 x 128
+// took 48 us so and takes 35, 11008 x 4730 x 258 52 and 46 (128 x 128 tiles).  The first
+// `rows` rows and `bytes` bytes of each lie inside C (none, if negative); any alignment.
+template <int TM, int RB>
+__device__ __forceinline__ void store_staged_block(char* C, int64_t pitch, int64_t rows, int64_t bytes, const char* stage,
+                                                   int lane) {
+  constexpr int CH = RB / 16, PER = 64 / CH;
+  const int c = lane % CH, r0 = lane / CH;
+  auto chunk = [&](int r) { return *reinterpret_cast<const u32x4*>(stage + r * RB + ((c ^ (r & (CH - 1))) << 4)); };
+  C += r0 * pitch + 16 * c;
+  if (rows >= TM && bytes >= RB) {
+#pragma unroll
+    for (int it = 0; it < TM / PER; ++it) gstore<u32x4>(C + it * PER * pitch, chunk(PER * it + r0));
+    return;
+  }
+  const int n = (int)(bytes < RB ? bytes : RB) - 16 * c, last = (int)(rows < TM ? rows : TM) - r0;
+#pragma unroll
+  for (int it = 0; it < TM / PER; ++it) {
+    const u32x4 v = chunk(PER * it + r0);
+    char* const p = C + it * PER * pitch;
+    if (PER * it < last) {
+      if (n >= 16) {
+        gstore<u32x4>(p, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+          if (2 * e < n) gstore<uint16_t>((uint16_t*)p + e, (uint16_t)(v[e / 2] >> (16 * (e % 2))));
+      }
+    }
+  }
 }
 
 // Bytes of a lane's 32 that lie behind rem, zeroed (those at k >= rem of the block:
@@ -385,16 +419,38 @@ __global__ __launch_bounds__(CF::NT, CF::WAVES) void f8s_tile_kernel(F8sArgs a) 
     wg_barrier();
     compute(std::true_type{}, slot);
   }
-  wait_vmcnt<0>();       // no LDS transfer may outlive the workgroup
-
+  wait_vmcnt<0>();       // no LDS transfer may outlive the workgroup, and every
+  wait_lgkmcnt0();       // wave has read its stage: the LDS is free
+  wg_barrier();
+  char* const stage = smem + wave * (CF::TM * CF::TN * 4);
+  const int64_t mw = m0 + wm * CF::TM, nw = n0 + wn * CF::TN, es = a.out == F8S_F32 ? 4 : 2;
+  char* const cw = (char*)a.C + (mw * a.ldc + nw) * es;
+  if (a.out == F8S_F32) {
 #pragma unroll
-  for (int j = 0; j < CF::FM; ++j) {
-    const int64_t m = m0 + wm * CF::TM + j * 16 + lr;
+    for (int j = 0; j < CF::FM; ++j)
 #pragma unroll
-    for (int i = 0; i < CF::FN; ++i) {
-      const int64_t n = n0 + wn * CF::TN + i * 16 + 4 * g;
-      if (m < a.M && n < a.N) store_out4(a.C, a.out, m * a.ldc + n, acc[i][j], a.N - n);
-    }
+      for (int i = 0; i < CF::FN; ++i) {
+        const int r = j * 16 + lr, c = 4 * i + g;
+        *reinterpret_cast<f32x4*>(stage + r * (CF::TN * 4) + ((c ^ (r & (CF::TN / 4 - 1))) << 4)) = acc[i][j];
+      }
+    store_staged_block<CF::TM, CF::TN * 4>(cw, a.ldc * 4, a.M - mw, (a.N - nw) * 4, stage, lane);
+  } else {
+    auto put = [&](auto dt_tag) {
+      constexpr int DT = decltype(dt_tag)::value;
+#pragma unroll
+      for (int j = 0; j < CF::FM; ++j)
+#pragma unroll
+        for (int i = 0; i < CF::FN; ++i) {
+          const int r = j * 16 + lr, c = 2 * i + (g >> 1);
+          *reinterpret_cast<u32x2*>(stage + r * (CF::TN * 2) + ((c ^ (r & (CF::TN / 8 - 1))) << 4) + 8 * (g & 1)) =
+              u32x2{pack_out2<DT>(acc[i][j][0], acc[i][j][1]), pack_out2<DT>(acc[i][j][2], acc[i][j][3])};
+        }
+    };
+    if (a.out == F8S_F16)
+      put(std::integral_constant<int, DT_F16>{});
+    else
+      put(std::integral_constant<int, DT_BF16>{});
+    store_staged_block<CF::TM, CF::TN * 2>(cw, a.ldc * 2, a.M - mw, (a.N - nw) * 2, stage, lane);
   }
 }
 

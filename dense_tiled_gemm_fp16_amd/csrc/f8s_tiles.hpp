@@ -50,9 +50,9 @@ constexpr F8sShape kF8sShapes[] = {
     f8s_strip_shape<F8sS32x32>(1.3f, 0.75f, 0.85f, 1.7f),
     f8s_strip_shape<F8sS64x32>(1.9f, 0.85f, 1.2f, 1.7f),
     f8s_strip_shape<F8sS64x64>(3.2f, 1.1f, 1.6f, 1.75f),
-    f8s_tile_shape<F8sT64x128>(4.8f, 0.45f, 0.7f, 1.85f),
-    f8s_tile_shape<F8sT128x128>(5.0f, 0.75f, 1.0f, 1.65f),
-    {F8sBig::BM, F8sBig::BN, 1, F8sBig::NT, 1, 5.3f, 1.2f, 1.7f, 1.0f},
+    f8s_tile_shape<F8sT64x128>(3.0f, 0.45f, 0.72f, 1.85f),
+    f8s_tile_shape<F8sT128x128>(3.4f, 0.75f, 1.0f, 1.7f),
+    {F8sBig::BM, F8sBig::BN, 1, F8sBig::NT, 1, 7.5f, 1.2f, 1.65f, 1.0f},
 };
 constexpr int kF8sVariants = sizeof(kF8sShapes) / sizeof(kF8sShapes[0]);
 static_assert(kF8sVariants == GEMM_F8S_TILE_256X256 + 1, "variants of the header");

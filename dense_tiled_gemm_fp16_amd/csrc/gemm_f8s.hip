@@ -83,14 +83,16 @@ bool takes(const F8sArgs& a, int variant, bool wide) {
 //   64 x 7168 x 2048     32x32 8.1, 64x32 5.5, 64x64 6.9, tile 64x128 12.9
 //   128 x 2048 x 7168    32x32 8.8, 64x32 10.3, 64x64 12.7, tile 64x128 31
 //   512 x 2048 x 7168    64x32 23, 64x64 17, tiles 64x128 30, 128x128 44
-//   1024 x 2048 x 2048   64x64 12.0, tiles 64x128 11.9, 128x128 16.0
-//   2048 x 2048 x 7168   64x64 59, tiles 64x128 46, 128x128 46, 256x256 76
-//   2048 x 4096 x 4096   64x64 72, tiles 64x128 53, 128x128 43, 256x256 46
-//   8192 x 2048 x 7168   64x64 226, tiles 64x128 170, 128x128 130, 256x256 99
-//   32768 x 2048 x 7168  256x256 410
-// Row blocks and float32: 2048 x 7168 x 8192 strips 64x64 313, tiles 64x128 298,
-// 128x128 248; 512 x 2048 x 7168 22, 45, 67.  Over 74 sizes, most of them random,
-// the choice took 3% longer than the best one in the mean, 20% at most.
+//   1024 x 2048 x 2048   64x64 12.0, tiles 64x128 11.3, 128x128 14.9
+//   2048 x 2048 x 7168   64x64 59, tiles 64x128 45, 128x128 45, 256x256 76
+//   2048 x 4096 x 4096   64x64 71, tiles 64x128 52, 128x128 41, 256x256 46
+//   16384 x 4096 x 128   64x64 197, tiles 64x128 51, 128x128 35, 256x256 36
+//   20864 x 1664 x 224   64x64 126, tiles 64x128 36, 128x128 28, 256x256 40
+//   8192 x 2048 x 7168   64x64 226, tiles 64x128 169, 128x128 131, 256x256 100
+//   32768 x 2048 x 7168  256x256 415
+// Row blocks and float32: 2048 x 7168 x 8192 strips 64x64 312, tiles 64x128 297,
+// 128x128 249; 512 x 2048 x 7168 22, 45, 67.  Over 74 sizes, most of them random,
+// the choice took 2% longer than the best one in the mean, 16% at most.
 int plan(const F8sArgs& a, bool wide, int cus) {
   int best = 0;
   float least = 0.0f;
