@@ -178,25 +178,52 @@ struct NormBackArgs {
   int32_t waves, lanes;
 };
 
+// The octet at k of a 16-bit row of K elements, zeros behind it.  One that K ends in
+// (TAIL: K is no multiple of 8) is loaded from 8 before K and moved to its place by
+// settle_oct when it is used: put together from single elements its wave would wait
+// for them at once (the gradients of 9698 x 3483 bfloat16, four workgroups a unit: 64 us
+// so, 54 now; of 9698 x 3480, 46).
+template <bool TAIL, bool ONCE, int FMT>
+__device__ __forceinline__ void load_oct(Oct<FMT>& o, const char* row, int k, int K) {
+  if (TAIL && K < 8) {
+    o.load(row + 2u * (uint32_t)k, 0, K - k);
+    return;
+  }
+  o.v[0] = zero4();
+  if (k < K) o.v[0] = load16_once<ONCE>(row + 2u * (uint32_t)(!TAIL || k + 8 <= K ? k : K - 8));
+}
+template <bool TAIL, int FMT>
+__device__ __forceinline__ void settle_oct(Oct<FMT>& o, int k, int K) {
+  if (!TAIL || K < 8 || k >= K || k + 8 <= K) return;
+  const int s = 16 * (k + 8 - K);                        // bits to drop, 16 .. 112
+  const u32x4 v = o.v[0];
+  const uint64_t lo = v[0] | ((uint64_t)v[1] << 32), hi = v[2] | ((uint64_t)v[3] << 32);
+  const uint64_t a = s >= 64 ? hi >> (s - 64) : (lo >> s) | (hi << (64 - s)), b = s >= 64 ? 0 : hi >> s;
+  o.v[0] = u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+}
+
 // Rows of at most 8 waves of U octets a lane: the weight stays in registers, and
 // the next row is loaded under this one's sums.
 constexpr int kBackThreads = 512;
-template <int FMT, int U, bool DH, bool W32, bool ONCE>
+template <int FMT, int U, bool TAIL, bool DH, bool W32, bool ONCE>
 __global__ __launch_bounds__(kBackThreads) void rms_norm_back_kernel(NormBackArgs a) {
   __shared__ float part[2][2][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int share = 64 >> a.lanes, sub = wave / a.waves * share + (lane >> a.lanes), rw = wave % a.waves;
+  // Only rows of one octet a lane share waves; the others' numbers, and with them
+  // their addresses but for 32-bit offsets, are the wave's.
+  const int lanes = U > 1 ? 6 : a.lanes;
+  const int share = 64 >> lanes, sub = wave / a.waves * share + (U > 1 ? 0 : lane >> lanes), rw = wave % a.waves;
   const int64_t per = blockDim.x / 64 / a.waves * share;
   const int64_t first = (int64_t)blockIdx.x * per + sub, stride = (int64_t)gridDim.x * per;
-  const int step = 64 * a.waves;
-  const int64_t o0 = 64 * rw + (lane & ((1 << a.lanes) - 1));
-  constexpr int ES = 2;
+  const int K = (int)a.K, step = 8 * 64 * a.waves, k0 = 8 * (64 * rw + (lane & ((1 << lanes) - 1)));
+  constexpr uint32_t ES = 2;
+  auto at = [](const void* base, uint32_t bytes) { return (const char*)base + bytes; };
   float w[U][8], dw[U][8];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t k = 8 * (o0 + u * step);
+    const int k = k0 + u * step;
     Oct<W32 ? MX_F32 : FMT> o;
-    o.load(a.w, k, a.K - k);
+    o.load(at(a.w, (W32 ? 4u : 2u) * k), 0, K - k);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       w[u][i] = o.get(i);
@@ -204,34 +231,46 @@ __global__ __launch_bounds__(kBackThreads) void rms_norm_back_kernel(NormBackArg
     }
   }
   struct Row {
-    Oct<FMT> y[U], h[U], d[DH ? U : 1];
+    Oct<FMT> y[U], h[U];
   };
   auto load = [&](Row& r, int64_t row) {
+    const char* const y = (const char*)a.dy + row * a.ldy * ES;
+    const char* const h = (const char*)a.h + row * a.ldh * ES;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t k = 8 * (o0 + u * step);
-      r.y[u].template load<ONCE>((const char*)a.dy + row * a.ldy * ES, k, a.K - k);
-      r.h[u].template load<ONCE>((const char*)a.h + row * a.ldh * ES, k, a.K - k);
-      if constexpr (DH) r.d[u].template load<ONCE>((const char*)a.dh + row * a.lddh * ES, k, a.K - k);
+      const int k = k0 + u * step;
+      load_oct<TAIL, ONCE>(r.y[u], y, k, K);
+      load_oct<TAIL, ONCE>(r.h[u], h, k, K);
     }
   };
   int turn = 0;
   Row next;
   if (first < a.R) load(next, first);
   for (int64_t row = first; row < a.R; row += stride, turn ^= 1) {
-    const Row now = next;
+    Row now = next;
+    Oct<FMT> dh[DH ? U : 1];
+    if constexpr (DH) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * step;
+        load_oct<TAIL, ONCE>(dh[u], (const char*)a.dh + row * a.lddh * ES, k, K);
+      }
+    }
     if (row + stride < a.R) load(next, row + stride);
     float ss = 0.0f, sg = 0.0f;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      settle_oct<TAIL>(now.y[u], k0 + u * step, K);
+      settle_oct<TAIL>(now.h[u], k0 + u * step, K);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float h = now.h[u].get(i);
         ss = __builtin_fmaf(h, h, ss);
         sg = __builtin_fmaf(now.y[u].get(i) * w[u][i], h, sg);
       }
-    ss = row_sum(ss, a.lanes);
-    sg = row_sum(sg, a.lanes);
+    }
+    ss = row_sum(ss, lanes);
+    sg = row_sum(sg, lanes);
     if (a.waves > 1) {
       // the other half of `part` is still being read by slower waves; this one was
       // before the last barrier
@@ -245,31 +284,33 @@ __global__ __launch_bounds__(kBackThreads) void rms_norm_back_kernel(NormBackArg
     }
     const float r = 1.0f / sqrtf(ss / (float)a.K + a.eps);
     const float c = sg / (float)a.K * r * r;
+    char* const out = (char*)a.dx + row * a.lddx * ES;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t k = 8 * (o0 + u * step);
+      const int k = k0 + u * step;
+      if constexpr (DH) settle_oct<TAIL>(dh[u], k, K);
       float d[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float h = now.h[u].get(i), y = now.y[u].get(i);
         d[i] = r * (y * w[u][i] - h * c);
-        if constexpr (DH) d[i] += now.d[u].get(i);
+        if constexpr (DH) d[i] += dh[u].get(i);
         dw[u][i] = __builtin_fmaf(y * r, h, dw[u][i]);
       }
-      if (k < a.K) store8_part<ONCE>((uint16_t*)a.dx + row * a.lddx + k, pack8<FMT>(d), a.K - k);
+      if (k < K) store8_part<ONCE>((uint16_t*)(out + ES * (uint32_t)k), pack8<FMT>(d), K - k);
     }
   }
   float* p = a.part + first * a.K;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t k = 8 * (o0 + u * step);
-    if (k + 8 <= a.K) {
+    const int k = k0 + u * step;
+    if (k + 8 <= K) {
       gstore<f32x4>(p + k, f32x4{dw[u][0], dw[u][1], dw[u][2], dw[u][3]});
       gstore<f32x4>(p + k + 4, f32x4{dw[u][4], dw[u][5], dw[u][6], dw[u][7]});
     } else {
 #pragma unroll
       for (int i = 0; i < 7; ++i)
-        if (k + i < a.K) gstore<float>(p + k + i, dw[u][i]);
+        if (k + i < K) gstore<float>(p + k + i, dw[u][i]);
     }
   }
 }

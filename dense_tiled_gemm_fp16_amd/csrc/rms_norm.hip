@@ -67,15 +67,19 @@ const void* norm_fn(int32_t fmt, int32_t fmt8, int U, bool res, bool w32, bool o
   return fmt8 == 0 ? norm_fn2<MX_BF16, F8_E4M3>(U, res, w32, o) : norm_fn2<MX_BF16, F8_E5M2>(U, res, w32, o);
 }
 
-template <int FMT>
-const void* back_fn1(int U, bool dh, bool w32, bool o) {
-  return U == 1   ? GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 1)
-         : U == 2 ? GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 2)
-         : U == 4 ? GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 4)
-                  : GEMM_BY_FLAGS2(rms_norm_back_wide_kernel, dh, w32, FMT);
+template <int FMT, bool TAIL>
+const void* back_fn2(int U, bool dh, bool w32, bool o) {
+  return U == 1   ? GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 1, TAIL)
+         : U == 2 ? GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 2, TAIL)
+                  : GEMM_BY_FLAGS(rms_norm_back_kernel, dh, w32, o, FMT, 4, TAIL);
 }
-const void* back_fn(int32_t fmt, int U, bool dh, bool w32, bool o) {
-  return fmt == GEMM_FMT_F16 ? back_fn1<MX_F16>(U, dh, w32, o) : back_fn1<MX_BF16>(U, dh, w32, o);
+template <int FMT>
+const void* back_fn1(int U, bool tail, bool dh, bool w32, bool o) {
+  if (U > 4) return GEMM_BY_FLAGS2(rms_norm_back_wide_kernel, dh, w32, FMT);
+  return tail ? back_fn2<FMT, true>(U, dh, w32, o) : back_fn2<FMT, false>(U, dh, w32, o);
+}
+const void* back_fn(int32_t fmt, int U, bool tail, bool dh, bool w32, bool o) {
+  return fmt == GEMM_FMT_F16 ? back_fn1<MX_F16>(U, tail, dh, w32, o) : back_fn1<MX_BF16>(U, tail, dh, w32, o);
 }
 
 template <int COLS>
@@ -87,11 +91,17 @@ const void* dw_fn1(int32_t fmt_w) {
 const void* dw_fn(int32_t fmt_w, int cols) { return cols == 16 ? dw_fn1<16>(fmt_w) : dw_fn1<64>(fmt_w); }
 
 // Workgroups of the backward kernel: each leaves a row of sums per row that it
-// takes at a time, so no more than are needed to fill the device, and at least two
-// rows for each (16384 x 512 bfloat16: 28.9 us with 512 workgroups of 4 rows).
+// takes at a time, so no more than are needed to fill 256 compute units, and at
+// least two rows for each (16384 x 512 bfloat16: 28.9 us with 512 workgroups of 4
+// rows).  Rows of several waves: as many workgroups a unit as have 12288 elements
+// between them, two at least and as many at most as find room (4 waves a SIMD; of
+// 5 waves and more two workgroups).  9698 x 3480: 57 us with two a unit, 46 with four;
+// 12000 x 5000: 83 with two, 103 with three.
 int64_t back_grid(int64_t R, int64_t K, const Shape& s) {
-  const int64_t parts = std::min<int64_t>(std::max<int64_t>(512, (INT64_C(2) << 20) / K),
-                                          std::max<int64_t>(cdiv(R, 4), std::min<int64_t>(cdiv(R, 2), 512)));
+  const int64_t room = s.waves <= 4 ? 16 / s.waves : 2;
+  const int64_t fill = s.waves == 1 ? std::max<int64_t>(512, (INT64_C(2) << 20) / K)
+                                    : 256 * std::min<int64_t>(room, std::max<int64_t>(2, cdiv(12288, K)));
+  const int64_t parts = std::min<int64_t>(fill, std::max<int64_t>(cdiv(R, 4), std::min<int64_t>(cdiv(R, 2), 512)));
   return std::max<int64_t>(parts / s.per(), 1);
 }
 
@@ -173,7 +183,7 @@ int gemm_rms_norm_backward(const gemm_rms_norm_backward_args* args, void* stream
   int rc = ws.take(workspace, workspace_bytes, need, s);
   if (rc) return rc;
   NormBackArgs a{DY, ldy, H, ldh, W, DH, lddh, DX, lddx, (float*)ws.get(), R, K, eps, sh.waves, sh.lanes};
-  rc = run(back_fn(fmt, sh.U, DH != nullptr, fmt_w == GEMM_FMT_F32, once(R, K, DH ? 8 : 6)), dim3((unsigned)grid), sh.threads(), &a, s);
+  rc = run(back_fn(fmt, sh.U, K % 8 != 0, DH != nullptr, fmt_w == GEMM_FMT_F32, once(R, K, DH ? 8 : 6)), dim3((unsigned)grid), sh.threads(), &a, s);
   if (rc == GEMM_OK) {
     const float* part = a.part;
     int64_t parts = grid * sh.per(), k = K;

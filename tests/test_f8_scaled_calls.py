@@ -4,10 +4,12 @@ workspace, two at a time, and on matrices larger than the caches or than 32-bit
 offsets reach."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
 import dense_tiled_gemm_fp16_amd as g
+import f8_ref as ref
 from dense_tiled_gemm_fp16_amd import _lib
 from gpu_util import DEV, say
 from test_streams import CYCLES, Elsewhere, dropped
@@ -242,6 +244,27 @@ def test_sort_without_a_workspace():
     torch.cuda.synchronize()
     for o in outs:
         same(o, want)
+
+
+@pytest.mark.parametrize("K", [3, 7, 8, 9, 12, 15, 505, 506, 507, 508, 509, 510, 511, 1025, 1027, 1031, 2053, 4103, 8199])
+@pytest.mark.parametrize("dtype,res", [(BF16, True), (F16, False)])
+def test_norm_backward_of_rows_that_end_inside_an_octet(K, dtype, res):
+    """Rows inside a field of NaN, on any side of them."""
+    R = 70
+    say(f"norm backward tails {K} {dtype}")
+    rows = []
+    for seed in range(3):
+        field = torch.full((R + 2, K + 11), float("nan"), dtype=dtype, device=DEV)
+        field[1:-1, 5:5 + K] = randn(R, K, dtype=dtype, seed=seed)
+        rows.append(field[1:-1, 5:5 + K])
+    dy, h, dh = rows
+    dh, w = dh if res else None, randn(K, dtype=F32, seed=4)
+    out = torch.full((R + 2, K + 11), 3.0, dtype=dtype, device=DEV)
+    dx, dw = g.rms_norm_backward(dy, h, w, 1e-6, dh=dh, out=out[1:-1, 5:5 + K])
+    wx, tx, ww, tw = ref.norm_grad(dy, h, w, 1e-6, dh)
+    ref.assert_near(dx, wx, tx + ref.half_step(np.abs(wx) + tx, dtype), "dx")
+    ref.assert_near(dw, ww, tw + ref.half_step(np.abs(ww) + tw, F32), "dw")
+    assert (out[0] == 3).all() and (out[-1] == 3).all() and (out[:, :5] == 3).all() and (out[:, 5 + K:] == 3).all()
 
 
 @pytest.mark.parametrize("R,K", [(300, 16384), (300, 16392), (290, 20001), (260, 65536)])
