@@ -13,7 +13,7 @@
 // exchanges), its row's waves (LDS), in that order always.
 //
 // 32768 x 7168 bfloat16 with a residual 272 us (6.1 TB/s), the gradients of 16384 x
-// 7168 160 us (5.9 TB/s); 16 rows of 7168 3.8 us, most of it launch and latency.
+// 7168 163 us (5.8 TB/s); 16 rows of 7168 3.8 us, most of it launch and latency.
 //
 // dw: a workgroup keeps its rows' sum for its columns in registers and leaves it
 // in the workspace; a second kernel adds the workgroups' in ascending order.
@@ -203,7 +203,9 @@ __device__ __forceinline__ void settle_oct(Oct<FMT>& o, int k, int K) {
 }
 
 // Rows of at most 8 waves of U octets a lane: the weight stays in registers, and
-// the next row is loaded under this one's sums.
+// the next row is loaded under this one's sums.  dh is not: its registers would leave
+// room for three waves a SIMD instead of four (12000 x 5000 96 us instead of 89, 16384
+// x 7168 160 instead of 163).
 constexpr int kBackThreads = 512;
 template <int FMT, int U, bool TAIL, bool DH, bool W32, bool ONCE>
 __global__ __launch_bounds__(kBackThreads) void rms_norm_back_kernel(NormBackArgs a) {
