@@ -185,7 +185,7 @@ __global__ __launch_bounds__(F8sBig::NT) void f8s_big_kernel(F8sArgs a) {
 #undef UNIT
     s3 = s[3];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = sn[j] * sbn;
+    for (int j = 0; j < 4; ++j) s[j] = sn[j] * (sbn * kF8sUp);
   };
 
   if (nf > 0) {
@@ -206,7 +206,7 @@ __global__ __launch_bounds__(F8sBig::NT) void f8s_big_kernel(F8sArgs a) {
     y2 = read_b(0, 3);
     sbn = *reinterpret_cast<const float*>(sb);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = *reinterpret_cast<const float*>(sa + j * 64) * sbn;
+    for (int j = 0; j < 4; ++j) s[j] = *reinterpret_cast<const float*>(sa + j * 64) * (sbn * kF8sUp);
     // Sources of step t + 2; past the end the last step is loaded again, into a
     // stage that no step reads.
     const char* na = pa + (int64_t)(nf > 2 ? 2 : nf - 1) * 128;
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(F8sBig::NT) void f8s_big_kernel(F8sArgs a) {
           is_a ? a.SA[row * a.sa_m + nf * a.sa_k] : a.SB[(row >> a.shift) * a.sb_n + nf * a.sb_k];
     }
     __syncthreads();
-    const float sbv = *reinterpret_cast<const float*>(sb);
+    const float sbv = *reinterpret_cast<const float*>(sb) * kF8sUp;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       fm[j] = mask_block(read_a(0, j), g, rem);
@@ -277,6 +277,8 @@ __global__ __launch_bounds__(F8sBig::NT) void f8s_big_kernel(F8sArgs a) {
     wait_lgkmcnt0();
     wg_barrier();
   }
+  uint32_t odd[4];
+  const bool again = f8s_bring_down(acc, odd);
   // Through LDS, so that each store instruction writes four whole rows of the
   // wave's block (store_staged_block): a lane's 4 columns are half a chunk.
   char* const stage = smem + wave * (CF::WTM * CF::WTN * 2);
@@ -290,6 +292,7 @@ __global__ __launch_bounds__(F8sBig::NT) void f8s_big_kernel(F8sArgs a) {
     }
   const int64_t mw = m0 + wm * CF::WTM, nw = n0 + wn * CF::WTN;
   store_staged_block<CF::WTM, CF::WTN * 2>((char*)a.C + (mw * a.ldc + nw) * 2, a.ldc * 2, a.M - mw, (a.N - nw) * 2, stage, lane);
+  if (again) f8s_store_again<FA, FB, false, CF::FN, CF::FM>(mw, nw, odd, lane);
 }
 
 }  // namespace gemmf16

@@ -91,7 +91,7 @@ __global__ __launch_bounds__(CF::NT) void f8s_strip_kernel(F8sArgs a) {
     auto part = [&](const i32x8& v) { return TAIL ? mask_block(v, g, rem) : v; };
     const char* st = mine + slot * CF::STAGE;
     const char* sc = st + CF::A_BYTES + CF::B_BYTES;
-    const float sb = ROWB ? 1.0f : *reinterpret_cast<const float*>(sc + 256);
+    const float sb = ROWB ? kF8sUp : *reinterpret_cast<const float*>(sc + 256) * kF8sUp;
     F8sFrag<WIDE> fb[CF::NS];
 #pragma unroll
     for (int i = 0; i < CF::NS; ++i) fb[i] = f8s_frag<WIDE, FB>(part(read(st + CF::A_BYTES, i)));
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(CF::NT) void f8s_strip_kernel(F8sArgs a) {
         if constexpr (ROWB) sn = *reinterpret_cast<const f32x4*>(sc + 256 + (16 * i + 4 * g) * 4);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          acc[i][j][e] = __builtin_fmaf(ROWB ? d[i][e] * sn[e] : d[i][e], s, acc[i][j][e]);
+          acc[i][j][e] = __builtin_fmaf(d[i][e], ROWB ? s * sn[e] : s, acc[i][j][e]);
       }
     }
   };
@@ -156,6 +156,22 @@ __global__ __launch_bounds__(CF::NT) void f8s_strip_kernel(F8sArgs a) {
 #pragma unroll
     for (int w = 0; w < CF::NW; ++w) v += sums[(w * (CF::NS * CF::MT) + q) * 64 + lane];
     const int64_t m = m0 + 16 * j + lr, n = n0 + 16 * i + 4 * g;
+    int which = 0;                 // elements that did not stay finite
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] *= kF8sDown;
+      if (m < a.M && n + e < a.N && !__builtin_isfinite(v[e])) which |= 1 << e;
+    }
+    if (__builtin_expect(__any(which != 0), 0)) {
+      const F8sArgs b = f8s_args_again();
+      const uint32_t rows = f8s_nan_rows(b, m0 + 16 * j, lane), cols = f8s_nan_cols(b, n0 + 16 * i, lane);
+      which = rows >> lr & 1 ? 0 : which & (int)~(cols >> (4 * g));      // the others are NaN
+      if (__any(which != 0)) {
+        const f32x4 w = f8s_again<FA, FB, WIDE>(b, m0 + 16 * j, n0 + 16 * i, which, lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = which >> e & 1 ? w[e] : v[e];
+      }
+    }
     if (m < a.M && n < a.N) store_out4(a.C, a.out, m * a.ldc + n, v, a.N - n);
   }
 }

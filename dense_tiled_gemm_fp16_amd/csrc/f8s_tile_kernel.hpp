@@ -23,6 +23,17 @@
 //          row lane % 16 of C, so one multiplication gives the scale of a row
 //          and a block of columns, and 8 or 16 consecutive bytes are stored.
 //
+//   range  the product of two scales may leave float32's range where the block's sum,
+//          which is 0 or between 2^-32 and 2^39, brings the result back into it.  So
+//          the running sums are kept 2^40 times as large: what a product of scales
+//          loses below 2^-126 is then, times such a sum, less than half a step of the
+//          smallest float32.  The few sums that do not stay finite so, which lie above
+//          2^88, meet scales above it or end as infinities or NaN, are formed again in
+//          64 bits (f8s_again).  One multiplication a step and three for two outputs:
+//          1 x 2048 x 7168 5.4 us instead of 5.3, 20864 x 1664 x 224 28.0 instead of
+//          26.8, 32768 x 2048 x 7168 the same; with a NaN in every tile 8 to 16% more,
+//          with all results above 2^88 twenty times as long.
+//
 // What bounds it: a step's data, which two stages give one step's time to arrive,
 // and for float32 results the vector unit's instructions (256 beside 64 matrix
 // instructions of 16 cycles).  Where the LDS holds two workgroups a compute unit
@@ -225,6 +236,139 @@ __device__ __forceinline__ i32x8 mask_block(i32x8 v, int g, int rem) {
   return v;
 }
 
+// The running sums are this much larger than the results (the comment at the top).
+constexpr float kF8sUp = 0x1p40f, kF8sDown = 0x1p-40f;
+
+// Sums to results.  Returns, to the whole wave, whether some may not have stayed finite;
+// then bit i FM + j of odd[e] tells that element e of sums[i][j] did not.  (The products
+// of two results add up to a finite number only if all are; large ones may overflow
+// without, at the cost of looking.)
+template <int FN, int FM>
+__device__ __forceinline__ bool f8s_bring_down(f32x4 (&sums)[FN][FM], uint32_t (&odd)[4]) {
+  static_assert(FN * FM <= 32, "bits of a flag");
+  float z[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sums[i][j][e] *= kF8sDown;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) z[h] = __builtin_fmaf(sums[i][j][2 * h], sums[i][j][2 * h + 1], z[h]);
+    }
+  odd[0] = odd[1] = odd[2] = odd[3] = 0;
+  if (__builtin_expect(!__any(!__builtin_isfinite(z[0]) || !__builtin_isfinite(z[1])), 1)) return false;
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (!__builtin_isfinite(sums[i][j][e])) odd[e] |= 1u << (i * FM + j);
+  return true;
+}
+
+// Of 16 rows (or columns), which have a NaN scale, a bit each: lane l looks at every
+// fourth scale, from l / 16 on, of row l % 16, which begin at s.
+__device__ __forceinline__ uint32_t f8s_nan_scales(const float* s, int64_t step, int64_t blocks, int lane) {
+  bool bad = false;
+#pragma unroll 4
+  for (int64_t b = lane >> 4; b < blocks; b += 4) {
+    const float v = s[b * step];
+    bad |= v != v;
+  }
+  const uint64_t m = __ballot(bad);
+  return (uint32_t)(m | m >> 16 | m >> 32 | m >> 48) & 0xFFFFu;
+}
+__device__ __forceinline__ int64_t f8s_below(int64_t i, int64_t n) { return i < n ? i : n - 1; }
+__device__ __forceinline__ uint32_t f8s_nan_rows(const F8sArgs& a, int64_t m0, int lane) {
+  return f8s_nan_scales(a.SA + f8s_below(m0 + (lane & 15), a.M) * a.sa_m, a.sa_k, (a.K + 127) / 128, lane);
+}
+__device__ __forceinline__ uint32_t f8s_nan_cols(const F8sArgs& a, int64_t n0, int lane) {
+  return f8s_nan_scales(a.SB + (f8s_below(n0 + (lane & 15), a.N) >> a.shift) * a.sb_n, a.sb_k, (a.K + 127) / 128, lane);
+}
+
+// A block of 16 rows from m0 (inside A) x 16 columns from n0 (inside C) again, its sums
+// in 64 bits; only the elements with a bit in `which` count (column n0 + 4 (lane / 16) +
+// e of row m0 + lane % 16).  Straight from memory, a step at a time: 1 us a step.
+template <int FA, int FB, bool WIDE>
+__device__ __forceinline__ f32x4 f8s_again(const F8sArgs& a, int64_t m0, int64_t n0, int which, int lane) {
+  const int lr = lane & 15, g = lane >> 4;
+  const int64_t m = f8s_below(m0 + lr, a.M), n = f8s_below(n0 + lr, a.N);
+  const char* pa = a.A + m * a.lda + 16 * g;
+  const char* pb = a.B + n * a.ldb + 16 * g;
+  const float* sa = a.SA + m * a.sa_m;
+  const float* sb[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sb[e] = a.SB + (f8s_below(n0 + 4 * g + e, a.N) >> a.shift) * a.sb_n;
+  double v[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 1
+  for (int64_t k = 0; k < a.K; k += 128) {
+    const int rem = a.K - k < 128 ? (int)(a.K - k) : 128;
+    auto part = [&](const char* p) {
+      return mask_block(join8(16 * g < rem ? load16(p) : zero4(), 64 + 16 * g < rem ? load16(p + 64) : zero4()), g, rem);
+    };
+    const f32x4 d = f8s_block<FA, FB>(f8s_frag<WIDE, FB>(part(pb)), f8s_frag<WIDE, FA>(part(pa)));
+    const double s = *sa;
+    int left = 0;                                           // NaN stays NaN
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = __builtin_fma((double)d[e] * s, (double)*sb[e], v[e]);
+      left |= v[e] == v[e] ? 1 << e : 0;
+      sb[e] += a.sb_k;
+    }
+    if (!__any((left & which) != 0)) break;
+    pa += 128;
+    pb += 128;
+    sa += a.sa_k;
+  }
+  return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+}
+
+// The kernel's arguments, loaded again where few calls come: what would be kept of
+// them costs the others scalar registers.
+__device__ __forceinline__ F8sArgs f8s_args_again() {
+  const char __attribute__((address_space(4)))* p =
+      (const char __attribute__((address_space(4)))*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  F8sArgs a;
+  __builtin_memcpy(&a, (const void*)p, sizeof(a));
+  return a;
+}
+
+// The elements of a wave's FN x FM blocks from row m0 and column n0 that did not stay
+// finite, over what was stored in their place; but for those of rows and columns with a
+// NaN scale, which are NaN.
+template <int FA, int FB, bool WIDE, int FN, int FM>
+__device__ __forceinline__ void f8s_store_again(int64_t m0, int64_t n0, const uint32_t (&odd)[4], int lane) {
+  static_assert(FM <= 4, "rows in 64 bits");
+  const F8sArgs a = f8s_args_again();
+  wait_vmcnt<0>();
+  uint64_t rows = 0;
+#pragma unroll 1
+  for (int j = 0; j < FM; ++j) rows |= (uint64_t)f8s_nan_rows(a, m0 + 16 * j, lane) << (16 * j);
+#pragma unroll 1
+  for (int i = 0; i < FN; ++i) {
+    const int64_t n = n0 + 16 * i + 4 * (lane >> 4);
+    const uint32_t cols = f8s_nan_cols(a, n0 + 16 * i, lane) >> (4 * (lane >> 4));
+#pragma unroll 1
+    for (int j = 0; j < FM; ++j) {
+      const int64_t m = m0 + 16 * j + (lane & 15);
+      int which = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) which |= n + e < a.N ? (int)(odd[e] >> (i * FM + j) & 1u) << e : 0;
+      which = m < a.M && !(rows >> (16 * j + (lane & 15)) & 1) ? which & (int)~cols : 0;
+      if (!__any(which != 0)) continue;
+      const f32x4 v = f8s_again<FA, FB, WIDE>(a, m0 + 16 * j, n0 + 16 * i, which, lane);
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e) {
+        const float f = e == 0 ? v[0] : e == 1 ? v[1] : e == 2 ? v[2] : v[3];
+        if (which >> e & 1) store_out4(a.C, a.out, m * a.ldc + n + e, f32x4{f, f, f, f}, 1);
+      }
+    }
+  }
+}
+
 // Offset of a DMA lane's chunk c in a block of which rem bytes are left: chunks
 // wholly behind K read the block's first one (mask_block clears them; a chunk
 // that K ends in is read whole, 16 aligned bytes of which one at least is K's).
@@ -342,7 +486,7 @@ __global__ __launch_bounds__(CF::NT, CF::WAVES) void f8s_tile_kernel(F8sArgs a) 
     i32x8 next = part(read(rb, 0));
     F8sFrag<WIDE> fm[CF::FM], fb;
     float s[CF::FM];
-    const float sb = ROWB ? 1.0f : *reinterpret_cast<const float*>(rsb);
+    const float sb = ROWB ? kF8sUp : *reinterpret_cast<const float*>(rsb) * kF8sUp;
 #pragma unroll
     for (int j = 0; j < CF::FM; ++j) {
       fm[j] = f8s_frag<WIDE, FA>(part(read(ra, j)));
@@ -357,7 +501,7 @@ __global__ __launch_bounds__(CF::NT, CF::WAVES) void f8s_tile_kernel(F8sArgs a) 
         for (int j = 0; j < CF::FM; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            acc[i][j][e] = __builtin_fmaf(ROWB ? d[i & 1][j][e] * sn[i & 1][e] : d[i & 1][j][e], s[j], acc[i][j][e]);
+            acc[i][j][e] = __builtin_fmaf(d[i & 1][j][e], ROWB ? s[j] * sn[i & 1][e] : s[j], acc[i][j][e]);
       };
       fb = f8s_frag<WIDE, FB>(next);
 #pragma unroll
@@ -395,7 +539,7 @@ __global__ __launch_bounds__(CF::NT, CF::WAVES) void f8s_tile_kernel(F8sArgs a) 
           if (j == 0 && i + 1 < CF::FN) sn[(i + 1) & 1] = *reinterpret_cast<const f32x4*>(rsb + (i + 1) * 64 + 16 * g);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          acc[i][j][e] = __builtin_fmaf(ROWB ? d[v % (LAG + 1)][e] * sn[i & 1][e] : d[v % (LAG + 1)][e], s[j], acc[i][j][e]);
+          acc[i][j][e] = __builtin_fmaf(d[v % (LAG + 1)][e], ROWB ? s[j] * sn[i & 1][e] : s[j], acc[i][j][e]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -422,6 +566,8 @@ __global__ __launch_bounds__(CF::NT, CF::WAVES) void f8s_tile_kernel(F8sArgs a) 
   wait_vmcnt<0>();       // no LDS transfer may outlive the workgroup, and every
   wait_lgkmcnt0();       // wave has read its stage: the LDS is free
   wg_barrier();
+  uint32_t odd[4];
+  const bool again = f8s_bring_down(acc, odd);
   char* const stage = smem + wave * (CF::TM * CF::TN * 4);
   const int64_t mw = m0 + wm * CF::TM, nw = n0 + wn * CF::TN, es = a.out == F8S_F32 ? 4 : 2;
   char* const cw = (char*)a.C + (mw * a.ldc + nw) * es;
@@ -452,6 +598,7 @@ __global__ __launch_bounds__(CF::NT, CF::WAVES) void f8s_tile_kernel(F8sArgs a) 
       put(std::integral_constant<int, DT_BF16>{});
     store_staged_block<CF::TM, CF::TN * 2>(cw, a.ldc * 2, a.M - mw, (a.N - nw) * 2, stage, lane);
   }
+  if (again) f8s_store_again<FA, FB, WIDE, CF::FN, CF::FM>(mw, nw, odd, lane);
 }
 
 }  // namespace gemmf16

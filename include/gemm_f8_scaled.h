@@ -63,6 +63,10 @@ int gemm_f8s_quantize(const gemm_f8s_quantize_args* args, void* stream);
  * of a sum of random products, far below C's own rounding.  For float32 C the
  * products are exact and all sums float32, at about half the rate.
  *
+ * Scales may be any float32: a result is right, and finite, wherever float32 holds it,
+ * also if the product of two scales is not a float32.  Results above 2^88, or under
+ * scales above it, are formed twice, the second time slowly.
+ *
  * variant: GEMM_F8S_AUTO, or a kernel by its tile (all compute the same; one that
  * does not take the call is GEMM_ERR_OPTS).  GEMM_ERR_SHAPE: more tiles than a
  * launch of any of them takes.
