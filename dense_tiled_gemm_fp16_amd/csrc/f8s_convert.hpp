@@ -64,20 +64,19 @@ __device__ __forceinline__ F8Scale f8_scale(uint32_t m) {
   return s;
 }
 
-// EXACT: rounded once for a 16-bit x; else twice.
-template <bool EXACT>
+// Rounded once for a 16-bit x; else twice, with x up itself.
 __device__ __forceinline__ float f8_quotient(float x, const F8Scale& s) {
   const float X = x * s.up;
   const float t = X * s.rf;
-  return EXACT ? __builtin_fmaf(__builtin_fmaf(-t, s.f, X), s.rf, t) : t;
+  return __builtin_fmaf(__builtin_fmaf(-t, s.f, X), s.rf, t);
 }
 
 // 8 floats -> 8 codes, the first in the lowest byte; zeros for a bad block.
-template <int F8, bool EXACT = true>
+template <int F8>
 __device__ __forceinline__ u32x2 f8_codes(const float (&x)[8], const F8Scale& s) {
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = f8_quotient<EXACT>(x[i], s);
+  for (int i = 0; i < 8; ++i) q[i] = f8_quotient(x[i], s);
   int d[2] = {0, 0};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {

@@ -156,7 +156,7 @@ __global__ __launch_bounds__(1024) void rms_norm_f8_kernel(NormArgs a) {
     }
     const F8Scale s = f8_scale<F8>(max16(m));
     if (k < a.K) {
-      store_codes<ONCE>(a.data + row * a.ldd + k, f8_codes<F8, false>(v[u], s), a.K - k);
+      store_codes<ONCE>(a.data + row * a.ldd + k, f8_codes<F8>(v[u], s), a.K - k);
       if ((lane & 15) == 0) gstore<float>(a.scales + row * a.ss_r + (k >> 7) * a.ss_k, s.scale);
     }
   }

@@ -20,10 +20,9 @@ extern "C" {
  * h := x + residual, each row of K elements of format fmt (GEMM_FMT_F16 or
  * GEMM_FMT_BF16), rounded to it; or h = x with residual == NULL (then the H
  * argument is not used).
- * y := h * w / sqrt(mean(h^2) + eps), quantised by row blocks of 128 into data
- * and scales as gemm_f8s_quantize does, but for the quotients, which lie within two
- * float32 steps before they are rounded to 8 bits.  y is not stored; all is float32,
- * so a row of h whose squares sum past 3.4e38 becomes zeros.
+ * y := h * w / sqrt(mean(h^2) + eps) in float32, quantised by row blocks of 128 into
+ * data and scales as gemm_f8s_quantize does a float32 X.  y is not stored; all is
+ * float32, so a row of h whose squares sum past 3.4e38 becomes zeros.
  * w: K elements of fmt_w, GEMM_FMT_F32 or fmt.  H may be X or the residual
  * itself, at the same row stride; nothing else overlaps.
  */
