@@ -102,25 +102,34 @@ __global__ __launch_bounds__(1024) void rms_norm_f8_kernel(NormArgs a) {
   __shared__ float part[16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Row of the workgroup, wave of the row.  A workgroup of several rows has each in
-  // a wave of its own, or a part of one.
-  const int share = 64 >> a.lanes, sub = wave / a.waves * share + (lane >> a.lanes), rw = wave % a.waves;
+  // a wave of its own, or (rows of one octet a lane) a part of one.  Other rows'
+  // numbers, and with them their addresses but for 32-bit offsets, are the wave's.
+  const int lanes = U > 1 ? 6 : a.lanes;
+  const int share = 64 >> lanes, sub = wave / a.waves * share + (U > 1 ? 0 : lane >> lanes), rw = wave % a.waves;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / 64 / a.waves * share) + sub;
   if (row >= a.R) return;
-  const int step = 64 * a.waves;
-  const int64_t o0 = 64 * rw + (lane & ((1 << a.lanes) - 1));
-  constexpr int ES = 2;
+  const int K = (int)a.K, step = 8 * 64 * a.waves, k0 = 8 * (64 * rw + (lane & ((1 << lanes) - 1)));
+  constexpr uint32_t ES = 2, EW = W32 ? 4 : 2;
+  // Element k0 + u step of a row, `bytes` each.
+  auto at = [&](const void* base, uint32_t bytes, int u) {
+    return (const char*)base + (size_t)bytes * (uint32_t)(u * step) + bytes * (uint32_t)k0;
+  };
+  const char* const px = (const char*)a.x + row * a.ldx * ES;
+  const char* const pr = (const char*)a.residual + row * a.ldr * ES;
+  char* const ph = (char*)a.h + row * a.ldh * ES;
+  char* const pd = (char*)a.data + row * a.ldd;
   Oct<FMT> vx[U], vr[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t k = 8 * (o0 + u * step);
-    vx[u].template load<ONCE>((const char*)a.x + row * a.ldx * ES, k, a.K - k);
-    if constexpr (RES) vr[u].template load<ONCE>((const char*)a.residual + row * a.ldr * ES, k, a.K - k);
+    const int n = K - (k0 + u * step);
+    vx[u].template load<ONCE>(at(px, ES, u), 0, n);
+    if constexpr (RES) vr[u].template load<ONCE>(at(pr, ES, u), 0, n);
   }
   float v[U][8];
   float sum = 0.0f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t k = 8 * (o0 + u * step);
+    const int n = K - (k0 + u * step);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[u][i] = vx[u].get(i);
     if constexpr (RES) {
@@ -128,25 +137,25 @@ __global__ __launch_bounds__(1024) void rms_norm_f8_kernel(NormArgs a) {
       for (int i = 0; i < 8; ++i) v[u][i] += vr[u].get(i);
       Oct<FMT> o;
       o.v[0] = pack8<FMT>(v[u]);
-      if (k < a.K) store8_part<ONCE>((uint16_t*)a.h + row * a.ldh + k, o.v[0], a.K - k);
+      if (n > 0) store8_part<ONCE>((uint16_t*)at(ph, ES, u), o.v[0], n);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[u][i] = o.get(i);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(v[u][i], v[u][i], sum);
   }
-  sum = row_sum(sum, a.lanes);
+  sum = row_sum(sum, lanes);
   if (a.waves > 1) {                                            // then the workgroup's only row
     if (lane == 0) part[wave] = sum;
     __syncthreads();
     sum = sum_parts(part, a.waves, lane);
   }
-  const float r = 1.0f / sqrtf(sum / (float)a.K + a.eps);
+  const float r = 1.0f / sqrtf(sum / (float)K + a.eps);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t k = 8 * (o0 + u * step);
+    const int n = K - (k0 + u * step);
     Oct<W32 ? MX_F32 : FMT> w;
-    w.load(a.w, k, a.K - k);
+    w.load(at(a.w, EW, u), 0, n);
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -155,9 +164,9 @@ __global__ __launch_bounds__(1024) void rms_norm_f8_kernel(NormArgs a) {
       m = b > m ? b : m;
     }
     const F8Scale s = f8_scale<F8>(max16(m));
-    if (k < a.K) {
-      store_codes<ONCE>(a.data + row * a.ldd + k, f8_codes<F8>(v[u], s), a.K - k);
-      if ((lane & 15) == 0) gstore<float>(a.scales + row * a.ss_r + (k >> 7) * a.ss_k, s.scale);
+    if (n > 0) {
+      store_codes<ONCE>((uint8_t*)at(pd, 1, u), f8_codes<F8>(v[u], s), n);
+      if ((lane & 15) == 0) gstore<float>(a.scales + row * a.ss_r + (int64_t)((k0 + u * step) >> 7) * a.ss_k, s.scale);
     }
   }
 }
@@ -180,9 +189,10 @@ struct NormBackArgs {
 
 // The octet at k of a 16-bit row of K elements, zeros behind it.  One that K ends in
 // (TAIL: K is no multiple of 8) is loaded from 8 before K and moved to its place by
-// settle_oct when it is used: put together from single elements its wave would wait
-// for them at once (the gradients of 9698 x 3483 bfloat16, four workgroups a unit: 64 us
-// so, 54 now; of 9698 x 3480, 46).
+// settle_oct when it is used, by a count that is the wave's (counts of the lanes took 6
+// registers more, and with them a wave a SIMD): put together from single elements its
+// wave would wait for them at once.  The gradients of 9698 x 3483 bfloat16 with dh take
+// 64 us, of 9698 x 3480 52.
 template <bool TAIL, bool ONCE, int FMT>
 __device__ __forceinline__ void load_oct(Oct<FMT>& o, const char* row, int k, int K) {
   if (TAIL && K < 8) {
@@ -194,21 +204,22 @@ __device__ __forceinline__ void load_oct(Oct<FMT>& o, const char* row, int k, in
 }
 template <bool TAIL, int FMT>
 __device__ __forceinline__ void settle_oct(Oct<FMT>& o, int k, int K) {
-  if (!TAIL || K < 8 || k >= K || k + 8 <= K) return;
-  const int s = 16 * (k + 8 - K);                        // bits to drop, 16 .. 112
+  if (!TAIL || K < 8) return;
+  const int s = 16 * (8 - K % 8);                        // bits to drop, 16 .. 112; the wave's
   const u32x4 v = o.v[0];
   const uint64_t lo = v[0] | ((uint64_t)v[1] << 32), hi = v[2] | ((uint64_t)v[3] << 32);
   const uint64_t a = s >= 64 ? hi >> (s - 64) : (lo >> s) | (hi << (64 - s)), b = s >= 64 ? 0 : hi >> s;
-  o.v[0] = u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+  if (k < K && k + 8 > K) o.v[0] = u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
 }
 
 // Rows of at most 8 waves of U octets a lane: the weight stays in registers, and
-// the next row is loaded under this one's sums.  dh is not: its registers would leave
-// room for three waves a SIMD instead of four (12000 x 5000 96 us instead of 89, 16384
-// x 7168 160 instead of 163).
+// the next row is loaded under this one's sums.  Up to two octets that takes 128
+// registers at most, so four waves a SIMD; four octets take up to 256, so two.  dh is not
+// loaded ahead: its registers would leave room for three waves instead of four (12000 x
+// 5000 96 us instead of 89, 16384 x 7168 160 instead of 163).
 constexpr int kBackThreads = 512;
 template <int FMT, int U, bool TAIL, bool DH, bool W32, bool ONCE>
-__global__ __launch_bounds__(kBackThreads) void rms_norm_back_kernel(NormBackArgs a) {
+__global__ __launch_bounds__(kBackThreads, U > 2 ? 2 : 4) void rms_norm_back_kernel(NormBackArgs a) {
   __shared__ float part[2][2][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Only rows of one octet a lane share waves; the others' numbers, and with them
@@ -319,14 +330,21 @@ __global__ __launch_bounds__(kBackThreads) void rms_norm_back_kernel(NormBackArg
 
 // Wider rows, up to 8 octets for each of 1024 lanes: only the weight gradient's
 // sums stay in registers; a row is read again after the sums over it, from the
-// caches.  (2048 x 20000 bfloat16 with dh 133 us; in registers, of which there are
-// 128 a lane, it spilled: 493.)
+// caches.  Addresses are the wave's but for one offset: with one for each octet of
+// each row in registers, of which there are 128 a lane, 36 to 46 of them went to memory
+// (2048 x 20000 bfloat16 with dh 127 us, 113 now; 1000 x 65536 281 and 233).
 constexpr int kWideThreads = 1024, kWideOcts = 8;
 template <int FMT, bool DH, bool W32>
 __global__ __launch_bounds__(kWideThreads) void rms_norm_back_wide_kernel(NormBackArgs a) {
   __shared__ float part[2][2][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, K = (int)a.K;
   using W = Oct<W32 ? MX_F32 : FMT>;
+  constexpr uint32_t ES = 2, EW = W32 ? 4 : 2;
+  // The thread's octet u of a row of elements of `bytes`: the row's part of the address
+  // and u's are the wave's, so that none of them stays in a register for each octet.
+  auto at = [&](const void* base, uint32_t bytes, int u) {
+    return uniform_ptr((const char*)base + (size_t)bytes * (8u * kWideThreads) * (uint32_t)u) + bytes * 8u * (uint32_t)tid;
+  };
   float dw[kWideOcts][8];
 #pragma unroll
   for (int u = 0; u < kWideOcts; ++u)
@@ -334,16 +352,18 @@ __global__ __launch_bounds__(kWideThreads) void rms_norm_back_wide_kernel(NormBa
     for (int i = 0; i < 8; ++i) dw[u][i] = 0.0f;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x, turn ^= 1) {
-    const char* const py = (const char*)a.dy + row * a.ldy * 2;
-    const char* const ph = (const char*)a.h + row * a.ldh * 2;
+    const char* const py = (const char*)a.dy + row * a.ldy * ES;
+    const char* const ph = (const char*)a.h + row * a.ldh * ES;
+    const char* const pd = (const char*)a.dh + row * a.lddh * ES;
+    const char* const px = (const char*)a.dx + row * a.lddx * ES;
     float ss = 0.0f, sg = 0.0f;
-#pragma unroll 2
-    for (int k = 8 * tid; k < K; k += 8 * kWideThreads) {
+    for (int u = 0; 8 * kWideThreads * u < K; ++u) {
+      const int n = K - 8 * (tid + u * kWideThreads);
       Oct<FMT> y, h;
       W w;
-      y.load(py, k, K - k);
-      h.load(ph, k, K - k);
-      w.load(a.w, k, K - k);
+      y.load(at(py, ES, u), 0, n);
+      h.load(at(ph, ES, u), 0, n);
+      w.load(at(a.w, EW, u), 0, n);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         ss = __builtin_fmaf(h.get(i), h.get(i), ss);
@@ -364,14 +384,14 @@ __global__ __launch_bounds__(kWideThreads) void rms_norm_back_wide_kernel(NormBa
 #pragma unroll
     for (int u = 0; u < kWideOcts; ++u) {
       asm volatile("" ::: "memory");   // no octet's loads before the one ahead is done with
-      const int k = 8 * (tid + u * kWideThreads);
-      if (k < K) {
+      const int n = K - 8 * (tid + u * kWideThreads);
+      if (n > 0) {
         Oct<FMT> y, h, d;
         W w;
-        y.load(py, k, K - k);
-        h.load(ph, k, K - k);
-        w.load(a.w, k, K - k);
-        if constexpr (DH) d.load((const char*)a.dh + row * a.lddh * 2, k, K - k);
+        y.load(at(py, ES, u), 0, n);
+        h.load(at(ph, ES, u), 0, n);
+        w.load(at(a.w, EW, u), 0, n);
+        if constexpr (DH) d.load(at(pd, ES, u), 0, n);
         float f[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -379,17 +399,17 @@ __global__ __launch_bounds__(kWideThreads) void rms_norm_back_wide_kernel(NormBa
           if constexpr (DH) f[i] += d.get(i);
           dw[u][i] = __builtin_fmaf(y.get(i) * r, h.get(i), dw[u][i]);
         }
-        store8_part((uint16_t*)a.dx + row * a.lddx + k, pack8<FMT>(f), K - k);
+        store8_part((uint16_t*)at(px, ES, u), pack8<FMT>(f), n);
       }
     }
   }
-  float* const p = a.part + (int64_t)blockIdx.x * a.K;
+  const char* const p = (const char*)(a.part + (int64_t)blockIdx.x * a.K);
 #pragma unroll
   for (int u = 0; u < kWideOcts; ++u) {
-    const int k = 8 * (tid + u * kWideThreads);
+    const int n = K - 8 * (tid + u * kWideThreads);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (k + i < K) gstore<float>(p + k + i, dw[u][i]);
+      if (i < n) gstore<float>((float*)at(p, 4, u) + i, dw[u][i]);
   }
 }
 
