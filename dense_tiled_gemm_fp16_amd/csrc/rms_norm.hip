@@ -94,11 +94,15 @@ const void* dw_fn(int32_t fmt_w, int cols) { return cols == 16 ? dw_fn1<16>(fmt_
 // takes at a time, so no more than are needed to fill 256 compute units, and at
 // least two rows for each (16384 x 512 bfloat16: 28.9 us with 512 workgroups of 4
 // rows).  Rows of several waves: as many workgroups a unit as have 12288 elements
-// between them, two at least and as many at most as find room (4 waves a SIMD; of
-// 5 waves and more two workgroups).  9698 x 3480: 57 us with two a unit, 46 with four;
-// 12000 x 5000: 83 with two, 103 with three.
+// between them, two at least, and as many at most as find room by their registers
+// (norm_kernel.hpp): of up to two octets four waves a SIMD, though of 5 waves and more
+// two workgroups; of four octets two waves a SIMD, and of the wide kernel's 1024 lanes,
+// one workgroup.  9698 x 3480: 57 us with two a unit, 46 with four; 12000 x 5000: 83
+// with two, 103 with three; twice as many as find room, a second round of them half
+// empty: 4000 x 12288 with dh 86 instead of 83, 2048 x 20000 113 instead of 97, 1000 x
+// 65536 233 instead of 183, and twice the rows of sums.
 int64_t back_grid(int64_t R, int64_t K, const Shape& s) {
-  const int64_t room = s.waves <= 4 ? 16 / s.waves : 2;
+  const int64_t room = s.U > 2 ? 1 : s.waves <= 4 ? 16 / s.waves : 2;
   const int64_t fill = s.waves == 1 ? std::max<int64_t>(512, (INT64_C(2) << 20) / K)
                                     : 256 * std::min<int64_t>(room, std::max<int64_t>(2, cdiv(12288, K)));
   const int64_t parts = std::min<int64_t>(fill, std::max<int64_t>(cdiv(R, 4), std::min<int64_t>(cdiv(R, 2), 512)));
