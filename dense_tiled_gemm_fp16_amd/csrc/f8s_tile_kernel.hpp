@@ -98,20 +98,6 @@ struct F8sCfg {
   static_assert(LDS <= 160 * 1024 && BM * BN * 4 <= LDS, "LDS budget, staging space");
 };
 
-// One 256-byte DMA: lane l's dword at base + off lands at LDS lds + 4 l.
-__device__ __forceinline__ void dma4_any(const void* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
-               :
-               : "s"(lds), "v"(p)
-               : "memory", "m0");
-}
-__device__ __forceinline__ void dma16_any(const void* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-               :
-               : "s"(lds), "v"(p)
-               : "memory", "m0");
-}
-
 // An operand's 32 bytes of a lane: as they are, or widened to binary16.
 template <bool WIDE>
 struct F8sFrag {
