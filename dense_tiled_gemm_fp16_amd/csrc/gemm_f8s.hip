@@ -151,8 +151,8 @@ int gemm_f8s_quantize(const gemm_f8s_quantize_args* args, void* stream) {
   }
   if (grid > kMaxWide) return GEMM_ERR_SHAPE;
   const bool along_k = ldx_k == 1 || K == 1;
-  // Past the caches: 32768 x 7168 bfloat16 110 us instead of 120, square blocks 122
-  // instead of 130, blocks along the columns 139 instead of 154.
+  // Past the caches: 32768 x 7168 bfloat16 111 us instead of 125, square blocks 122
+  // instead of 130, blocks along the columns 138 instead of 154.
   const bool once = (double)R * (double)K * (double)(elem_size(fmt) + 1) > kOnceBytes;
   const void* fn = fmt8 == 0 ? quant_fn<F8_E4M3>(fmt, tiles, block_rows == 128, along_k, a.few.rows > 0, once)
                              : quant_fn<F8_E5M2>(fmt, tiles, block_rows == 128, along_k, a.few.rows > 0, once);

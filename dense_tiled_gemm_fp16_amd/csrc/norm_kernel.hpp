@@ -12,8 +12,9 @@
 // hold a block.  Sums are float32, over a lane's elements, its wave (lane
 // exchanges), its row's waves (LDS), in that order always.
 //
-// 32768 x 7168 bfloat16 with a residual 272 us (6.1 TB/s), the gradients of 16384 x
-// 7168 163 us (5.8 TB/s); 16 rows of 7168 3.8 us, most of it launch and latency.
+// 32768 x 7168 bfloat16 with a residual 276 us (6.0 TB/s), the gradients of 16384 x
+// 7168 with dh 165 us (5.7 TB/s); 16 rows of 7168 3.9 us, most of it launch and latency;
+// 1024 x 40000 with a residual 64 us, its gradients with dh 111.
 //
 // dw: a workgroup keeps its rows' sum for its columns in registers and leaves it
 // in the workspace; a second kernel adds the workgroups' in ascending order.

@@ -107,7 +107,10 @@ def gemm_f8_scaled(a, a_scales, b, b_scales, out=None, dtype=None, variant="auto
 
     Sums are float32; for a 16-bit C the FP8 matrix instructions cut products that
     are added together at 2^-13 of the largest of eight (1 to 3 in 10^5 of a sum of
-    random products), for a float32 C nothing is cut, at about half the rate.
+    random products), for a float32 C nothing is cut, at about half the rate (and
+    rounded by the caller, that is a 16-bit result without cuts).  Scales may be any
+    float32, also where the product of two is not one; results above 2^88 are formed
+    twice, the second time slowly.
 
     variant: a kernel by its tile (VARIANTS), for measurements; all compute the
     same."""

@@ -146,7 +146,7 @@ def _out(out, rows, H, like, stream):
 def moe_gather(x, order, out=None, stream=None):
     """[T * top_k, H] of x [T, H]'s rows sorted by expert: row order.slots[t, j]
     is x[t]; rows from order.offsets[E] on are zeros.  Any dtype of 1, 2 or 4
-    bytes, so 8-bit rows and their scales too."""
+    bytes, so 8-bit rows too (which gemm_grouped takes without scales), or scales."""
     device, size = x.device, x.element_size()
     offsets, slots, T, k, E = _check_order(order, device)
     H, ld = _check_matrix(x, T, "x")

@@ -72,8 +72,8 @@ def rms_norm_f8(x, weight, eps=1e-6, residual=None, dtype=torch.float8_e4m3fn, o
     (float8_e4m3fn or float8_e5m2) by row blocks, as quantize_f8 does it.
 
     x, residual [R, K] float16 or bfloat16, unit stride along K, K at most 65536;
-    weight [K] of their dtype or float32.  Sums are float32: a row whose squares sum
-    past 3.4e38 becomes zeros.
+    weight [K] of their dtype or float32.  All is float32: a row whose squares sum
+    past 3.4e38 becomes zeros, one whose squares are all 0 has NaN scales if eps is 0.
     out: a pair (data, scales); h: where the sum goes, which may be x or residual
     themselves."""
     shape, R, K, ldx, fmt = _check_rows(x, weight, eps)
@@ -117,7 +117,8 @@ def rms_norm_backward(dy, h, weight, eps=1e-6, dh=None, out=None, workspace=None
     given y's (dy [R, K]) and, where h goes on as the residual stream, h's own
     (dh).  dx, which is x's and the residual's gradient alike, has h's dtype,
     dweight weight's; the rounding of y to 8 bits is passed straight through.
-    Sums are float32, in a fixed order.
+    Sums are float32, in a fixed order; where a row's squares sum past 3.4e38, dx is dh
+    or NaN.
 
     dy, h, dh [R, K] float16 or bfloat16, unit stride along K, K at most 65536.
     out: where dx goes, which may be dy or dh themselves.

@@ -61,7 +61,8 @@ int gemm_f8s_quantize(const gemm_f8s_quantize_args* args, void* stream);
  * Sums: for 16-bit C the FP8 matrix instructions add each 8 consecutive products
  * aligned to their largest and cut 2^-13 below it, then in float32: 1 to 3 in 10^5
  * of a sum of random products, far below C's own rounding.  For float32 C the
- * products are exact and all sums float32, at about half the rate.
+ * products are exact and all sums float32, at about half the rate; a 16-bit result of
+ * such sums is a float32 one, rounded.
  *
  * Scales may be any float32: a result is right, and finite, wherever float32 holds it,
  * also if the product of two scales is not a float32.  Results above 2^88, or under

@@ -16,6 +16,9 @@
  * All three int64, on the device.  The calls below that take them read no slot
  * outside 0 .. P-1 (such a pair counts as one without).
  *
+ * T below 2^23, P below 2^31, H at most 2^24, and T times the parts of a row of X or Y
+ * (2048 bytes in gather, 1024 elements in combine) below 2^25; else GEMM_ERR_SHAPE.
+ *
  * Results are deterministic; sums over rows are float32, in a fixed order.
  */
 #ifndef GEMM_MOE_ROWS_H
@@ -29,7 +32,7 @@ extern "C" {
 
 /*
  * The three tables of experts[t*ld + j], int32 (id_bytes 4) or int64 (8).  The
- * same expert may be chosen twice.  E at most 1024, P below 2^31.
+ * same expert may be chosen twice.  E at most 1024.
  * Needs gemm_moe_sort_workspace_bytes(T, top_k, E) bytes of workspace (may be 0),
  * 256-byte aligned; with workspace == NULL they are allocated in stream order.
  */

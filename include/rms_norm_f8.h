@@ -22,7 +22,8 @@ extern "C" {
  * argument is not used).
  * y := h * w / sqrt(mean(h^2) + eps) in float32, quantised by row blocks of 128 into
  * data and scales as gemm_f8s_quantize does a float32 X.  y is not stored; all is
- * float32, so a row of h whose squares sum past 3.4e38 becomes zeros.
+ * float32, so a row of h whose squares sum past 3.4e38 becomes zeros, and with eps 0
+ * one whose squares are all 0 has NaN scales.
  * w: K elements of fmt_w, GEMM_FMT_F32 or fmt.  H may be X or the residual
  * itself, at the same row stride; nothing else overlaps.
  */
@@ -50,7 +51,8 @@ int gemm_rms_norm_f8(const gemm_rms_norm_f8_args* args, void* stream);
  * h itself (DH, or NULL): with r = 1 / sqrt(mean(h^2) + eps) and g = DY * w,
  *     DX[row] := r (g - h r^2 mean(g h)) + DH[row]       (of x and the residual)
  *     DW[k]   := sum over rows of DY[row,k] h[row,k] r   (of fmt_w)
- * DX may be DY or DH itself, at the same row stride.
+ * All is float32: a row of h whose squares sum past 3.4e38 has r = 0, and a DX of DH or
+ * NaN.  DX may be DY or DH itself, at the same row stride.
  * Needs gemm_rms_norm_backward_workspace_bytes(R, K) bytes of workspace, 256-byte
  * aligned; with workspace == NULL they are allocated in stream order.
  */
