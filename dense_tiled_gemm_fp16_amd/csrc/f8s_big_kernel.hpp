@@ -22,8 +22,8 @@
 // (40).  The stages' halves lie so that all LDS addresses of both are one base
 // and an immediate; the loop takes two steps a turn.
 //
-// 32768 x 2048 x 7168 in 415 us (2320 TFLOP/s), 348 on zeros: the clock falls to
-// 1.8 GHz at the power of multiplying random bytes, with the matrix core busy 57%
+// 32768 x 2048 x 7168 in 424 us (2270 TFLOP/s), 348 on zeros: the clock falls to
+// 1.8 GHz at the power of multiplying random bytes, with the matrix core busy 55%
 // of the cycles (the unscaled FP8 tile, without the multiply-adds: 373).  Touching
 // the lines of later steps ahead of their transfer made it slower (432).
 #pragma once

@@ -9,8 +9,8 @@
 // for by touching 16 rows in every 16 lanes.  The waves' sums are added through
 // LDS at the end, in ascending order.
 //
-// Bound by the latency of one pass of loads: 1 x 2048 x 7168 5.6 us in a graph
-// (14.7 MB), 64 x 7168 x 2048 5.5, 512 x 2048 x 7168 17; a tile per workgroup without
+// Bound by the latency of one pass of loads: 1 x 2048 x 7168 5.4 us in a graph
+// (14.7 MB), 64 x 7168 x 2048 5.5, 512 x 2048 x 7168 18; a tile per workgroup without
 // the split of K takes 31 us and more for 7168 k.
 #pragma once
 

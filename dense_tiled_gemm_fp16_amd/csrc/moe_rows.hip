@@ -31,8 +31,8 @@ bool pairs_ok(int64_t T, int32_t top_k, int64_t* P) {
 // Whether the experts' rows go past the caches.  us without | with it, of one run, in
 // graphs over two sets of bfloat16 rows in turn (T x top_k x H): gather and the combine
 // that reads its rows 4096 x 8 x 7168 (504 MiB) 232 | 189, 16384 x 8 x 7168 840 | 792;
-// gather alone 107 | 96 and 410 | 410, combine 106 | 96 and 408 | 406, its gradients 211
-// | 198 and 789 | 779.  Below the bound the pair gains and loses by turns: 384 MiB 166 |
+// gather alone 107 | 96 and 410 | 410 (over and over on one set 425 | 362), combine 106 |
+// 96 and 408 | 406 (424 | 375), its gradients 211 | 198 and 789 | 779.  Below the bound the pair gains and loses by turns: 384 MiB 166 |
 // 158, 288 120 | 110, 219 97 | 108, 160 63 | 57, 72 27 | 29.
 bool once(int64_t T, int64_t P, int64_t row_bytes) { return (double)(T + P) * (double)row_bytes > kOnceBytes; }
 #define GEMM_ONCE(KERNEL, FMT, o) ((o) ? (const void*)KERNEL<FMT, true> : (const void*)KERNEL<FMT, false>)

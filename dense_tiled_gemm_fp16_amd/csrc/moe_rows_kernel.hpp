@@ -19,9 +19,9 @@
 // The last three move rows of up to some ten KB with a few operations per
 // element: memory bounds them.  Lanes take 16 bytes each, so that loads and
 // stores are whole lines.  16384 tokens, top 8 of 64, 7168 bfloat16: sort 15 us,
-// gather 410 (5.2 TB/s, nearly all of it writes of rows in no order; in their order,
-// reading x in no order, 520), combine 406 (5.2 TB/s; over and over on one set of rows
-// 363 and 374), its gradients 780.  A token's slots are loaded one after another, in
+// gather 360 to 425 (5.0 to 5.9 TB/s by where its rows lie, nearly all of it writes of
+// rows in no order; in their order, reading x in no order, 520), combine 358 to 406,
+// its gradients 730 to 780.  A token's slots are loaded one after another, in
 // gather each behind the store ahead of it, which counts with few tokens: 48 of them in
 // a graph 4.0, 4.5 and 3.9, the gradients 11.
 #pragma once
