@@ -22,7 +22,6 @@
 //   sums   the first operand is B: a lane holds columns 4 (lane / 16) .. + 3 of
 //          row lane % 16 of C, so one multiplication gives the scale of a row
 //          and a block of columns, and 8 or 16 consecutive bytes are stored.
-//
 //   range  the product of two scales may leave float32's range where the block's sum,
 //          which is 0 or between 2^-32 and 2^39, brings the result back into it.  So
 //          the running sums are kept 2^40 times as large: what a product of scales
@@ -50,8 +49,8 @@
 // 8, aligned to the group's largest and cut 2^-13 below it (measured; the older
 // and the newer ones alike), which leaves sums of 1 to 3 in 10^5 of their
 // size: far below a 16-bit result's last place, but not a float32 one's.  Those go
-// through binary16, which holds every 8-bit value, at half the rate: 248 us
-// (970 TFLOP/s; 200 on zeros, so the power it takes counts too).  Matrix
+// through binary16, which holds every 8-bit value, at half the rate: 253 us
+// (950 TFLOP/s; 200 on zeros, so the power it takes counts too).  Matrix
 // instructions of 32 x 32 with their longer sums did not fit the registers.
 #pragma once
 
@@ -225,10 +224,10 @@ __device__ __forceinline__ i32x8 mask_block(i32x8 v, int g, int rem) {
 // The running sums are this much larger than the results (the comment at the top).
 constexpr float kF8sUp = 0x1p40f, kF8sDown = 0x1p-40f;
 
-// Sums to results.  Returns, to the whole wave, whether some may not have stayed finite;
-// then bit i FM + j of odd[e] tells that element e of sums[i][j] did not.  (The products
-// of two results add up to a finite number only if all are; large ones may overflow
-// without, at the cost of looking.)
+// Sums to results.  Returns, to the whole wave, whether any of its elements did not stay
+// finite; bit i FM + j of odd[e] tells that element e of sums[i][j] did not.  (Products of
+// two results add up to a finite number only if all are; where they do not, each result
+// is looked at.)
 template <int FN, int FM>
 __device__ __forceinline__ bool f8s_bring_down(f32x4 (&sums)[FN][FM], uint32_t (&odd)[4]) {
   static_assert(FN * FM <= 32, "bits of a flag");
@@ -251,7 +250,7 @@ __device__ __forceinline__ bool f8s_bring_down(f32x4 (&sums)[FN][FM], uint32_t (
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (!__builtin_isfinite(sums[i][j][e])) odd[e] |= 1u << (i * FM + j);
-  return true;
+  return __any((odd[0] | odd[1] | odd[2] | odd[3]) != 0);
 }
 
 // Of 16 rows (or columns), which have a NaN scale, a bit each: lane l looks at every
