@@ -119,3 +119,27 @@ def test_rows_of_large_results_leave_the_others_as_they_are(variant):
         check(c[rows], a[rows], sa[rows], b, sb, dtype, f"{variant} {dtype}")
         again = g.gemm_f8_scaled(a, sa, b, sb, dtype=dtype, variant=variant)
         assert torch.equal(c[keep], again[keep]) and torch.equal(c[rows], again[rows])
+
+
+@pytest.mark.parametrize("size", [(1, 203, 300), (37, 203, 300), (150, 391, 700)])
+@pytest.mark.parametrize("brows", [1, 128])
+@pytest.mark.parametrize("variant", VARIANTS)
+def test_large_results_into_views(size, brows, variant):
+    """Sums that are formed again, with strides of their own in scales and output, whose
+    surroundings stay as they were; infinities where float32 ends."""
+    M, N, K = size
+    say(f"f8 scaled large views {size} {brows} {variant}")
+    a, b = codes(M, K, E5M2, 8, 1.0), codes(N, K, E4M3, 9, 1.0)
+    n = ref.blocks(K)
+    sa, sb = torch.ones(2 * n, 3 * M, device=DEV).t()[::3, ::2], torch.ones(n, -(-N // brows), device=DEV).t()
+    sa[::2] = 1.25 * 2.0 ** 70
+    sa[::3] = 1.25 * 2.0 ** 110
+    sb[::2] = 1.5 * 2.0 ** 14
+    for dtype in (F32, BF16, F16)[:2 if M == 1 else 3]:     # (a row of infinities in float16)
+        if taken(variant, brows, dtype):
+            buf = torch.full((M + 2, N + 5), 7.0, dtype=dtype, device=DEV)
+            out = buf[1:M + 1, 3:3 + N]
+            c = g.gemm_f8_scaled(a, sa, b, sb, out=out, variant=variant)
+            check(c.contiguous(), a, sa, b, sb, dtype, f"{variant} {dtype}")
+            out.fill_(7.0)
+            assert (buf == 7).all()
