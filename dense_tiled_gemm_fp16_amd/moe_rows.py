@@ -48,7 +48,11 @@ class MoeOrder(NamedTuple):
 
     offsets  int64 [E + 1]: expert e has the slots offsets[e] .. offsets[e+1]-1
     rows     int64 [T * top_k]: number of the pair in a slot; -1 from offsets[E] on
-    slots    int64 [T, top_k]: slot of a pair, -1 without one"""
+    slots    int64 [T, top_k]: slot of a pair, -1 without one
+
+    One that moe_sort did not make has to keep to this: of pairs that share a slot, or
+    whose slot is offsets[E] or above, moe_gather and moe_combine_backward leave any, or
+    parts of each."""
     offsets: torch.Tensor
     rows: torch.Tensor
     slots: torch.Tensor

@@ -14,7 +14,9 @@
  *     rows    [P]         number of the pair in a slot; -1 from offsets[E] on
  *     slots   [T, top_k]  slot of a pair; -1 without one
  * All three int64, on the device.  The calls below that take them read no slot
- * outside 0 .. P-1 (such a pair counts as one without).
+ * outside 0 .. P-1 (such a pair counts as one without).  In tables that no
+ * gemm_moe_sort made, slots that two pairs share, or from offsets[E] on, leave in the
+ * rows written there any of what is written to them, or parts of each.
  *
  * T below 2^23, P below 2^31, H at most 2^24, and T times the parts of a row of X or Y
  * (2048 bytes in gather, 1024 elements in combine) below 2^25; else GEMM_ERR_SHAPE.
